@@ -2,7 +2,7 @@
  * zopt.h — C ABI of libzopt, the rank-local optimizer step of a ZeRO-sharded trainer on one
  * GB300 (sm_103a).
  *
- * Five parts, each a few calls:
+ * Eight parts, each a few calls:
  *   1. the flat bucketed shard layout            (zopt_shard_layout and accessors, host only)
  *   2. the gradient norm / clip / found_inf stats (zopt_grad_norm_clip, zopt_clip_finalize,
  *      zopt_grad_accumulate / zopt_grad_accumulate2 for micro-step sums with the stats fused;
@@ -11,6 +11,9 @@
  *                                                 zopt_adamw_rescale_step)
  *   4. Muon's quintic Newton-Schulz               (zopt_ns_orthogonalize, _many)
  *   5. Muon's update around Newton-Schulz         (zopt_muon_step, _many)
+ *   6. 8-bit activation checkpoints               (zopt_act_pack, zopt_act_unpack)
+ *   7. the gated feed-forward block, both ways    (zopt_ffn_forward, zopt_ffn_backward)
+ *   8. linear cross entropy, both ways            (zopt_linear_ce_forward, zopt_linear_ce_backward)
  *
  * Conventions shared by every call:
  *   - Pointers named d_* and every tensor argument are DEVICE pointers owned by the caller,
@@ -483,6 +486,145 @@ ZOPT_API size_t zopt_muon_workspace_many(const zopt_muon_job* jobs, int32_t n_jo
  * zopt_muon_step. */
 ZOPT_API zopt_status zopt_muon_step_many(const zopt_muon_job* jobs, int32_t n_jobs, const zopt_muon_hparams* hparams,
                                          void* d_ws, size_t ws_bytes, zopt_stream stream);
+
+/* ======================================================================================
+ * 6. 8-bit activation checkpoints
+ *
+ * What a backward pass needs of a forward pass, kept in one byte per entry. A matrix of rows x
+ * cols bf16 entries is cut along each row into `parts` equal parts, each part into blocks of 128
+ * columns (its last block may be shorter). With amax a block's largest finite magnitude,
+ * m 2^k (1 <= m < 2), the block's power is 2^e with e = k - 8, or k - 7 where m > 1.75 (so amax
+ * 2^-e <= 448), at least -126. q holds e4m3(x 2^-e), rounded to nearest even, inf and NaN both as
+ * NaN; scale holds the byte e + 127. What an entry stands for, q 2^e, is exactly a bf16 value
+ * (above 2^-124), so operators read a checkpoint without a further rounding.
+ * ====================================================================================== */
+typedef struct zopt_act8 {
+  uint8_t* q;     /* rows x cols e4m3 bytes, contiguous, 16-byte aligned */
+  uint8_t* scale; /* rows x parts x ceil(cols / parts / 128) exponent bytes, contiguous */
+  int64_t rows, cols;
+  int32_t parts;    /* 1, or 2 for a gate beside its up; divides cols */
+  int32_t reserved; /* 0 */
+} zopt_act8;        /* 40 bytes; the struct itself is read during the call only */
+
+/* Bytes of a checkpoint's scale (0 for an empty or inconsistent shape). */
+ZOPT_API size_t zopt_act8_scale_bytes(int64_t rows, int64_t cols, int32_t parts);
+/* out = the checkpoint of x (rows of ld_x >= cols bf16 elements). Errors: EINVAL for NULL or
+ * misaligned pointers (x and q 16 bytes), rows < 0, cols < 1, parts outside 1 .. 2 or not dividing
+ * cols, ld_x < cols, rows or cols above 2^30. rows = 0 does nothing. */
+ZOPT_API zopt_status zopt_act_pack(const uint16_t* x, int64_t ld_x, const zopt_act8* out, zopt_stream stream);
+/* out = what the checkpoint stands for, in bf16 (rows of ld_out >= cols elements). Same errors. */
+ZOPT_API zopt_status zopt_act_unpack(const zopt_act8* in, uint16_t* out, int64_t ld_out, zopt_stream stream);
+
+/* ======================================================================================
+ * 7. The gated feed-forward block
+ *
+ * For T = tokens rows x of D = dim features, weights gate_up [D][2 F] (F = hidden; the gate's
+ * columns first) and down [F][D], as a Llama-style block stores them (bluscript_zero_ckpt.cpp,
+ * model config):
+ *   g | u = x gate_up;  h = a(g) * u;  y = h down
+ *   a(z) = z s(phi(z)), s the logistic function; phi(z) = z (ZOPT_ACT_SILU) or
+ *   2 sqrt(2/pi) (z + 0.044715 z^3) (ZOPT_ACT_GELU, the tanh form).
+ * and, given dy, with g and u as they were kept:
+ *   dh = dy down';  dg = dh u a'(g);  du = dh a(g)
+ *   dx = dg | du gate_up';  dgate_up = x' (dg | du);  ddown = h' dy.
+ * Tensors are bf16, rows ld_* elements apart; products accumulate in fp32; h, dg and du are
+ * rounded to bf16 once, as operands of the next product, and each result once. The forward keeps
+ * g | u in bf16 (kept, one rounding) or as an 8-bit checkpoint (kept8, parts = 2, rounded from
+ * fp32), or nothing; the backward takes what was kept, and x in bf16 or as a checkpoint (x8). The
+ * weight gradients have the weights' layout: zopt_grad_accumulate takes them as they are.
+ *
+ * Rows that the TMA cannot read in place (ld not a multiple of 8 elements, or F not a multiple of
+ * 8) are copied into the workspace first. A result does not depend on the time or place of any
+ * block's execution: a call repeated on the same inputs gives the same bits.
+ * ====================================================================================== */
+#define ZOPT_ACT_SILU 0
+#define ZOPT_ACT_GELU 1
+
+typedef struct zopt_ffn_job {
+  int64_t tokens, dim, hidden;
+  int32_t act;   /* ZOPT_ACT_SILU or ZOPT_ACT_GELU */
+  int32_t dtype; /* a zopt_dtype: ZOPT_BF16 */
+  const uint16_t* w_gate_up;
+  int64_t ld_gate_up;
+  const uint16_t* w_down;
+  int64_t ld_down;
+  const uint16_t* x; /* NULL in a backward call that is given x8 */
+  int64_t ld_x;
+  const zopt_act8* x8; /* backward: x as a checkpoint (tokens x dim, parts = 1), else NULL */
+  uint16_t* kept;      /* g | u, tokens x 2 hidden (forward: written; backward: read), or NULL */
+  int64_t ld_kept;
+  const zopt_act8* kept8; /* g | u as a checkpoint (tokens x 2 hidden, parts = 2), or NULL */
+  uint16_t* y;            /* forward */
+  int64_t ld_y;
+  const uint16_t* dy; /* backward, from here on */
+  int64_t ld_dy;
+  uint16_t* dx;
+  int64_t ld_dx;
+  uint16_t* dw_gate_up;
+  int64_t ld_dw_gate_up;
+  uint16_t* dw_down;
+  int64_t ld_dw_down;
+} zopt_ffn_job; /* 192 bytes */
+
+/* Workspace bytes for a forward (backward = 0) or backward call, or either (backward = 1 covers
+ * both), of a job: from its tokens, dim, hidden, the ld_* of the direction's inputs and x8; no
+ * other pointer is looked at. 0 for a shape that the calls refuse. */
+ZOPT_API size_t zopt_ffn_workspace(const zopt_ffn_job* job, int32_t backward);
+/* Errors of both: EINVAL for NULL or misaligned pointers (16 bytes; scale bytes any), tokens < 0,
+ * dim or hidden < 1, any of them above 2^30, a row distance below the row's length or above 2^32,
+ * another act, both or (backward) neither of x / x8 and of kept / kept8, a checkpoint of another
+ * shape, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16; ETIMEOUT
+ * if a bounded wait of an earlier call's kernel gave up. tokens = 0: the forward does nothing, the
+ * backward sets the weight gradients to zero. */
+ZOPT_API zopt_status zopt_ffn_forward(const zopt_ffn_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream);
+ZOPT_API zopt_status zopt_ffn_backward(const zopt_ffn_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream);
+
+/* ======================================================================================
+ * 8. Linear cross entropy over a vocabulary
+ *
+ * For T = tokens rows x of D = dim features and the output matrix w [V][D] (V = vocab; the tied
+ * embedding's layout), with l = x w' the logits, which are never stored:
+ *   lse_t = log sum_v exp l_tv;  loss_t = lse_t - l_t,target(t)
+ *   dl_tv = (exp(l_tv - lse_t) - [v = target(t)]) dloss_t;  dx = dl w;  dw = dl' x.
+ * The forward reduces each tile of logits to a maximum and a sum where it was computed; the
+ * backward computes the logits again, a piece of the vocabulary at a time, and keeps at most two
+ * pieces' dl (bf16) in the workspace. A row whose target is ignore_index takes no part: loss, lse
+ * and its dx are 0 and its x adds nothing to dw, whatever x holds there. A target that is neither
+ * ignore_index nor in [0, vocab) makes its loss NaN and its gradients NaN, for found_inf to skip
+ * the step on. dloss is the gradient of each row's loss (1 / the number of counted rows for a
+ * mean). Repeated on the same inputs a call gives the same bits.
+ * ====================================================================================== */
+typedef struct zopt_linear_ce_job {
+  int64_t tokens, dim, vocab;
+  int64_t ignore_index;
+  const uint16_t* x;
+  int64_t ld_x;
+  const uint16_t* w;
+  int64_t ld_w;
+  const int64_t* target; /* [tokens] */
+  float* loss;           /* [tokens] forward: written */
+  float* lse;            /* [tokens] forward: written; backward: read */
+  const float* dloss;    /* [tokens] backward, from here on */
+  uint16_t* dx;          /* may be NULL */
+  int64_t ld_dx;
+  uint16_t* dw; /* may be NULL, not both */
+  int64_t ld_dw;
+  int32_t dtype; /* a zopt_dtype: ZOPT_BF16 */
+  int32_t reserved; /* 0 */
+} zopt_linear_ce_job; /* 136 bytes */
+
+/* Workspace bytes for a forward (backward = 0) or backward call, or either (backward = 1 covers
+ * both), of a job: from its tokens, dim, vocab, ld_x and ld_w alone. 0 for a shape that the calls
+ * refuse. */
+ZOPT_API size_t zopt_linear_ce_workspace(const zopt_linear_ce_job* job, int32_t backward);
+/* Errors of both: EINVAL for NULL or misaligned pointers (matrices 16 bytes, vectors their
+ * element), tokens < 0, dim or vocab < 1, any of them above 2^30, a row distance below dim or
+ * above 2^32, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16;
+ * ETIMEOUT as above. tokens = 0: the forward does nothing, the backward sets dw to zero. */
+ZOPT_API zopt_status zopt_linear_ce_forward(const zopt_linear_ce_job* job, void* d_ws, size_t ws_bytes,
+                                            zopt_stream stream);
+ZOPT_API zopt_status zopt_linear_ce_backward(const zopt_linear_ce_job* job, void* d_ws, size_t ws_bytes,
+                                             zopt_stream stream);
 
 #ifdef __cplusplus
 }

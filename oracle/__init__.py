@@ -17,6 +17,9 @@ written from the source pages' own statement of the method:
 * ``oracle.ns``      — Muon's quintic Newton-Schulz in fp64 (bluscript_zero_ckpt.cpp, the
   ShardedMuon design note: ``X <- aX + (bXX' + c(XX')^2)X``).
 
+* ``oracle.lm``      — the training operators beside the step: linear cross entropy, the gated
+  feed-forward block (bluscript_zero_ckpt.cpp, model config), the 8-bit activation checkpoint.
+
 Only ``tests/``, ``__graft_entry__.smoke()`` and ``bench.py``'s CPU-baseline / reference arm
 may import this package. The product path (the ``zero_sharded_optimizer_flat_gb300``
 package and its CUDA library) never imports, links or runs anything here, and this package

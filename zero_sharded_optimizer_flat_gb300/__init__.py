@@ -3,7 +3,9 @@ GB300 (sm_103a).
 
 Argument marshalling only: every step of the path runs in the library's CUDA kernels. The
 calls keep the C names: ``zopt_shard_layout`` (as :class:`ShardLayout`),
-``zopt_grad_norm_clip``, ``zopt_adamw_step``, ``zopt_ns_orthogonalize``. PyTorch provides
+``zopt_grad_norm_clip``, ``zopt_adamw_step``, ``zopt_ns_orthogonalize``, and the training
+operators whose gradients the step takes: ``zopt_ffn_forward`` / ``_backward``,
+``zopt_linear_ce_forward`` / ``_backward``, ``zopt_act_pack`` / ``_unpack``. PyTorch provides
 device memory and streams. The library must be built (``build_lib.build()``); if it is
 missing every call raises — there is no fallback.
 """
@@ -45,6 +47,34 @@ class _MuonHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("nesterov", ctypes.c_int32), ("adjust", ctypes.c_int32), ("ns_steps", ctypes.c_int32),
                 ("abc", ctypes.c_float * 3), ("eps", ctypes.c_float), ("guard", ctypes.c_float)]
+
+
+class _Act8(ctypes.Structure):
+    """``zopt_act8``: an 8-bit activation checkpoint."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("parts", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _FfnJob(ctypes.Structure):
+    """``zopt_ffn_job``: a gated feed-forward block, either direction."""
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32)] + [
+        f for name in ("w_gate_up", "w_down", "x") for f in
+        ((name, ctypes.c_void_p), ("ld_" + name.removeprefix("w_"), ctypes.c_int64))] + [
+        ("x8", ctypes.POINTER(_Act8)), ("kept", ctypes.c_void_p), ("ld_kept", ctypes.c_int64),
+        ("kept8", ctypes.POINTER(_Act8))] + [
+        f for name in ("y", "dy", "dx", "dw_gate_up", "dw_down") for f in
+        ((name, ctypes.c_void_p), ("ld_" + name, ctypes.c_int64))]
+
+
+class _LinearCeJob(ctypes.Structure):
+    """``zopt_linear_ce_job``: a linear cross entropy, either direction."""
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ignore_index", ctypes.c_int64), ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64),
+                ("w", ctypes.c_void_p), ("ld_w", ctypes.c_int64), ("target", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("dloss", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("ld_dx", ctypes.c_int64), ("dw", ctypes.c_void_p), ("ld_dw", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def lib() -> ctypes.CDLL:
@@ -104,6 +134,15 @@ def lib() -> ctypes.CDLL:
                                                vp]),
         "zopt_ns_orthogonalize_many": (ctypes.c_int, [ctypes.POINTER(_NsJob), i32, i32,
                                                       ctypes.POINTER(ctypes.c_float), ctypes.c_float, vp, sz, vp]),
+        "zopt_act8_scale_bytes": (sz, [i64, i64, i32]),
+        "zopt_act_pack": (ctypes.c_int, [vp, i64, ctypes.POINTER(_Act8), vp]),
+        "zopt_act_unpack": (ctypes.c_int, [ctypes.POINTER(_Act8), vp, i64, vp]),
+        "zopt_ffn_workspace": (sz, [ctypes.POINTER(_FfnJob), i32]),
+        "zopt_ffn_forward": (ctypes.c_int, [ctypes.POINTER(_FfnJob), vp, sz, vp]),
+        "zopt_ffn_backward": (ctypes.c_int, [ctypes.POINTER(_FfnJob), vp, sz, vp]),
+        "zopt_linear_ce_workspace": (sz, [ctypes.POINTER(_LinearCeJob), i32]),
+        "zopt_linear_ce_forward": (ctypes.c_int, [ctypes.POINTER(_LinearCeJob), vp, sz, vp]),
+        "zopt_linear_ce_backward": (ctypes.c_int, [ctypes.POINTER(_LinearCeJob), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -521,6 +560,201 @@ def muon_step(master, momentum, grad, out_bf16, ws, stats, *, lr: float, momentu
     hp = _muon_hparams(lr, momentum_coef, weight_decay, nesterov, match_rms_adamw, ns_steps, abc, eps, guard)
     _check(lib().zopt_muon_step(_ptr(master), _ptr(momentum), _ptr(grad), _dtype_code(grad), _ptr(out_bf16), rows,
                                 cols, batch, ctypes.byref(hp), _ptr(stats), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+# --------------------------------------------------------------------------- training operators
+
+ACT_SILU, ACT_GELU = 0, 1
+_ACTS = {"silu": ACT_SILU, "gelu": ACT_GELU}
+
+
+class Act8:
+    """An 8-bit activation checkpoint of a rows x cols bf16 matrix (``zopt_act8``): ``q`` holds the
+    e4m3 bytes, ``scale`` one exponent byte per block of 128 columns of each part."""
+
+    __slots__ = ("q", "scale", "rows", "cols", "parts", "_c")
+
+    def __init__(self, q, scale, parts: int = 1):
+        if q.dim() != 2 or not q.is_contiguous() or not scale.is_contiguous():
+            raise ValueError("q must be a contiguous matrix, scale contiguous")
+        self.q, self.scale, self.parts = q, scale, int(parts)
+        self.rows, self.cols = q.shape
+        if q.element_size() != 1 or scale.element_size() != 1 or scale.numel() != act8_scale_bytes(*q.shape, parts):
+            raise ValueError("q and scale must be byte tensors, scale of act8_scale_bytes(rows, cols, parts) bytes")
+        _on_device(q, scale)
+        self._c = _Act8(_ptr(q), _ptr(scale), self.rows, self.cols, self.parts, 0)
+
+
+def act8_scale_bytes(rows: int, cols: int, parts: int = 1) -> int:
+    return int(lib().zopt_act8_scale_bytes(int(rows), int(cols), int(parts)))
+
+
+def new_act8(rows: int, cols: int, parts: int = 1, device="cuda") -> Act8:
+    """An empty checkpoint for a rows x cols matrix (parts = 2 for a gate beside its up)."""
+    import torch
+    return Act8(torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                torch.empty(act8_scale_bytes(rows, cols, parts), dtype=torch.uint8, device=device), parts)
+
+
+def _on_device(*tensors) -> None:
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("tensors must be on the GPU")
+
+
+def _matrix(t, rows: int, cols: int, name: str):
+    """(address, row distance) of a rows x cols bf16 matrix with contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a {rows} x {cols} matrix with a contiguous last dimension")
+    if not t.is_cuda:
+        raise ValueError("tensors must be on the GPU")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _same_dtype(*tensors) -> int:
+    code = _dtype_code(tensors[0])
+    return code if all(t.dtype == tensors[0].dtype for t in tensors) else -1
+
+
+def act_pack(x, out: Act8, stream=None) -> None:
+    """``zopt_act_pack``: out = the 8-bit checkpoint of the bf16 matrix x."""
+    p, ld = _matrix(x, out.rows, out.cols, "x")
+    if _dtype_code(x) != BF16:
+        raise ValueError("x must be bf16")
+    _check(lib().zopt_act_pack(p, ld, out._c, _stream(stream)))
+
+
+def act_unpack(packed: Act8, out, stream=None) -> None:
+    """``zopt_act_unpack``: out (bf16) = the values the checkpoint stands for."""
+    p, ld = _matrix(out, packed.rows, packed.cols, "out")
+    if _dtype_code(out) != BF16:
+        raise ValueError("out must be bf16")
+    _check(lib().zopt_act_unpack(packed._c, p, ld, _stream(stream)))
+
+
+def _ffn_job(x, w_gate_up, w_down, act) -> _FfnJob:
+    hidden, dim = w_down.shape
+    rows = x.rows if isinstance(x, Act8) else x.shape[0]
+    j = _FfnJob()
+    j.tokens, j.dim, j.hidden = rows, dim, hidden
+    j.act = _ACTS.get(act, act if isinstance(act, int) else -1)
+    j.w_gate_up, j.ld_gate_up = _matrix(w_gate_up, dim, 2 * hidden, "w_gate_up")
+    j.w_down, j.ld_down = _matrix(w_down, hidden, dim, "w_down")
+    if isinstance(x, Act8):
+        j.x8 = ctypes.pointer(x._c)
+        j.dtype = _same_dtype(w_gate_up, w_down)
+    else:
+        j.x, j.ld_x = _matrix(x, rows, dim, "x")
+        j.dtype = _same_dtype(x, w_gate_up, w_down)
+    return j
+
+
+def _ffn_kept(j: _FfnJob, kept) -> None:
+    if isinstance(kept, Act8):
+        j.kept8 = ctypes.pointer(kept._c)
+    elif kept is not None:
+        if _dtype_code(kept) != BF16:
+            raise ValueError("kept must be bf16 or an Act8")
+        j.kept, j.ld_kept = _matrix(kept, j.tokens, 2 * j.hidden, "kept")
+
+
+def ffn_workspace(x, w_gate_up, w_down, backward: bool = True, dy=None) -> int:
+    """``zopt_ffn_workspace`` for these operands (x a bf16 matrix or an :class:`Act8`; dy, if it is
+    not contiguous)."""
+    j = _ffn_job(x, w_gate_up, w_down, "silu")
+    j.ld_dy = j.dim if dy is None else _matrix(dy, j.tokens, j.dim, "dy")[1]
+    return int(lib().zopt_ffn_workspace(j, int(bool(backward))))
+
+
+def new_ffn_workspace(x, w_gate_up, w_down, backward: bool = True, dy=None, device="cuda"):
+    """A workspace for :func:`ffn_forward` and (``backward``) :func:`ffn_backward`."""
+    import torch
+    return torch.empty(max(ffn_workspace(x, w_gate_up, w_down, backward, dy), 16), dtype=torch.uint8, device=device)
+
+
+def ffn_forward(x, w_gate_up, w_down, y, ws, *, kept=None, act: str = "silu", stream=None) -> None:
+    """``zopt_ffn_forward``: y = (a(x Wgate) * (x Wup)) Wdown. ``kept`` takes gate and up for the
+    backward: a bf16 matrix [tokens, 2 hidden], an :class:`Act8` of that shape in two parts, or None."""
+    j = _ffn_job(x, w_gate_up, w_down, act)
+    _ffn_kept(j, kept)
+    j.y, j.ld_y = _matrix(y, j.tokens, j.dim, "y")
+    if y.dtype != w_down.dtype:
+        j.dtype = -1
+    _on_device(ws)
+    _check(lib().zopt_ffn_forward(j, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def ffn_backward(dy, x, kept, w_gate_up, w_down, dx, dw_gate_up, dw_down, ws, *, act: str = "silu",
+                 stream=None) -> None:
+    """``zopt_ffn_backward`` from dy, x (bf16 or :class:`Act8`) and what the forward kept."""
+    j = _ffn_job(x, w_gate_up, w_down, act)
+    _ffn_kept(j, kept)
+    j.dy, j.ld_dy = _matrix(dy, j.tokens, j.dim, "dy")
+    j.dx, j.ld_dx = _matrix(dx, j.tokens, j.dim, "dx")
+    j.dw_gate_up, j.ld_dw_gate_up = _matrix(dw_gate_up, j.dim, 2 * j.hidden, "dw_gate_up")
+    j.dw_down, j.ld_dw_down = _matrix(dw_down, j.hidden, j.dim, "dw_down")
+    if _same_dtype(dy, dx, dw_gate_up, dw_down, w_down) != j.dtype:
+        j.dtype = -1
+    _on_device(ws)
+    _check(lib().zopt_ffn_backward(j, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def _linear_ce_job(x, w) -> _LinearCeJob:
+    j = _LinearCeJob()
+    j.tokens, j.dim, j.vocab = x.shape[0], x.shape[1], w.shape[0]
+    j.x, j.ld_x = _matrix(x, j.tokens, j.dim, "x")
+    j.w, j.ld_w = _matrix(w, j.vocab, j.dim, "w")
+    j.dtype = _same_dtype(x, w)
+    return j
+
+
+def _vector(t, n: int, dtype, name: str):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on the GPU")
+    return t.data_ptr()
+
+
+def linear_ce_workspace(x, w, backward: bool = True) -> int:
+    """``zopt_linear_ce_workspace`` for these operands."""
+    return int(lib().zopt_linear_ce_workspace(_linear_ce_job(x, w), int(bool(backward))))
+
+
+def new_linear_ce_workspace(x, w, backward: bool = True, device="cuda"):
+    """A workspace for :func:`linear_ce_forward` and (``backward``) :func:`linear_ce_backward`."""
+    import torch
+    return torch.empty(max(linear_ce_workspace(x, w, backward), 16), dtype=torch.uint8, device=device)
+
+
+def linear_ce_forward(x, w, target, loss, lse, ws, *, ignore_index: int = -100, stream=None) -> None:
+    """``zopt_linear_ce_forward``: each row's loss and log-sum-exp (fp32) of the logits x w' against
+    target (int64), without storing the logits."""
+    import torch
+    j = _linear_ce_job(x, w)
+    j.ignore_index = int(ignore_index)
+    j.target = _vector(target, j.tokens, torch.int64, "target")
+    j.loss = _vector(loss, j.tokens, torch.float32, "loss")
+    j.lse = _vector(lse, j.tokens, torch.float32, "lse")
+    _on_device(ws)
+    _check(lib().zopt_linear_ce_forward(j, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def linear_ce_backward(x, w, target, lse, dloss, dx, dw, ws, *, ignore_index: int = -100, stream=None) -> None:
+    """``zopt_linear_ce_backward``: dx and dw (either may be None) from the forward's lse and the
+    gradient dloss (fp32) of each row's loss."""
+    import torch
+    j = _linear_ce_job(x, w)
+    j.ignore_index = int(ignore_index)
+    j.target = _vector(target, j.tokens, torch.int64, "target")
+    j.lse = _vector(lse, j.tokens, torch.float32, "lse")
+    j.dloss = _vector(dloss, j.tokens, torch.float32, "dloss")
+    if dx is not None:
+        j.dx, j.ld_dx = _matrix(dx, j.tokens, j.dim, "dx")
+    if dw is not None:
+        j.dw, j.ld_dw = _matrix(dw, j.vocab, j.dim, "dw")
+    if any(t is not None and t.dtype != x.dtype for t in (dx, dw)):
+        j.dtype = -1
+    _on_device(ws)
+    _check(lib().zopt_linear_ce_backward(j, _ptr(ws), ws.numel(), _stream(stream)))
 
 
 def take_device_error() -> int:

@@ -1,0 +1,370 @@
+// The gated feed-forward block, forward and backward.
+//
+// Forward, two products: gate and up in one kernel whose epilogue applies the activation and the
+// product (and keeps gate and up, in bf16 or in 8 bits), then y = h down. h takes one pass through
+// memory in bf16; the gate and up themselves only where they are kept.
+//
+// Backward, four products in two launches: dh = dy down', whose epilogue reads the kept gate and up
+// and writes dgate, dup and h; then dx, dgate_up and ddown in one launch, longest units first, so
+// that only one launch's last wave runs short. 18 T D F flops for both directions.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "act8_host.h"
+#include "launch.cuh"
+#include "lm_gemm.cuh"
+#include "ns_internal.h"
+
+namespace zopt {
+namespace lm {
+namespace {
+
+constexpr long long kMaxDim = 1LL << 30, kMaxLd = 1LL << 32;
+
+struct FfnPlan {
+  long long dp, fp;  // dim and hidden rounded up to 8
+  bool stage_x, stage_dy, stage_gate_up, stage_down;
+  size_t xs, dys, gate_up, down, h, dgu, slab, total;
+};
+
+size_t take(size_t& at, long long bytes) {
+  const size_t here = at;
+  at += static_cast<size_t>(round_up(bytes, 1024));
+  return here;
+}
+
+bool shape_ok(const zopt_ffn_job& c, bool backward) {
+  auto ld = [](int64_t v, int64_t least) { return v >= least && v <= kMaxLd; };
+  return c.tokens >= 0 && c.dim >= 1 && c.hidden >= 1 && c.tokens <= kMaxDim && c.dim <= kMaxDim && c.hidden <= kMaxDim / 2 &&
+         ld(c.ld_gate_up, 2 * c.hidden) && ld(c.ld_down, c.dim) && (c.x8 != nullptr || ld(c.ld_x, c.dim)) &&
+         (!backward || ld(c.ld_dy, c.dim));
+}
+
+void y_job(const zopt_ffn_job& c, Job& j) {
+  j = Job{};
+  j.kind = kStore;
+  j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.dim), j.K = static_cast<int>(c.hidden);
+  j.b_mn = 1;
+  set_tiles(j);
+}
+
+// The backward's second launch: dx, dgate_up (one job, or the gate's and up's columns apart where
+// the workspace pads them) and ddown. Returns their number.
+int grad_jobs(const zopt_ffn_job& c, const FfnPlan& p, Job* j) {
+  const int T = static_cast<int>(c.tokens), D = static_cast<int>(c.dim), F = static_cast<int>(c.hidden);
+  int n = 0;
+  auto add = [&](int m, int nn, int k, bool mn) {
+    j[n] = Job{};
+    j[n].kind = kStore;
+    j[n].M = m, j[n].N = nn, j[n].K = k;
+    j[n].a_mn = j[n].b_mn = mn;
+    set_tiles(j[n++]);
+  };
+  add(T, D, static_cast<int>(2 * p.fp), false);
+  if (p.fp == F) {
+    add(D, 2 * F, T, true);
+  } else {
+    add(D, F, T, true);
+    add(D, F, T, true);
+  }
+  add(F, D, T, true);
+  return n;
+}
+
+long long slab_elems(Job* j, int n) {
+  plan_splits(j, n);
+  long long e = 0;
+  for (int i = 0; i < n; ++i) e += round_up(split_elems(j[i]), 256);
+  return e;
+}
+
+FfnPlan plan(const zopt_ffn_job& c, bool backward) {
+  FfnPlan p{};
+  const long long T = c.tokens, D = c.dim, F = c.hidden;
+  p.dp = round_up(D, 8), p.fp = round_up(F, 8);
+  p.stage_x = (backward && c.x8 != nullptr) || c.ld_x % 8 != 0;
+  p.stage_dy = backward && c.ld_dy % 8 != 0;
+  p.stage_gate_up = c.ld_gate_up % 8 != 0 || F % 8 != 0;
+  p.stage_down = c.ld_down % 8 != 0;
+  size_t at = 0;
+  if (p.stage_gate_up) p.gate_up = take(at, D * 2 * p.fp * 2);
+  if (p.stage_down) p.down = take(at, F * p.dp * 2);
+  if (p.stage_x) p.xs = take(at, T * p.dp * 2);
+  p.h = take(at, T * p.fp * 2);
+  const size_t shared = at;
+  Job j[kMaxJobs];
+  y_job(c, j[0]);
+  if (T > 0) {
+    const long long e = slab_elems(j, 1);
+    if (e) p.slab = take(at, e * 4);
+  }
+  p.total = at;
+  if (!backward) return p;
+  at = shared;
+  if (p.stage_dy) p.dys = take(at, T * p.dp * 2);
+  p.dgu = take(at, T * 2 * p.fp * 2);
+  p.slab = at;
+  if (T > 0) {
+    const long long e = slab_elems(j, grad_jobs(c, p, j));
+    if (e) take(at, e * 4);
+  }
+  p.total = std::max(p.total, at);
+  return p;
+}
+
+zopt_status check(const char* fn, const zopt_ffn_job* c, bool backward, void* d_ws, size_t ws_bytes) {
+  const std::string f(fn);
+  auto bad = [&](const char* what) { return fail(ZOPT_EINVAL, f + ": " + what); };
+  if (c == nullptr) return bad("NULL job");
+  if (c->dtype != ZOPT_BF16) return fail(ZOPT_EUNSUPPORTED, f + ": dtype must be ZOPT_BF16");
+  if (c->act != ZOPT_ACT_SILU && c->act != ZOPT_ACT_GELU) return bad("act must be ZOPT_ACT_SILU or ZOPT_ACT_GELU");
+  if (c->tokens < 0 || c->dim < 1 || c->hidden < 1) return bad("tokens < 0, dim < 1 or hidden < 1");
+  if (c->tokens > kMaxDim || c->dim > kMaxDim || c->hidden > kMaxDim / 2)
+    return bad("tokens or dim above 2^30, or hidden above 2^29");
+  const int64_t T = c->tokens, D = c->dim, F = c->hidden;
+  auto ld_bad = [](int64_t ld, int64_t least) { return ld < least || ld > kMaxLd; };
+  if (ld_bad(c->ld_gate_up, 2 * F) || ld_bad(c->ld_down, D)) return bad("a weight's row distance below its row or above 2^32");
+  if (c->w_gate_up == nullptr || c->w_down == nullptr) return bad("NULL weight");
+  if (!aligned16(c->w_gate_up) || !aligned16(c->w_down)) return bad("matrices must be 16-byte aligned");
+  if (c->kept != nullptr && c->kept8 != nullptr) return bad("both kept and kept8");
+  if (c->kept != nullptr && (ld_bad(c->ld_kept, 2 * F) || !aligned16(c->kept))) return bad("kept: row distance or alignment");
+  if (c->kept8 != nullptr) {
+    const zopt_status st = act8::check(fn, *c->kept8);
+    if (st != ZOPT_OK) return st;
+    if (c->kept8->rows != T || c->kept8->cols != 2 * F || c->kept8->parts != 2)
+      return bad("kept8 must be tokens x 2 hidden in two parts");
+  }
+  if (backward) {
+    if ((c->dx == nullptr && T > 0) || c->dw_gate_up == nullptr || c->dw_down == nullptr) return bad("NULL dx, dw_gate_up or dw_down");
+    if (ld_bad(c->ld_dx, D) || ld_bad(c->ld_dw_gate_up, 2 * F) || ld_bad(c->ld_dw_down, D))
+      return bad("a gradient's row distance below its row or above 2^32");
+    if (!aligned16(c->dx) || !aligned16(c->dw_gate_up) || !aligned16(c->dw_down)) return bad("matrices must be 16-byte aligned");
+  }
+  if (!backward && c->x8 != nullptr) return bad("the forward takes x in bf16");
+  if ((c->x != nullptr) == (backward && c->x8 != nullptr) && T > 0) return bad("exactly one of x and x8 is wanted");
+  if (T == 0) return ok();
+  if (c->x8 != nullptr) {
+    const zopt_status st = act8::check(fn, *c->x8);
+    if (st != ZOPT_OK) return st;
+    if (c->x8->rows != T || c->x8->cols != D || c->x8->parts != 1) return bad("x8 must be tokens x dim in one part");
+  } else if (ld_bad(c->ld_x, D) || !aligned16(c->x)) {
+    return bad("x: row distance or alignment");
+  }
+  if (backward) {
+    if (c->kept == nullptr && c->kept8 == nullptr) return bad("the backward needs kept or kept8");
+    if (c->dy == nullptr || ld_bad(c->ld_dy, D) || !aligned16(c->dy)) return bad("dy: NULL, row distance or alignment");
+  } else {
+    if (c->y == nullptr || ld_bad(c->ld_y, D) || !aligned16(c->y)) return bad("y: NULL, row distance or alignment");
+  }
+  if (d_ws == nullptr || !aligned16(d_ws)) return bad("the workspace must be 16-byte aligned");
+  if (ws_bytes < plan(*c, backward).total) return bad("workspace too small");
+  return ok();
+}
+
+#define TRY(expr)                   \
+  do {                              \
+    const zopt_status st_ = (expr); \
+    if (st_ != ZOPT_OK) return st_; \
+  } while (0)
+
+// The operands as the TMA reads them: in place, or copied (or unpacked) into the workspace.
+struct Inputs {
+  const uint16_t *x, *gate_up, *down, *dy;
+  long long px, pgu, pdown, pdy;
+  long long up;  // gate_up's column of up column 0
+};
+zopt_status stage_inputs(const char* fn, const zopt_ffn_job& c, const FfnPlan& p, uint8_t* ws, Inputs& in, cudaStream_t s) {
+  in = Inputs{c.x, c.w_gate_up, c.w_down, c.dy, c.ld_x, c.ld_gate_up, c.ld_down, c.ld_dy, c.hidden};
+  auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
+  if (p.stage_gate_up) {
+    uint16_t* d = at(p.gate_up);
+    TRY(launch_stage(fn, d, 2 * p.fp, p.fp, c.w_gate_up, c.ld_gate_up, c.dim, c.hidden, s));
+    TRY(launch_stage(fn, d + p.fp, 2 * p.fp, p.fp, c.w_gate_up + c.hidden, c.ld_gate_up, c.dim, c.hidden, s));
+    in.gate_up = d, in.pgu = 2 * p.fp, in.up = p.fp;
+  }
+  if (p.stage_down) {
+    TRY(launch_stage(fn, at(p.down), p.dp, p.dp, c.w_down, c.ld_down, c.hidden, c.dim, s));
+    in.down = at(p.down), in.pdown = p.dp;
+  }
+  if (p.stage_x) {
+    if (c.x8 != nullptr) {
+      TRY(act8::unpack(fn, *c.x8, at(p.xs), p.dp, s));
+    } else {
+      TRY(launch_stage(fn, at(p.xs), p.dp, p.dp, c.x, c.ld_x, c.tokens, c.dim, s));
+    }
+    in.x = at(p.xs), in.px = p.dp;
+  }
+  if (p.stage_dy) {
+    TRY(launch_stage(fn, at(p.dys), p.dp, p.dp, c.dy, c.ld_dy, c.tokens, c.dim, s));
+    in.dy = at(p.dys), in.pdy = p.dp;
+  }
+  return ok();
+}
+
+void glu_fields(Job& j, const zopt_ffn_job& c) {
+  j.act = c.act;
+  j.hidden = static_cast<int>(c.hidden);
+  if (c.kept8 != nullptr) {
+    j.kept_mode = kKeep8;
+    j.kept = c.kept8->q;
+    j.ld_kept = 2 * c.hidden;
+    j.kept_scale = c.kept8->scale;
+  } else if (c.kept != nullptr) {
+    j.kept_mode = kKeepBf16;
+    j.kept = c.kept;
+    j.ld_kept = c.ld_kept;
+  }
+}
+
+// Where a kStore job's result goes: its partial sums' slab, or the caller's matrix.
+zopt_status finish(const char* fn, Job& j, uint16_t* out, long long ld, float*& slab, SumBatch& sums) {
+  if (j.splits > 1) {
+    j.out_mode = kOutF32;
+    j.out = slab;
+    j.ld_out = split_pitch(j.N);
+    j.split_stride = j.M * j.ld_out;
+    SumJob& q = sums.job[sums.n];
+    q = SumJob{slab, j.split_stride, j.ld_out, j.splits, j.M, j.N, out, ld, nullptr};
+    sums.start[sums.n + 1] = sums.start[sums.n] + q.M * (q.pitch / 4);
+    ++sums.n;
+    slab += round_up(split_elems(j), 256);
+    return ok();
+  }
+  if (tma_out_ok(out, j.N, ld)) {
+    j.out_mode = kOutTma;
+    return map_output(fn, &j.D0, out, j.M, j.N, ld);
+  }
+  j.out_mode = kOutBf16;
+  j.out = out;
+  j.ld_out = ld;
+  return ok();
+}
+
+zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStream_t s) {
+  const char* fn = "zopt_ffn_forward";
+  TRY(check(fn, cp, false, d_ws, ws_bytes));
+  const zopt_ffn_job& c = *cp;
+  if (c.tokens == 0) return ok();
+  int* err = nullptr;
+  TRY(ns::take_error_word(fn, &err));
+  const FfnPlan p = plan(c, false);
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  Inputs in;
+  TRY(stage_inputs(fn, c, p, ws, in, s));
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
+  {
+    Batch b{};
+    b.err = err;
+    b.n = 1;
+    Job& j = b.job[0];
+    j.kind = kGluFwd;
+    j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.hidden), j.K = static_cast<int>(c.dim);
+    j.b_mn = 1;
+    j.q_up = static_cast<int>(in.up);
+    set_tiles(j);
+    glu_fields(j, c);
+    TRY(map_operand(fn, &j.P, in.x, c.tokens, c.dim, in.px, false));
+    TRY(map_operand(fn, &j.Q, in.gate_up, in.up + c.hidden, c.dim, in.pgu, true));
+    TRY(map_output(fn, &j.D0, h, c.tokens, c.hidden, p.fp));
+    if (j.kept_mode == kKeepBf16 && tma_out_ok(c.kept, c.hidden, c.ld_kept)) {
+      j.kept_mode = kKeepTma;
+      TRY(map_output(fn, &j.D1, c.kept, c.tokens, c.hidden, c.ld_kept));
+      TRY(map_output(fn, &j.D2, c.kept + c.hidden, c.tokens, c.hidden, c.ld_kept));
+    }
+    TRY(launch(fn, b, kGluFwd, s));
+  }
+  Batch b{};
+  b.err = err;
+  b.n = 1;
+  y_job(c, b.job[0]);
+  plan_splits(b.job, 1);
+  TRY(map_operand(fn, &b.job[0].P, h, c.tokens, c.hidden, p.fp, false));
+  TRY(map_operand(fn, &b.job[0].Q, in.down, c.dim, c.hidden, in.pdown, true));
+  SumBatch sums{};
+  float* slab = reinterpret_cast<float*>(ws + p.slab);
+  TRY(finish(fn, b.job[0], c.y, c.ld_y, slab, sums));
+  TRY(launch(fn, b, kStore, s));
+  return sums.n > 0 ? launch_sums(fn, sums, s) : ok();
+}
+
+zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStream_t s) {
+  const char* fn = "zopt_ffn_backward";
+  TRY(check(fn, cp, true, d_ws, ws_bytes));
+  const zopt_ffn_job& c = *cp;
+  if (c.tokens == 0) {
+    ZOPT_CUDA_TRY(cudaMemset2DAsync(c.dw_gate_up, c.ld_dw_gate_up * 2, 0, 2 * c.hidden * 2, c.dim, s));
+    ZOPT_CUDA_TRY(cudaMemset2DAsync(c.dw_down, c.ld_dw_down * 2, 0, c.dim * 2, c.hidden, s));
+    return ok();
+  }
+  int* err = nullptr;
+  TRY(ns::take_error_word(fn, &err));
+  const FfnPlan p = plan(c, true);
+  uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  Inputs in;
+  TRY(stage_inputs(fn, c, p, ws, in, s));
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
+  uint16_t* dgu = reinterpret_cast<uint16_t*>(ws + p.dgu);
+  {
+    Batch b{};
+    b.err = err;
+    b.n = 1;
+    Job& j = b.job[0];
+    j.kind = kGluBwd;
+    // over the padded width: down's missing rows read as zero, so the pad columns become zero and
+    // may stand in the inner length of dx
+    j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(p.fp), j.K = static_cast<int>(c.dim);
+    set_tiles(j);
+    glu_fields(j, c);
+    TRY(map_operand(fn, &j.P, in.dy, c.tokens, c.dim, in.pdy, false));
+    TRY(map_operand(fn, &j.Q, in.down, c.hidden, c.dim, in.pdown, false));
+    TRY(map_output(fn, &j.D0, dgu, c.tokens, p.fp, 2 * p.fp));
+    TRY(map_output(fn, &j.D1, dgu + p.fp, c.tokens, p.fp, 2 * p.fp));
+    TRY(map_output(fn, &j.D2, h, c.tokens, p.fp, p.fp));
+    TRY(launch(fn, b, kGluBwd, s));
+  }
+  Batch b{};
+  b.err = err;
+  Job jobs[kMaxJobs];
+  const int n = grad_jobs(c, p, jobs);
+  plan_splits(jobs, n);
+  SumBatch sums{};
+  float* slab = reinterpret_cast<float*>(ws + p.slab);
+  TRY(map_operand(fn, &jobs[0].P, dgu, c.tokens, 2 * p.fp, 2 * p.fp, false));
+  TRY(map_operand(fn, &jobs[0].Q, in.gate_up, c.dim, 2 * p.fp, in.pgu, false));
+  TRY(finish(fn, jobs[0], c.dx, c.ld_dx, slab, sums));
+  for (int k = 1; k + 1 < n; ++k) {  // the gate's and up's columns together, or apart
+    const int up = k - 1;
+    TRY(map_operand(fn, &jobs[k].P, in.x, c.dim, c.tokens, in.px, true));
+    TRY(map_operand(fn, &jobs[k].Q, dgu + up * p.fp, jobs[k].N, c.tokens, 2 * p.fp, true));
+    TRY(finish(fn, jobs[k], c.dw_gate_up + up * c.hidden, c.ld_dw_gate_up, slab, sums));
+  }
+  TRY(map_operand(fn, &jobs[n - 1].P, h, c.hidden, c.tokens, p.fp, true));
+  TRY(map_operand(fn, &jobs[n - 1].Q, in.dy, c.dim, c.tokens, in.pdy, true));
+  TRY(finish(fn, jobs[n - 1], c.dw_down, c.ld_dw_down, slab, sums));
+  // The longest units first: the launch's end is then made of short ones.
+  const bool dx_first = jobs[0].kb_per_split >= jobs[1].kb_per_split;
+  b.n = n;
+  for (int k = 0; k < n; ++k) b.job[k] = jobs[dx_first ? k : (k + 1) % n];
+  TRY(launch(fn, b, kStore, s));
+  return sums.n > 0 ? launch_sums(fn, sums, s) : ok();
+}
+
+}  // namespace
+}  // namespace lm
+}  // namespace zopt
+
+extern "C" size_t zopt_ffn_workspace(const zopt_ffn_job* job, int32_t backward) {
+  if (job == nullptr || !zopt::lm::shape_ok(*job, backward != 0)) return 0;
+  const size_t n = zopt::lm::plan(*job, backward != 0).total;
+  return n < 16 ? 16 : n;
+}
+
+extern "C" zopt_status zopt_ffn_forward(const zopt_ffn_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream) {
+  return zopt::guarded([&] { return zopt::lm::forward(job, d_ws, ws_bytes, stream); });
+}
+
+extern "C" zopt_status zopt_ffn_backward(const zopt_ffn_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream) {
+  return zopt::guarded([&] { return zopt::lm::backward(job, d_ws, ws_bytes, stream); });
+}

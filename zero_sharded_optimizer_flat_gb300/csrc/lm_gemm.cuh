@@ -1,0 +1,153 @@
+// The matrix products of the training operators (linear_ce.cu, ffn.cu) on CTA pairs, each with the
+// epilogue its operator needs: what a launch is made of, on both sides of the launch.
+//
+// A launch is a batch of jobs. A job is one product D = P Q, D of M x N with inner length K,
+// fp32 accumulation over bf16 operands, cut into 256 x 256 tiles (kGluFwd: 256 rows x 128 gate and
+// the matching 128 up columns) and, where a launch would leave most CTA pairs idle, into runs of
+// k-blocks as well. Operands come through 2-D tensor maps: P's rows and Q's columns either with the
+// inner length contiguous ("K-major") or with the other one ("MN-major", a_mn / b_mn).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace zopt {
+namespace lm {
+
+constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+constexpr int kStages = 6;
+constexpr int kHalfBytes = 128 * kTileK * 2;  // one CTA's half of a stage's P or Q: 16 KiB
+constexpr int kMnBoxBytes = 64 * kTileK * 2;  // one 64 (MN) x 64 (K) box of an MN-major operand
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr int kBoxBytes = 32 * 32 * 2;
+constexpr int kBoxes = 2;  // output boxes per epilogue warp
+constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxes * kBoxBytes + 1024 + 256;
+static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+constexpr int kMaxJobs = 5;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// What an epilogue makes of its accumulators.
+enum Kind : int {
+  kStore = 1,   // D (+ add), rounded to bf16 or kept in fp32
+  kCeFwd = 2,   // softmax statistics of the logits
+  kCeBwd = 4,   // the logits' gradient
+  kGluFwd = 8,  // h = a(gate) * up, gate and up kept
+  kGluBwd = 16  // dgate, dup and h from dh
+};
+
+enum OutMode : int { kOutTma = 0, kOutBf16 = 1, kOutF32 = 2 };          // kStore: through D0, or row stores
+enum KeptMode : int { kKeepNone = 0, kKeepTma = 1, kKeepBf16 = 2, kKeep8 = 3 };  // kGluFwd, kGluBwd
+
+struct alignas(64) Job {
+  CUtensorMap P, Q, D0, D1, D2;
+  int kind;
+  int M, N, K;
+  int a_mn, b_mn;
+  int q_up;  // kGluFwd: Q's column of up column 0
+  int tiles_m, tiles_n, tiles;
+  int nk, kb_per_split, splits;
+  int whole;      // its inner length is not cut
+  int rows_fast;  // consecutive tiles walk down a tile column (else along a tile row)
+  // kStore
+  int out_mode;
+  void* out;
+  long long ld_out, split_stride;  // split_stride: elements between the partial sums of one tile's runs of k
+  const float* add;                // fp32 M x N added to D; null: none
+  long long ld_add;
+  const float* alpha;  // (D + add) is multiplied by *alpha; null: 1
+  // kCeFwd, kCeBwd
+  const int64_t* target;
+  int64_t ignore, vocab, col0;  // the job's columns are vocabulary entries col0 ...
+  const float* lse;
+  const float* dloss;
+  const float* unit;  // kCeBwd: dl is stored in this unit (it is its products' alpha)
+  float2* part;   // kCeFwd: (max, sum) of 128 columns' logits times kLog2e, at [2 tile column + half][row]
+  float* tlogit;  // kCeFwd: the target's logit
+  // kGluFwd, kGluBwd
+  int act, kept_mode;
+  void* kept;  // gate and up as the caller keeps them: row r's gate at r * ld_kept, its up hidden later
+  long long ld_kept;
+  uint8_t* kept_scale;  // kKeep8: row r's block exponents at r * 2 blocks, the gate's first
+  int hidden;           // true width of the gate (N is its padded width in kGluBwd)
+};
+
+struct Batch {
+  int n;
+  int start[kMaxJobs + 1];
+  int* err;
+  Job job[kMaxJobs];
+};
+
+// ------------------------------------------------------------------ host side
+
+// A bf16 row-major matrix [outer][inner] with `pitch` elements between rows, boxes box_inner x
+// box_outer: the 128-byte swizzle for operands (box_inner 64), the 64-byte one for 32 x 32 outputs.
+zopt_status make_map(const char* fn, CUtensorMap* m, const void* base, long long inner, long long outer,
+                     long long pitch, int box_inner, int box_outer);
+// P [M][K] (K contiguous), or stored [K][M]; the same for Q's columns [N][K] or [K][N].
+zopt_status map_operand(const char* fn, CUtensorMap* m, const void* base, long long mn, long long k, long long pitch,
+                        bool mn_major);
+zopt_status map_output(const char* fn, CUtensorMap* m, void* base, long long rows, long long cols, long long pitch);
+// Whether a result's rows of `cols` elements, `pitch` apart, can be stored by the TMA: it moves whole
+// 16-byte pieces, so a row has to end on one or it would overwrite what lies beside the result.
+inline bool tma_out_ok(const void* base, long long cols, long long pitch) {
+  return aligned16(base) && pitch % 8 == 0 && cols % 8 == 0;
+}
+
+// Fills a job's tile counts from kind, M, N, K; k_blocks is its number of 64-deep blocks.
+void set_tiles(Job& j);
+// Cuts the inner length of the batch's kStore jobs so that no pair's run of k-blocks is much longer
+// than the launch's average (none where there are tiles enough). Depends on the shapes alone.
+void plan_splits(Job* jobs, int n);
+// fp32 elements of a job's partial sums (0 without splits): splits matrices of M x split_pitch(N).
+inline long long split_pitch(long long n) { return (n + 3) / 4 * 4; }
+inline long long split_elems(const Job& j) {
+  return j.splits > 1 ? static_cast<long long>(j.splits) * j.M * split_pitch(j.N) : 0;
+}
+// Launches the batch with the kernel for `kinds` (a union of Kind values it was built for).
+zopt_status launch(const char* fn, Batch& b, int kinds, cudaStream_t s);
+
+// After a launch with splits: out = the sum of each job's partial sums in split order, as bf16.
+struct SumJob {
+  const float* part;
+  long long split_stride, pitch;
+  int splits;
+  long long M, N;
+  uint16_t* out;
+  long long ld_out;
+  const float* alpha;
+};
+struct SumBatch {
+  int n;
+  long long start[kMaxJobs + 1];  // in groups of four columns
+  SumJob job[kMaxJobs];
+};
+zopt_status launch_sums(const char* fn, const SumBatch& b, cudaStream_t s);
+
+// dst[r][c] = src[r][c] for c < cols, 0 for cols <= c < dst_cols: an operand that the TMA cannot read
+// where it is.
+zopt_status launch_stage(const char* fn, uint16_t* dst, long long dst_pitch, long long dst_cols, const uint16_t* src,
+                         long long src_pitch, long long rows, long long cols, cudaStream_t s);
+
+// Blocks of 256 threads for `items` threads' work, at most eight per SM.
+unsigned blocks_for(long long items, int sms);
+
+// Eight bf16 elements from s, those from n on zero.
+__device__ __forceinline__ uint4 row_piece8(const uint16_t* s, long long n) {
+  if (n >= 8 && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) return *reinterpret_cast<const uint4*>(s);
+  uint32_t x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = k < n ? s[k] : 0u;
+  return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
+}
+
+inline long long round_up(long long x, long long a) { return (x + a - 1) / a * a; }
+
+}  // namespace lm
+}  // namespace zopt
