@@ -123,12 +123,63 @@ __device__ __forceinline__ int job_of(const Batch& b, int t) {
   return j;
 }
 
-__device__ __forceinline__ bool wait_drain(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = tc::globaltimer();
-  while (!tc::mbar_try_wait(bar, parity)) {
-    if (tc::globaltimer() - t0 > tc::kWaitLimitNs) return false;
+// True in one lane of a converged warp. The copies and MMAs take their operands from uniform
+// registers: behind this predicate the compiler knows that one thread issues them, behind a
+// comparison of lanes it has to issue them lane by lane (680 against 521 cycles a k-block of 8192^3, whose MMAs
+// take 512).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// A bounded wait for an mbarrier (given by its shared-memory address) that costs the two threads
+// feeding the tensor cores as little as a wait can: the clock and the error word (in host memory)
+// are only looked at every 256th failed try. Each try may sleep in the hardware until the phase
+// completes.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, int* err) {
+  unsigned long long t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    if (try_wait(bar, parity)) return true;
+    if ((spin & 255u) == 0) {
+      const unsigned long long t = tc::globaltimer();
+      if (t0 == 0) t0 = t;
+      if (err != nullptr && t - t0 > 1000000ull && *reinterpret_cast<volatile int*>(err) != 0) return false;
+      if (t - t0 > tc::kWaitLimitNs) {
+        if (err != nullptr) atomicExch(err, 1);
+        return false;
+      }
+    }
   }
-  return true;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int* err) {
+  return try_wait(bar, parity) || wait_slow(bar, parity, err);
+}
+// The same without an error to report or heed: for copies and products that must have ended before
+// their memory is given up.
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) { wait(bar, parity, nullptr); }
+
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(dst),
+      "l"(m), "r"(bar_cluster), "r"(c0), "r"(c1)
+      : "memory");
 }
 
 // a(z) = z s(phi(z)) with the logistic s: phi = z (SiLU), or 2 sqrt(2/pi) (z + 0.044715 z^3), which
@@ -476,43 +527,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::pdl_launch_dependents();
   tc::pdl_wait();  // the previous launch's outputs are complete and visible
 
+  int* const err = B.err;
+  const uint32_t full0 = tc::smem_u32(full), empty0 = tc::smem_u32(empty);
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ---------------------------------------------------------------- TMA producer (both CTAs)
-      int s = 0;
-      uint32_t ph = 0;
-      int armed[kStages];
-      for (int q = 0; q < kStages; ++q) armed[q] = -1;
+      // Every cycle of this loop counts: a k-block takes the MMAs 512 cycles, and the thread has to
+      // wait for a stage, arm it and issue two to four loads in less. So everything that a job fixes
+      // is in registers before its k-loop.
+      const uint32_t a0 = tc::smem_u32(sA), b0 = tc::smem_u32(sB);
+      const uint32_t lead0 = tc::map_to_rank(full0, 0);  // all loads complete on the leader's barriers
+      uint32_t s = 0, ph = 1;
+      long long done = 0;  // stages armed so far
       bool ok = true;
       for (int t = pair; ok && t < total; t += npairs) {
         const int ji = job_of(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of(j, t - B.start[ji]);
+        const CUtensorMap* const P = &j.P;
+        const CUtensorMap* const Q = &j.Q;
+        const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
         const int row0 = w.ti * kTileM + static_cast<int>(rank) * 128;  // this CTA's rows of P
         int col0 = w.tj * kTileN + static_cast<int>(rank) * 128;        // this CTA's columns of Q
         if ((kKinds & kGluFwd) && j.kind == kGluFwd) col0 = w.tj * 128 + (leader ? 0 : j.q_up);
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!tc::mbar_wait(empty + s, ph ^ 1u, B.err)) {
+        const int k_end = w.kb1 * kTileK;
+        for (int k = w.kb0 * kTileK; k < k_end; k += kTileK) {
+          if (!wait(empty0 + 8 * s, ph, err)) {
             ok = false;
             break;
           }
           if (leader) tc::mbar_arrive_expect_tx(full + s, 4 * kHalfBytes);  // both CTAs' halves of P and Q
-          armed[s] = static_cast<int>(ph);
-          const uint32_t bar = tc::map_to_rank(tc::smem_u32(full + s), 0);
-          uint8_t* a = sA + s * kHalfBytes;
-          uint8_t* b = sB + s * kHalfBytes;
-          if (!j.a_mn) {
-            tc::tma_load_2d_pair(a, &j.P, bar, kb * kTileK, row0);
+          const uint32_t bar = lead0 + 8 * s, a = a0 + s * kHalfBytes, b = b0 + s * kHalfBytes;
+          if (!amn) {
+            load_box(a, P, bar, k, row0);
           } else {
-            tc::tma_load_2d_pair(a, &j.P, bar, row0, kb * kTileK);
-            tc::tma_load_2d_pair(a + kMnBoxBytes, &j.P, bar, row0 + 64, kb * kTileK);
+            load_box(a, P, bar, row0, k);
+            load_box(a + kMnBoxBytes, P, bar, row0 + 64, k);
           }
-          if (!j.b_mn) {
-            tc::tma_load_2d_pair(b, &j.Q, bar, kb * kTileK, col0);
+          if (!bmn) {
+            load_box(b, Q, bar, k, col0);
           } else {
-            tc::tma_load_2d_pair(b, &j.Q, bar, col0, kb * kTileK);
-            tc::tma_load_2d_pair(b + kMnBoxBytes, &j.Q, bar, col0 + 64, kb * kTileK);
+            load_box(b, Q, bar, col0, k);
+            load_box(b + kMnBoxBytes, Q, bar, col0 + 64, k);
           }
+          ++done;
           if (++s == kStages) {
             s = 0;
             ph ^= 1u;
@@ -520,45 +578,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && leader) {  // the leader's stage barriers count both CTAs' copies: leave none in flight
-        for (int q = 0; q < kStages; ++q)
-          if (armed[q] >= 0) wait_drain(full + q, static_cast<uint32_t>(armed[q]));
+        for (long long q = done > kStages ? done - kStages : 0; q < done; ++q)
+          wait_drain(full0 + 8 * static_cast<uint32_t>(q % kStages), static_cast<uint32_t>(q / kStages) & 1u);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       // ---------------------------------------------------------------- MMA issuer (leader)
-      int s = 0, it = 0;
-      uint32_t ph = 0;
+      uint32_t s = 0, ph = 0;
+      int it = 0;
       bool ok = true;
+      const uint32_t tempty0 = tc::smem_u32(tempty);
       for (int t = pair; ok && t < total; t += npairs, ++it) {
         const int ji = job_of(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of(j, t - B.start[ji]);
         const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
         const uint32_t idesc = tc::idesc_bf16_f32(kTileM, kTileN, amn, bmn);
-        const uint32_t astep = amn ? 2048u : 32u, bstep = bmn ? 2048u : 32u;  // bytes per 16 of the inner length
-        const uint32_t albo = amn ? kMnBoxBytes : 16u, blbo = bmn ? kMnBoxBytes : 16u;
+        // a stage's descriptors differ in the address alone (16-byte units), and so do a stage's steps
+        const uint64_t ad0 = tc::smem_desc_sw128(tc::smem_u32(sA), amn ? kMnBoxBytes : 16u, 1024u);
+        const uint64_t bd0 = tc::smem_desc_sw128(tc::smem_u32(sB), bmn ? kMnBoxBytes : 16u, 1024u);
+        const uint32_t astep = amn ? 128u : 2u, bstep = bmn ? 128u : 2u;
         const int b = it & 1;
         const uint32_t tph = static_cast<uint32_t>(it >> 1) & 1u;
-        if (!tc::mbar_wait(tempty + b, tph ^ 1u, B.err)) {
+        if (!wait(tempty0 + 8 * b, tph ^ 1u, err)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
         const uint32_t d = tmem + static_cast<uint32_t>(b * kTileN);
+        uint32_t accumulate = 0;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!tc::mbar_wait(full + s, ph, B.err)) {
+          if (!wait(full0 + 8 * s, ph, err)) {
             ok = false;
             break;
           }
           tc::fence_after_sync();
-          const uint32_t abase = tc::smem_u32(sA + s * kHalfBytes);
-          const uint32_t bbase = tc::smem_u32(sB + s * kHalfBytes);
+          const uint64_t ad = ad0 + s * (kHalfBytes / 16), bd = bd0 + s * (kHalfBytes / 16);
 #pragma unroll
-          for (int kk = 0; kk < kTileK / 16; ++kk) {
-            const uint64_t ad = tc::smem_desc_sw128(abase + astep * kk, albo, 1024u);
-            const uint64_t bd = tc::smem_desc_sw128(bbase + bstep * kk, blbo, 1024u);
-            tc::umma_bf16_pair(d, ad, bd, idesc, (kb != w.kb0 || kk != 0) ? 1u : 0u);
+          for (uint32_t kk = 0; kk < kTileK / 16; ++kk) {
+            tc::umma_bf16_pair(d, ad + kk * astep, bd + kk * bstep, idesc, accumulate);
+            accumulate = 1;
           }
           tc::umma_commit_pair(empty + s, 3);  // both CTAs' stage s is free
           if (++s == kStages) {
@@ -570,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::umma_commit_pair(tfull + b, 3);  // both CTAs' accumulator b is complete
       }
       tc::umma_commit_pair(drain, 1);
-      wait_drain(drain, 0);
+      wait_drain(tc::smem_u32(drain), 0);
     }
   } else {
     // ------------------------------------------------------------------ epilogue (warps 2..9)
@@ -584,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int b = it & 1;
       const uint32_t tph = static_cast<uint32_t>(it >> 1) & 1u;
       int ok = 1;
-      if (lane == 0) ok = tc::mbar_wait_idle(tfull + b, tph, B.err) ? 1 : 0;
+      if (lane == 0) ok = tc::mbar_wait_idle(tfull + b, tph, err) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
       tc::fence_after_sync();
       const int ji = job_of(B, t);
