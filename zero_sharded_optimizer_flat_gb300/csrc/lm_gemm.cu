@@ -42,61 +42,99 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// True in one lane of a converged warp. The copies and MMAs take their operands from uniform
+// registers: behind this predicate the compiler knows that one thread issues them, behind a
+// comparison of lanes it has to issue them lane by lane (680 against 521 cycles a k-block of 8192^3,
+// whose MMAs take 512).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Row `lane` of a 32 x 32 bf16 box under the 64-byte swizzle: row r at 64 r, its 16-byte piece q at
 // piece q ^ ((r >> 1) & 3).
-__device__ __forceinline__ void box_row(uint8_t* box, int lane, const float (&o)[32]) {
+__device__ __forceinline__ void box_row(uint8_t* box, int lane, const uint32_t (&o)[16]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint4 u;
-    u.x = pack2(o[8 * q + 0], o[8 * q + 1]);
-    u.y = pack2(o[8 * q + 2], o[8 * q + 3]);
-    u.z = pack2(o[8 * q + 4], o[8 * q + 5]);
-    u.w = pack2(o[8 * q + 6], o[8 * q + 7]);
-    *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = u;
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+}
+
+// Where a box of a warp goes when the TMA cannot take it there: `bytes` of each row from the box's
+// byte `skip` on (a multiple of 16), rows `pitch` bytes apart, the first `rows` of the 32.
+struct Rows {
+  uint8_t* base;
+  long long pitch;
+  int bytes, rows, skip;
+};
+
+// Pieces of kPiece bytes of a box's rows to memory, consecutive lanes along a row.
+template <typename Piece>
+__device__ __forceinline__ void rows_out(const uint8_t* box, const Rows& r, int lane) {
+  constexpr int kPiece = sizeof(Piece), kPerRow = 64 / kPiece, kRowsAtOnce = 32 / (kPerRow < 32 ? kPerRow : 32);
+  constexpr int kPasses = kPerRow <= 32 ? 1 : kPerRow / 32;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
+#pragma unroll
+    for (int q = 0; q < kPasses; ++q) {
+      const int row = r0 + (kPerRow < 32 ? lane / kPerRow : 0);
+      const int off = (kPerRow < 32 ? lane % kPerRow : lane + 32 * q) * kPiece;
+      const int in = off + r.skip;
+      if (row < r.rows && off + kPiece <= r.bytes)
+        *reinterpret_cast<Piece*>(r.base + row * r.pitch + off) =
+            *reinterpret_cast<const Piece*>(box + row * 64 + (((in >> 4) ^ ((row >> 1) & 3)) << 4) + (in & 15));
+    }
+  }
+}
+// The widest piece that every row's start and length allow.
+__device__ __forceinline__ void rows_out(const uint8_t* box, const Rows& r, int lane) {
+  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(r.base)) | static_cast<unsigned>(r.pitch) |
+                       static_cast<unsigned>(r.bytes);
+  if ((mis & 15u) == 0) {
+    rows_out<uint4>(box, r, lane);
+  } else if ((mis & 7u) == 0) {
+    rows_out<uint2>(box, r, lane);
+  } else if ((mis & 3u) == 0) {
+    rows_out<uint32_t>(box, r, lane);
+  } else if ((mis & 1u) == 0) {
+    rows_out<uint16_t>(box, r, lane);
+  } else {
+    rows_out<uint8_t>(box, r, lane);
   }
 }
 
-// Hands a warp's output boxes to the TMA in turn: a box is written again only when the store that
-// read it kBoxes stores earlier has finished reading.
+// Hands a warp's output boxes to the TMA (or to the warp's own stores) in turn: a box is written
+// again only when the copy that read it kBoxes boxes earlier has finished reading.
 struct Boxes {
   uint8_t* mine;
   int next;
-  __device__ __forceinline__ void store(const CUtensorMap* m, int lane, const float (&o)[32], int col, int row) {
+  __device__ __forceinline__ uint8_t* open() {
     uint8_t* box = mine + next * kBoxBytes;
-    if (lane == 0) tc::bulk_wait_read<kBoxes - 1>();
+    next = next + 1 == kBoxes ? 0 : next + 1;
+    if (elect_one()) tc::bulk_wait_read<kBoxes - 1>();
     __syncwarp();
-    box_row(box, lane, o);
+    return box;
+  }
+  __device__ __forceinline__ void close(const CUtensorMap* m, uint8_t* box, int col, int row) {
     tc::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
+    if (elect_one()) {
       tc::tma_store_2d(m, box, col, row);
       tc::bulk_commit();
     }
-    next = next + 1 == kBoxes ? 0 : next + 1;
+  }
+  __device__ __forceinline__ void close(const Rows& r, uint8_t* box, int lane) {
+    __syncwarp();
+    rows_out(box, r, lane);
+    if (elect_one()) tc::bulk_commit();  // an empty group, so that open()'s count holds
+    __syncwarp();
   }
 };
-
-// 32 values to a row of bf16 in global memory, columns beyond n left out.
-__device__ __forceinline__ void put_bf16(__nv_bfloat16* p, const float (&o)[32], int n) {
-  if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      reinterpret_cast<uint4*>(p)[q] = make_uint4(pack2(o[8 * q], o[8 * q + 1]), pack2(o[8 * q + 2], o[8 * q + 3]),
-                                                  pack2(o[8 * q + 4], o[8 * q + 5]), pack2(o[8 * q + 6], o[8 * q + 7]));
-  } else {
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (k < n) p[k] = __float2bfloat16_rn(o[k]);
-  }
-}
-
-__device__ __forceinline__ void ld32(uint32_t taddr, float (&o)[32]) {
-  uint32_t v[32];
-  tc::tmem_ld32(taddr, v);
-  tc::tmem_wait_ld();
-#pragma unroll
-  for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]);
-}
 
 // A unit of work: one tile of one job over one run of k-blocks.
 struct Unit {
@@ -121,20 +159,6 @@ __device__ __forceinline__ int job_of(const Batch& b, int t) {
   int j = 0;
   while (j + 1 < b.n && t >= b.start[j + 1]) ++j;
   return j;
-}
-
-// True in one lane of a converged warp. The copies and MMAs take their operands from uniform
-// registers: behind this predicate the compiler knows that one thread issues them, behind a
-// comparison of lanes it has to issue them lane by lane (680 against 521 cycles a k-block of 8192^3, whose MMAs
-// take 512).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
 }
 
 // A bounded wait for an mbarrier (given by its shared-memory address) that costs the two threads
@@ -200,44 +224,66 @@ __device__ __forceinline__ void gate_of(int act, float z, float& a, float& da) {
 
 // ---------------------------------------------------------------------- epilogues
 //
-// Each turns one warp's part of a tile into outputs: TMEM address `acc` (this warp's 32 lanes, the
-// tile's column 0), row = the lane's row of D, row0 = the warp's first, h = which half of the
-// tile's columns.
+// Each turns one warp's part of a tile into outputs: 32 rows from row0 on and half h of the columns,
+// a lane one row. `acc` reads the accumulators and gives them back to the MMAs as soon as the warp
+// has read its last ones, while the arithmetic and the stores on them still run; every epilogue
+// reads all it needs and calls done() once.
+struct Acc {
+  uint32_t base;         // the TMEM address of the warp's lanes, the tile's column 0
+  uint32_t release_bar;  // the leader's barrier of this accumulator
+  int lane;
+  __device__ __forceinline__ void read32(int c, uint32_t (&v)[32]) const {
+    tc::tmem_ld32(base + static_cast<uint32_t>(c), v);
+    tc::tmem_wait_ld();
+  }
+  __device__ __forceinline__ void read64(int c, uint32_t (&v)[2][32]) const {
+    tc::tmem_ld32(base + static_cast<uint32_t>(c), v[0]);
+    tc::tmem_ld32(base + static_cast<uint32_t>(c + 32), v[1]);
+    tc::tmem_wait_ld();
+  }
+  __device__ __forceinline__ void done() const {
+    tc::fence_before_sync();
+    __syncwarp();  // every lane's TMEM reads are done: one arrival releases the warp's part
+    if (lane == 0) tc::mbar_arrive_cluster(release_bar);
+  }
+};
+__device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
 
-__device__ __forceinline__ void epi_store(const Job& j, const Unit& w, uint32_t acc, int row0, int lane, int h,
+__device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
                                           Boxes& boxes) {
   const int row = row0 + lane;
   const float alpha = j.alpha != nullptr && j.splits == 1 ? __ldcg(j.alpha) : 1.0f;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = w.tj * kTileN + 128 * h + 32 * c;
-    if (col >= j.N || row0 >= j.M) break;  // (warp-uniform)
-    float o[32];
-    ld32(acc + static_cast<uint32_t>(128 * h + 32 * c), o);
-    if (j.add != nullptr && row < j.M) {
-      const float* a = j.add + static_cast<long long>(row) * j.ld_add + col;
-      if (col + 32 <= j.N) {
+  for (int half = 0; half < 2; ++half) {
+    uint32_t v[2][32];
+    acc.read64(128 * h + 64 * half, v);
+    if (half == 1) acc.done();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 v = reinterpret_cast<const float4*>(a)[q];
-          o[4 * q] += v.x, o[4 * q + 1] += v.y, o[4 * q + 2] += v.z, o[4 * q + 3] += v.w;
+    for (int c = 0; c < 2; ++c) {
+      const int col = w.tj * kTileN + 128 * h + 64 * half + 32 * c;
+      if (col >= j.N || row0 >= j.M) continue;  // (warp-uniform)
+      float o[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = f(v[c][k]);
+      if (j.add != nullptr && row < j.M) {
+        const float* a = j.add + static_cast<long long>(row) * j.ld_add + col;
+        if (col + 32 <= j.N) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 x = reinterpret_cast<const float4*>(a)[q];
+            o[4 * q] += x.x, o[4 * q + 1] += x.y, o[4 * q + 2] += x.z, o[4 * q + 3] += x.w;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (col + k < j.N) o[k] += a[k];
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (col + k < j.N) o[k] += a[k];
       }
-    }
 #pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] *= alpha;
-    if (j.out_mode == kOutTma) {
-      boxes.store(&j.D0, lane, o, col, row0);
-    } else if (row < j.M) {
-      const long long off = static_cast<long long>(row) * j.ld_out + col;
-      if (j.out_mode == kOutBf16) {
-        put_bf16(static_cast<__nv_bfloat16*>(j.out) + off, o, j.N - col);
-      } else {
-        float* p = static_cast<float*>(j.out) + w.split * j.split_stride + off;
+      for (int k = 0; k < 32; ++k) o[k] *= alpha;
+      if (j.out_mode == kOutF32) {
+        if (row >= j.M) continue;
+        float* p = static_cast<float*>(j.out) + w.split * j.split_stride + static_cast<long long>(row) * j.ld_out + col;
         if (col + 32 <= j.N) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -247,48 +293,69 @@ __device__ __forceinline__ void epi_store(const Job& j, const Unit& w, uint32_t 
           for (int k = 0; k < 32; ++k)
             if (col + k < j.N) p[k] = o[k];
         }
+        continue;
+      }
+      uint32_t words[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) words[k] = pack2(o[2 * k], o[2 * k + 1]);
+      uint8_t* box = boxes.open();
+      box_row(box, lane, words);
+      if (j.out_mode == kOutTma) {
+        boxes.close(&j.D0, box, col, row0);
+      } else {
+        uint16_t* p = static_cast<uint16_t*>(j.out) + static_cast<long long>(row0) * j.ld_out + col;
+        boxes.close(Rows{reinterpret_cast<uint8_t*>(p), j.ld_out * 2, min(32, j.N - col) * 2, min(32, j.M - row0), 0}, box,
+                    lane);
       }
     }
   }
 }
 
-// The running maximum m and sum s = sum 2^(x - m) of the row's 128 logits times log2(e), one pass.
-// Columns beyond the vocabulary take no part; an all -inf row keeps m = -inf, s = 0.
-__device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, uint32_t acc, int row0, int lane, int h) {
+// The maximum m and the sum s = sum 2^(x - m) of the row's 128 logits times log2(e), 64 at a time.
+// Columns beyond the vocabulary take no part; where all logits are -inf, m = -inf and s = 0.
+__device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h) {
   const int row = row0 + lane;
-  if (row0 >= j.M) return;
   const long long tgt = row < j.M ? j.target[row] : -1;
   float m = -INFINITY, s = 0.0f;
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = w.tj * kTileN + 128 * h + 32 * c;
-    if (col >= j.N) break;
-    float o[32];
-    ld32(acc + static_cast<uint32_t>(128 * h + 32 * c), o);
-    if (tgt >= col && tgt < col + 32 && tgt < j.N) {
+  for (int half = 0; half < 2; ++half) {
+    uint32_t v[2][32];
+    acc.read64(128 * h + 64 * half, v);
+    if (half == 1) acc.done();
+    const int col = w.tj * kTileN + 128 * h + 64 * half;
+    if (tgt >= col && tgt < col + 64 && tgt < j.N) {
       float t = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (col + k == tgt) t = o[k];
+      for (int k = 0; k < 64; ++k)
+        if (col + k == tgt) t = f(v[k >> 5][k & 31]);
       j.tlogit[row] = t;
     }
-    if (col + 32 > j.N) {
+    if (col + 64 > j.N) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (col + k >= j.N) o[k] = -INFINITY;
+      for (int k = 0; k < 64; ++k)
+        if (col + k >= j.N) v[k >> 5][k & 31] = 0xFF800000u;
     }
-    float top = -INFINITY;
+    float top[8];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) top = fmaxf(top, o[k]);
-    const float mn = fmaxf(m, top * kLog2e);
+    for (int i = 0; i < 8; ++i) top[i] = f(v[0][i]);
+#pragma unroll
+    for (int k = 8; k < 64; ++k) top[k & 7] = fmaxf(top[k & 7], f(v[k >> 5][k & 31]));
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < d; ++i) top[i] = fmaxf(top[i], top[i + d]);
+    const float mn = fmaxf(m, top[0] * kLog2e);
     const float base = mn == -INFINITY ? 0.0f : mn;
-    float t0 = 0.0f, t1 = 0.0f;
+    float part[8];
 #pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      t0 += ex2(fmaf(o[k], kLog2e, -base));
-      t1 += ex2(fmaf(o[k + 1], kLog2e, -base));
-    }
-    s = fmaf(s, ex2(m - base), t0 + t1);
+    for (int i = 0; i < 8; ++i) part[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 64; ++k) part[k & 7] += ex2(fmaf(f(v[k >> 5][k & 31]), kLog2e, -base));
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < d; ++i) part[i] += part[i + d];
+    s = fmaf(s, ex2(m - base), part[0]);
     m = mn;
   }
   if (row < j.M) j.part[static_cast<long long>(2 * w.tj + h) * j.M + row] = make_float2(m, s);
@@ -301,10 +368,9 @@ __device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, uint32_t
 // a row's norm, is p - 1, close to a bf16 value for a small p; times 1 / n it would carry one and the
 // same rounding error, up to 2^-8, into every row (8192 x 2048 x 32000: gradients 2.8e-3 off in
 // 64 bits' norm without the unit).
-__device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, uint32_t acc, int row0, int lane, int h,
+__device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
                                            Boxes& boxes) {
   const int row = row0 + lane;
-  if (row0 >= j.M) return;
   long long tgt = j.ignore;
   float lse2 = 0.0f, dl = 0.0f;
   if (row < j.M) {
@@ -317,164 +383,227 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, uint32_t
   const bool live = tgt != j.ignore;
   const long long at = tgt - j.col0;  // the target's column in this job
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = w.tj * kTileN + 128 * h + 32 * c;
-    if (col >= j.N) break;
-    float o[32];
-    ld32(acc + static_cast<uint32_t>(128 * h + 32 * c), o);
+  for (int half = 0; half < 2; ++half) {
+    uint32_t v[2][32];
+    acc.read64(128 * h + 64 * half, v);
+    if (half == 1) acc.done();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] = ex2(fmaf(o[k], kLog2e, -lse2));
-    if (at >= col && at < col + 32) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (col + k == at) o[k] -= 1.0f;
-    }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) o[k] = live ? o[k] * dl : 0.0f;
-    boxes.store(&j.D0, lane, o, col, row0);
-  }
-}
-
-// TMEM columns 0 .. 127 hold the gate, 128 .. 255 the up product of the same 128 hidden columns.
-// Warp half h makes h's columns 64 h .. 64 h + 63 and, where 8 bits are kept, the whole block of
-// the gate (half 0) or of up (half 1): a tile is one block wide, so a block's largest magnitude is
-// found within a lane.
-__device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, uint32_t acc, int row0, int lane, int h,
-                                            Boxes& boxes) {
-  const int row = row0 + lane;
-  if (row0 >= j.M) return;
-  const int n0 = w.tj * 128;
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    const int off = 64 * h + 32 * c, col = n0 + off;
-    if (col >= j.N) break;
-    float g[32], u[32];
-    ld32(acc + static_cast<uint32_t>(off), g);
-    ld32(acc + static_cast<uint32_t>(128 + off), u);
-    if (j.kept_mode == kKeepTma) {
-      boxes.store(&j.D1, lane, g, col, row0);
-      boxes.store(&j.D2, lane, u, col, row0);
-    } else if (j.kept_mode == kKeepBf16 && row < j.M) {
-      __nv_bfloat16* p = static_cast<__nv_bfloat16*>(j.kept) + static_cast<long long>(row) * j.ld_kept + col;
-      put_bf16(p, g, j.hidden - col);
-      put_bf16(p + j.hidden, u, j.hidden - col);
-    }
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      float a, da;
-      gate_of(j.act, g[k], a, da);
-      u[k] *= a;
-    }
-    boxes.store(&j.D0, lane, u, col, row0);
-  }
-  if (j.kept_mode == kKeep8) {
-    const int width = min(128, j.hidden - n0);
-    float amax = 0.0f;
-#pragma unroll 1
-    for (int c = 0; 32 * c < width; ++c) {
+    for (int c = 0; c < 2; ++c) {
+      const int col = w.tj * kTileN + 128 * h + 64 * half + 32 * c;
+      if (col >= j.N || row0 >= j.M) continue;
       float o[32];
-      ld32(acc + static_cast<uint32_t>(128 * h + 32 * c), o);
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (32 * c + k < width) amax = act8::amax_step(amax, o[k]);
-    }
-    const uint32_t e = act8::exponent_byte(amax);
-    const float inv = act8::inv_scale(e);
-    const long long nb = act8::blocks_of(j.hidden);
-    if (row < j.M) j.kept_scale[static_cast<long long>(row) * 2 * nb + h * nb + w.tj] = static_cast<uint8_t>(e);
-    uint8_t* p = static_cast<uint8_t*>(j.kept) + static_cast<long long>(row) * j.ld_kept + static_cast<long long>(h) * j.hidden + n0;
-#pragma unroll 1
-    for (int c = 0; 32 * c < width; ++c) {
-      float o[32];
-      ld32(acc + static_cast<uint32_t>(128 * h + 32 * c), o);
-      if (row >= j.M) continue;
-      uint32_t v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = act8::encode4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3], inv);
-      uint8_t* d = p + 32 * c;
-      if (32 * c + 32 <= width && (reinterpret_cast<uintptr_t>(d) & 15u) == 0) {
-        reinterpret_cast<uint4*>(d)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4*>(d)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-      } else {
+      for (int k = 0; k < 32; ++k) o[k] = ex2(fmaf(f(v[c][k]), kLog2e, -lse2));
+      if (at >= col && at < col + 32) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          if (32 * c + k < width) d[k] = static_cast<uint8_t>(v[k >> 2] >> (8 * (k & 3)));
+          if (col + k == at) o[k] -= 1.0f;
       }
+      uint32_t words[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) words[k] = live ? pack2(o[2 * k] * dl, o[2 * k + 1] * dl) : 0u;
+      uint8_t* box = boxes.open();
+      box_row(box, lane, words);
+      boxes.close(&j.D0, box, col, row0);
     }
   }
 }
 
-// 32 kept values of one row (zero beyond n columns).
-__device__ __forceinline__ void kept32(const Job& j, long long row, int col, int part, int n, float (&o)[32]) {
+// TMEM columns 0 .. 127 hold the gate, 128 .. 255 the up product of the same 128 hidden columns; the
+// warp's are 64 h .. 64 h + 63 of each. A tile is one 8-bit block wide: a block's largest magnitude
+// is found within a lane and its partner in the warp that has the other half, through `swap` (two
+// bytes a lane; the two warps share barrier `bar`).
+__device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
+                                            Boxes& boxes, uint16_t* swap, int bar) {
+  const int row = row0 + lane, n0 = w.tj * 128, rows = min(32, j.M - row0);
+  if (row0 >= j.M) {  // (the partner warp has the same rows)
+    acc.done();
+    return;
+  }
+  float inv[2] = {1.0f, 1.0f};
   if (j.kept_mode == kKeep8) {
-    const uint8_t* p = static_cast<const uint8_t*>(j.kept) + row * j.ld_kept + static_cast<long long>(part) * j.hidden + col;
-    const long long nb = act8::blocks_of(j.hidden);
-    const float sc = act8::scale(j.kept_scale[row * 2 * nb + part * nb + (col >> 7)]);
-    uint32_t v[8];
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
+    uint32_t e[2];
+    uint32_t v[2][32];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        v[q] = 0;
+    for (int part = 0; part < 2; ++part) {
+      acc.read64(128 * part + 64 * h, v);
+      float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int n = j.hidden - n0 - 64 * h;
+      if (n >= 64) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (4 * q + t < n) v[q] |= static_cast<uint32_t>(p[4 * q + t]) << (8 * t);
+        for (int k = 0; k < 64; ++k) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (k < n) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
       }
+      e[part] = act8::exponent_byte(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
     }
+    swap[32 * h + lane] = static_cast<uint16_t>(e[0] | (e[1] << 8));
+    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+    const uint32_t other = swap[32 * (1 - h) + lane];
+    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // read before the next tile's are written
+    e[0] = max(e[0], other & 255u), e[1] = max(e[1], other >> 8);  // the byte grows with the magnitude
+    const long long nb = act8::blocks_of(j.hidden);
+    if (row < j.M)
+      j.kept_scale[static_cast<long long>(row) * 2 * nb + h * nb + w.tj] = static_cast<uint8_t>(h == 0 ? e[0] : e[1]);
+    inv[0] = act8::inv_scale(e[0]), inv[1] = act8::inv_scale(e[1]);
+  }
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int col = n0 + 64 * h + 32 * c;
+    uint32_t g[32], u[32];
+    tc::tmem_ld32(acc.base + static_cast<uint32_t>(64 * h + 32 * c), g);
+    tc::tmem_ld32(acc.base + static_cast<uint32_t>(128 + 64 * h + 32 * c), u);
+    tc::tmem_wait_ld();
+    if (c == 1) acc.done();
+    if (col >= j.N) continue;
+    if (j.kept_mode == kKeepTma || j.kept_mode == kKeepBf16) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const float2 f = act8::decode2(v[q >> 1] >> (16 * (q & 1)), sc);
-      o[2 * q] = f.x;
-      o[2 * q + 1] = f.y;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(j.kept) + row * j.ld_kept + static_cast<long long>(part) * j.hidden + col;
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      for (int part = 0; part < 2; ++part) {
+        const uint32_t(&x)[32] = part == 0 ? g : u;
+        uint32_t words[16];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + q);
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          o[8 * q + 2 * t] = __uint_as_float(x[t] << 16);
-          o[8 * q + 2 * t + 1] = __uint_as_float(x[t] & 0xFFFF0000u);
+        for (int k = 0; k < 16; ++k) words[k] = pack2(f(x[2 * k]), f(x[2 * k + 1]));
+        uint8_t* box = boxes.open();
+        box_row(box, lane, words);
+        if (j.kept_mode == kKeepTma) {
+          boxes.close(part == 0 ? &j.D1 : &j.D2, box, col, row0);
+        } else {
+          uint16_t* p = static_cast<uint16_t*>(j.kept) + static_cast<long long>(row0) * j.ld_kept + static_cast<long long>(part) * j.hidden + col;
+          boxes.close(Rows{reinterpret_cast<uint8_t*>(p), j.ld_kept * 2, min(32, j.hidden - col) * 2, rows, 0}, box, lane);
         }
       }
-    } else {
+    } else if (j.kept_mode == kKeep8) {  // one box: a row's 32 gate bytes, then its 32 up bytes
+      uint32_t words[16];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = k < n ? __bfloat162float(p[k]) : 0.0f;
+      for (int q = 0; q < 8; ++q) {
+        words[q] = act8::encode4(f(g[4 * q]), f(g[4 * q + 1]), f(g[4 * q + 2]), f(g[4 * q + 3]), inv[0]);
+        words[8 + q] = act8::encode4(f(u[4 * q]), f(u[4 * q + 1]), f(u[4 * q + 2]), f(u[4 * q + 3]), inv[1]);
+      }
+      uint8_t* box = boxes.open();
+      box_row(box, lane, words);
+      uint8_t* p = static_cast<uint8_t*>(j.kept) + static_cast<long long>(row0) * j.ld_kept + col;
+      const int n = min(32, j.hidden - col);
+      __syncwarp();
+      rows_out(box, Rows{p, j.ld_kept, n, rows, 0}, lane);
+      boxes.close(Rows{p + j.hidden, j.ld_kept, n, rows, 32}, box, lane);
+    }
+    uint32_t words[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float a0, a1, da;
+      gate_of(j.act, f(g[2 * k]), a0, da);
+      gate_of(j.act, f(g[2 * k + 1]), a1, da);
+      words[k] = pack2(a0 * f(u[2 * k]), a1 * f(u[2 * k + 1]));
+    }
+    uint8_t* box = boxes.open();
+    box_row(box, lane, words);
+    boxes.close(&j.D0, box, col, row0);
+  }
+}
+
+// The words of 32 kept columns of one row and part as they lie in memory (bf16: 16 words, 8 bits: 8),
+// zero beyond n columns, by the widest loads that the row's start allows.
+template <int kWords, typename Piece>
+__device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t (&x)[kWords]) {
+  constexpr int kPiece = sizeof(Piece);
+#pragma unroll
+  for (int i = 0; i < 4 * kWords / kPiece; ++i) {
+    Piece v{};
+    if ((i + 1) * kPiece <= bytes) v = __ldg(reinterpret_cast<const Piece*>(p) + i);
+    if constexpr (kPiece == 16) {
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    } else if constexpr (kPiece == 8) {
+      x[2 * i] = v.x, x[2 * i + 1] = v.y;
+    } else if constexpr (kPiece == 4) {
+      x[i] = v;
+    } else {
+      const int shift = 8 * (i * kPiece & 3);
+      x[i * kPiece / 4] = (shift == 0 ? 0u : x[i * kPiece / 4]) | (static_cast<uint32_t>(v) << shift);
     }
   }
+}
+template <int kWords>
+__device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t (&x)[kWords]) {
+  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) | static_cast<unsigned>(bytes);
+  if ((mis & 15u) == 0) {
+    words_in<kWords, uint4>(p, bytes, x);
+  } else if ((mis & 3u) == 0) {
+    words_in<kWords, uint32_t>(p, bytes, x);
+  } else if ((mis & 1u) == 0) {
+    words_in<kWords, uint16_t>(p, bytes, x);
+  } else {
+    words_in<kWords, uint8_t>(p, bytes, x);
+  }
+}
+
+// What gate and up of 32 columns are read as, and their values.
+struct Kept {
+  uint32_t x[2][16];
+  float sc[2];
+};
+__device__ __forceinline__ void kept_load(const Job& j, int row, int col, Kept& k) {
+  const bool in = row < j.M && col < j.hidden;
+  const int n = in ? min(32, j.hidden - col) : 0;
+  const long long off = in ? static_cast<long long>(row) * j.ld_kept + col : 0;
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    const long long at = off + (in ? static_cast<long long>(part) * j.hidden : 0);
+    if (j.kept_mode == kKeep8) {
+      const long long nb = act8::blocks_of(j.hidden);
+      uint32_t w8[8];
+      words_in<8>(static_cast<const uint8_t*>(j.kept) + at, n, w8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) k.x[part][i] = w8[i];
+      k.sc[part] = in ? act8::scale(j.kept_scale[static_cast<long long>(row) * 2 * nb + part * nb + (col >> 7)]) : 1.0f;
+    } else {
+      words_in<16>(static_cast<const uint8_t*>(j.kept) + 2 * at, 2 * n, k.x[part]);
+    }
+  }
+}
+// Values 2 q and 2 q + 1 of a part.
+__device__ __forceinline__ float2 kept_two(bool eight, const Kept& k, int part, int q) {
+  if (eight) return act8::decode2(k.x[part][q >> 1] >> (16 * (q & 1)), k.sc[part]);
+  return make_float2(__uint_as_float(k.x[part][q] << 16), __uint_as_float(k.x[part][q] & 0xFFFF0000u));
 }
 
 // dgate = dh up a'(gate), dup = dh a(gate), h = a(gate) up, each rounded to bf16 once: they are
-// operands of the three products that follow.
-__device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, uint32_t acc, int row0, int lane, int h,
-                                            Boxes& boxes) {
+// operands of the three products that follow. `k` holds the kept values of the first 32 columns,
+// read while the tile's products ran; each later 32 are read while the ones before are worked on.
+__device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
+                                            Boxes& boxes, Kept& k) {
   const int row = row0 + lane;
-  if (row0 >= j.M) return;
+  const bool eight = j.kept_mode == kKeep8;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const int col = w.tj * kTileN + 128 * h + 32 * c;
-    if (col >= j.N) break;
-    float g[32], u[32], d[32];
-    const int n = row < j.M ? j.hidden - col : 0;
-    kept32(j, row < j.M ? row : 0, col < j.hidden ? col : 0, 0, n, g);
-    kept32(j, row < j.M ? row : 0, col < j.hidden ? col : 0, 1, n, u);
-    ld32(acc + static_cast<uint32_t>(128 * h + 32 * c), d);
+    uint32_t v[32];
+    acc.read32(128 * h + 32 * c, v);
+    if (c == 3) acc.done();
+    if (col >= j.N || row0 >= j.M) continue;
+    uint32_t dg[16], du[16], hh[16];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      float a, da;
-      gate_of(j.act, g[k], a, da);
-      g[k] = d[k] * u[k] * da;
-      d[k] *= a;
-      u[k] *= a;
+    for (int q = 0; q < 16; ++q) {
+      const float2 g = kept_two(eight, k, 0, q), u = kept_two(eight, k, 1, q);
+      float a0, a1, da0, da1;
+      gate_of(j.act, g.x, a0, da0);
+      gate_of(j.act, g.y, a1, da1);
+      const float d0 = f(v[2 * q]), d1 = f(v[2 * q + 1]);
+      dg[q] = pack2(d0 * u.x * da0, d1 * u.y * da1);
+      du[q] = pack2(d0 * a0, d1 * a1);
+      hh[q] = pack2(a0 * u.x, a1 * u.y);
     }
-    boxes.store(&j.D0, lane, g, col, row0);
-    boxes.store(&j.D1, lane, d, col, row0);
-    boxes.store(&j.D2, lane, u, col, row0);
+    if (c < 3) kept_load(j, row, col + 32, k);
+    uint8_t* box = boxes.open();
+    box_row(box, lane, dg);
+    boxes.close(&j.D0, box, col, row0);
+    box = boxes.open();
+    box_row(box, lane, du);
+    boxes.close(&j.D1, box, col, row0);
+    box = boxes.open();
+    box_row(box, lane, hh);
+    boxes.close(&j.D2, box, col, row0);
   }
 }
 
@@ -488,7 +617,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kHalfBytes;
   uint8_t* sEpi = sB + kStages * kHalfBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + kEpiWarps * kBoxes * kBoxBytes);
+  uint16_t* sSwap = reinterpret_cast<uint16_t*>(sEpi + kEpiWarps * kBoxes * kBoxBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sSwap) + kSwapBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
@@ -639,29 +769,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tempty_leader[2] = {tc::map_to_rank(tc::smem_u32(tempty), 0),
                                        tc::map_to_rank(tc::smem_u32(tempty + 1), 0)};
     Boxes boxes{sEpi + (warp - 2) * kBoxes * kBoxBytes, 0};
+    uint16_t* swap = sSwap + 64 * quad;
+    const int rows0 = static_cast<int>(rank) * 128 + 32 * quad;  // this warp's rows within a tile
     int it = 0;
     for (int t = pair; t < total; t += npairs, ++it) {
       const int b = it & 1;
       const uint32_t tph = static_cast<uint32_t>(it >> 1) & 1u;
+      const int ji = job_of(B, t);
+      const Job& j = B.job[ji];
+      const Unit w = unit_of(j, t - B.start[ji]);
+      const int row0 = w.ti * kTileM + rows0;
+      Kept kept;
+      if constexpr ((kKinds & kGluBwd) != 0) kept_load(j, row0 + lane, w.tj * kTileN + 128 * half, kept);
       int ok = 1;
       if (lane == 0) ok = tc::mbar_wait_idle(tfull + b, tph, err) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
       tc::fence_after_sync();
-      const int ji = job_of(B, t);
-      const Job& j = B.job[ji];
-      const Unit w = unit_of(j, t - B.start[ji]);
-      const uint32_t acc = tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN);
-      const int row0 = w.ti * kTileM + static_cast<int>(rank) * 128 + 32 * quad;
+      const Acc acc{tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN), tempty_leader[b], lane};
       if ((kKinds & kStore) && j.kind == kStore) epi_store(j, w, acc, row0, lane, half, boxes);
       if ((kKinds & kCeFwd) && j.kind == kCeFwd) epi_ce_fwd(j, w, acc, row0, lane, half);
       if ((kKinds & kCeBwd) && j.kind == kCeBwd) epi_ce_bwd(j, w, acc, row0, lane, half, boxes);
-      if ((kKinds & kGluFwd) && j.kind == kGluFwd) epi_glu_fwd(j, w, acc, row0, lane, half, boxes);
-      if ((kKinds & kGluBwd) && j.kind == kGluBwd) epi_glu_bwd(j, w, acc, row0, lane, half, boxes);
-      tc::fence_before_sync();
-      __syncwarp();  // every lane's TMEM reads are done: one arrival releases the warp's part
-      if (lane == 0) tc::mbar_arrive_cluster(tempty_leader[b]);
+      if constexpr ((kKinds & kGluFwd) != 0) epi_glu_fwd(j, w, acc, row0, lane, half, boxes, swap, 1 + quad);
+      if constexpr ((kKinds & kGluBwd) != 0) epi_glu_bwd(j, w, acc, row0, lane, half, boxes, kept);
     }
-    if (lane == 0) tc::bulk_wait_all();  // every store has reached global memory
+    if (elect_one()) tc::bulk_wait_all();  // every store has reached global memory
     __syncwarp();
   }
   tc::fence_before_sync();

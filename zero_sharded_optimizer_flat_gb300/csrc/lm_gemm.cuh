@@ -27,7 +27,8 @@ constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
 constexpr int kBoxBytes = 32 * 32 * 2;
 constexpr int kBoxes = 2;  // output boxes per epilogue warp
-constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxes * kBoxBytes + 1024 + 256;
+constexpr int kSwapBytes = 4 * 64 * 2;  // kGluFwd: two warps' block exponents for each quarter of the rows
+constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxes * kBoxBytes + kSwapBytes + 1024 + 256;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr int kMaxJobs = 5;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -44,7 +45,7 @@ enum Kind : int {
 enum OutMode : int { kOutTma = 0, kOutBf16 = 1, kOutF32 = 2 };          // kStore: through D0, or row stores
 enum KeptMode : int { kKeepNone = 0, kKeepTma = 1, kKeepBf16 = 2, kKeep8 = 3 };  // kGluFwd, kGluBwd
 
-struct alignas(64) Job {
+struct Job {
   CUtensorMap P, Q, D0, D1, D2;
   int kind;
   int M, N, K;
