@@ -88,8 +88,8 @@ __global__ void __launch_bounds__(256) act8_kernel(const Args a) {
       uint32_t o[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float2 f = decode2(w[t >> 1] >> (16 * (t & 1)), sc);
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        const float2 f = decode2(w[t >> 1] >> (16 * (t & 1)));
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * sc, f.y * sc);
         o[t] = *reinterpret_cast<const uint32_t*>(&h);
       }
       if (n == 8 && a.vec) {

@@ -49,10 +49,10 @@ __device__ __forceinline__ uint32_t encode2(float a, float b, float inv) {
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
   return encode2(a, b, inv) | (encode2(c, d, inv) << 16);
 }
-__device__ __forceinline__ float2 decode2(uint32_t two, float sc) {
+// Two stored bytes' e4m3 values (without the block's power).
+__device__ __forceinline__ float2 decode2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return make_float2(f.x * sc, f.y * sc);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 }  // namespace act8

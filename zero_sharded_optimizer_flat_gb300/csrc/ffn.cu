@@ -219,7 +219,7 @@ void glu_fields(Job& j, const zopt_ffn_job& c) {
 }
 
 // Where a kStore job's result goes: its partial sums' slab, or the caller's matrix.
-zopt_status finish(const char* fn, Job& j, uint16_t* out, long long ld, float*& slab, SumBatch& sums) {
+void finish(Job& j, uint16_t* out, long long ld, float*& slab, SumBatch& sums) {
   if (j.splits > 1) {
     j.out_mode = kOutF32;
     j.out = slab;
@@ -230,16 +230,11 @@ zopt_status finish(const char* fn, Job& j, uint16_t* out, long long ld, float*& 
     sums.start[sums.n + 1] = sums.start[sums.n] + q.M * (q.pitch / 4);
     ++sums.n;
     slab += round_up(split_elems(j), 256);
-    return ok();
-  }
-  if (tma_out_ok(out, j.N, ld)) {
-    j.out_mode = kOutTma;
-    return map_output(fn, &j.D0, out, j.M, j.N, ld);
+    return;
   }
   j.out_mode = kOutBf16;
   j.out = out;
   j.ld_out = ld;
-  return ok();
 }
 
 zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStream_t s) {
@@ -267,12 +262,8 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
     glu_fields(j, c);
     TRY(map_operand(fn, &j.P, in.x, c.tokens, c.dim, in.px, false));
     TRY(map_operand(fn, &j.Q, in.gate_up, in.up + c.hidden, c.dim, in.pgu, true));
-    TRY(map_output(fn, &j.D0, h, c.tokens, c.hidden, p.fp));
-    if (j.kept_mode == kKeepBf16 && tma_out_ok(c.kept, c.hidden, c.ld_kept)) {
-      j.kept_mode = kKeepTma;
-      TRY(map_output(fn, &j.D1, c.kept, c.tokens, c.hidden, c.ld_kept));
-      TRY(map_output(fn, &j.D2, c.kept + c.hidden, c.tokens, c.hidden, c.ld_kept));
-    }
+    j.out = h;
+    j.ld_out = p.fp;
     TRY(launch(fn, b, kGluFwd, s));
   }
   Batch b{};
@@ -284,7 +275,7 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
   TRY(map_operand(fn, &b.job[0].Q, in.down, c.dim, c.hidden, in.pdown, true));
   SumBatch sums{};
   float* slab = reinterpret_cast<float*>(ws + p.slab);
-  TRY(finish(fn, b.job[0], c.y, c.ld_y, slab, sums));
+  finish(b.job[0], c.y, c.ld_y, slab, sums);
   TRY(launch(fn, b, kStore, s));
   return sums.n > 0 ? launch_sums(fn, sums, s) : ok();
 }
@@ -319,9 +310,9 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
     glu_fields(j, c);
     TRY(map_operand(fn, &j.P, in.dy, c.tokens, c.dim, in.pdy, false));
     TRY(map_operand(fn, &j.Q, in.down, c.hidden, c.dim, in.pdown, false));
-    TRY(map_output(fn, &j.D0, dgu, c.tokens, p.fp, 2 * p.fp));
-    TRY(map_output(fn, &j.D1, dgu + p.fp, c.tokens, p.fp, 2 * p.fp));
-    TRY(map_output(fn, &j.D2, h, c.tokens, p.fp, p.fp));
+    j.out = dgu;
+    j.ld_out = 2 * p.fp;
+    j.out_h = h;
     TRY(launch(fn, b, kGluBwd, s));
   }
   Batch b{};
@@ -333,16 +324,16 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
   float* slab = reinterpret_cast<float*>(ws + p.slab);
   TRY(map_operand(fn, &jobs[0].P, dgu, c.tokens, 2 * p.fp, 2 * p.fp, false));
   TRY(map_operand(fn, &jobs[0].Q, in.gate_up, c.dim, 2 * p.fp, in.pgu, false));
-  TRY(finish(fn, jobs[0], c.dx, c.ld_dx, slab, sums));
+  finish(jobs[0], c.dx, c.ld_dx, slab, sums);
   for (int k = 1; k + 1 < n; ++k) {  // the gate's and up's columns together, or apart
     const int up = k - 1;
     TRY(map_operand(fn, &jobs[k].P, in.x, c.dim, c.tokens, in.px, true));
     TRY(map_operand(fn, &jobs[k].Q, dgu + up * p.fp, jobs[k].N, c.tokens, 2 * p.fp, true));
-    TRY(finish(fn, jobs[k], c.dw_gate_up + up * c.hidden, c.ld_dw_gate_up, slab, sums));
+    finish(jobs[k], c.dw_gate_up + up * c.hidden, c.ld_dw_gate_up, slab, sums);
   }
   TRY(map_operand(fn, &jobs[n - 1].P, h, c.hidden, c.tokens, p.fp, true));
   TRY(map_operand(fn, &jobs[n - 1].Q, in.dy, c.dim, c.tokens, in.pdy, true));
-  TRY(finish(fn, jobs[n - 1], c.dw_down, c.ld_dw_down, slab, sums));
+  finish(jobs[n - 1], c.dw_down, c.ld_dw_down, slab, sums);
   // The longest units first: the launch's end is then made of short ones.
   const bool dx_first = jobs[0].kb_per_split >= jobs[1].kb_per_split;
   b.n = n;

@@ -311,7 +311,9 @@ zopt_status backward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, 
     j.unit = unit;
     TRY(map_operand(fn, &j.P, x, c.tokens, c.dim, px, false));
     TRY(map_operand(fn, &j.Q, w + v0 * pw, vc, c.dim, pw, false));
-    return map_output(fn, &j.D0, dl_of(i), c.tokens, vc, p.piece);
+    j.out = dl_of(i);
+    j.ld_out = p.piece;
+    return ok();
   };
   {
     Batch b{};
@@ -372,9 +374,6 @@ zopt_status backward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, 
         j.out_mode = kOutF32;
         j.out = acc;
         j.ld_out = acc_pitch;
-      } else if (tma_out_ok(out, j.N, ld)) {
-        j.out_mode = kOutTma;
-        TRY(map_output(fn, &j.D0, out, j.M, j.N, ld));
       } else {
         j.out_mode = kOutBf16;
         j.out = out;

@@ -37,9 +37,48 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two fp32 operations an instruction: the epilogues are bound by the instructions they issue.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(F2 a) {
+  const float2 x = f2(a);
+  return pack2(x.x, x.y);
 }
 
 // True in one lane of a converged warp. The copies and MMAs take their operands from uniform
@@ -56,83 +95,99 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Row `lane` of a 32 x 32 bf16 box under the 64-byte swizzle: row r at 64 r, its 16-byte piece q at
-// piece q ^ ((r >> 1) & 3).
-__device__ __forceinline__ void box_row(uint8_t* box, int lane, const uint32_t (&o)[16]) {
+// ---------------------------------------------------------------------- results to memory
+//
+// A warp's results are 32 rows, one lane each; memory wants consecutive lanes along a row. So a lane
+// writes its row (128 bytes) into the warp's 4 KiB box and the warp stores the box row by row. The
+// box's 16-byte piece q of row r lies at piece q ^ (r & 7): neither side meets a bank twice. (Boxes
+// handed to the TMA instead waited behind the operands' loads in its queue: 6000 cycles for a tile
+// of bf16 results.)
+__device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int q) {
+  return box + static_cast<uint32_t>(row * 128 + ((q ^ (row & 7)) << 4));
+}
+// Pieces q0 .. of the lane's row. (box is a multiple of 128.)
+template <int kWords>
+__device__ __forceinline__ void box_put(uint32_t box, int lane, int q0, const uint32_t (&o)[kWords]) {
+  const uint32_t at = box_piece(box, lane, 0);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint4*>(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+  for (int q = 0; q < kWords / 4; ++q)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ static_cast<uint32_t>((q0 + q) << 4)), "r"(o[4 * q]),
+                 "r"(o[4 * q + 1]), "r"(o[4 * q + 2]), "r"(o[4 * q + 3])
+                 : "memory");
 }
 
-// Where a box of a warp goes when the TMA cannot take it there: `bytes` of each row from the box's
-// byte `skip` on (a multiple of 16), rows `pitch` bytes apart, the first `rows` of the 32.
-struct Rows {
-  uint8_t* base;
-  long long pitch;
-  int bytes, rows, skip;
-};
-
-// Pieces of kPiece bytes of a box's rows to memory, consecutive lanes along a row.
-template <typename Piece>
-__device__ __forceinline__ void rows_out(const uint8_t* box, const Rows& r, int lane) {
-  constexpr int kPiece = sizeof(Piece), kPerRow = 64 / kPiece, kRowsAtOnce = 32 / (kPerRow < 32 ? kPerRow : 32);
-  constexpr int kPasses = kPerRow <= 32 ? 1 : kPerRow / 32;
-#pragma unroll 4
-  for (int r0 = 0; r0 < 32; r0 += kRowsAtOnce) {
+// Pieces of kPiece bytes, for rows whose start or length is not a multiple of 16 bytes.
+template <typename Piece, int kBytes>
+__device__ __noinline__ void rows_out_odd(uint32_t box, uint8_t* base, long long pitch, int bytes, int rows, int skip, int lane) {
+  constexpr int kPiece = sizeof(Piece), kAll = kBytes / kPiece, kPerRow = kAll < 32 ? kAll : 32, kAtOnce = 32 / kPerRow;
 #pragma unroll
-    for (int q = 0; q < kPasses; ++q) {
-      const int row = r0 + (kPerRow < 32 ? lane / kPerRow : 0);
-      const int off = (kPerRow < 32 ? lane % kPerRow : lane + 32 * q) * kPiece;
-      const int in = off + r.skip;
-      if (row < r.rows && off + kPiece <= r.bytes)
-        *reinterpret_cast<Piece*>(r.base + row * r.pitch + off) =
-            *reinterpret_cast<const Piece*>(box + row * 64 + (((in >> 4) ^ ((row >> 1) & 3)) << 4) + (in & 15));
+  for (int o = 0; o < kAll / kPerRow; ++o) {
+    const int off = (lane % kPerRow + o * kPerRow) * kPiece, in = off + skip;
+    uint8_t* p = base + lane / kPerRow * pitch + off;
+#pragma unroll 8
+    for (int row = lane / kPerRow; row < 32; row += kAtOnce) {
+      const Piece v = *reinterpret_cast<const Piece*>(__cvta_shared_to_generic(box_piece(box, row, in >> 4) + (in & 15)));
+      if (row < rows && off + kPiece <= bytes) *reinterpret_cast<Piece*>(p) = v;
+      p += kAtOnce * pitch;
     }
   }
 }
-// The widest piece that every row's start and length allow.
-__device__ __forceinline__ void rows_out(const uint8_t* box, const Rows& r, int lane) {
-  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(r.base)) | static_cast<unsigned>(r.pitch) |
-                       static_cast<unsigned>(r.bytes);
+template <int kBytes>
+__device__ __noinline__ void rows_out_any(uint32_t box, uint8_t* base, long long pitch, int bytes, int rows, int skip, int lane) {
+  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(base)) | static_cast<unsigned>(pitch) |
+                       static_cast<unsigned>(bytes);
   if ((mis & 15u) == 0) {
-    rows_out<uint4>(box, r, lane);
+    rows_out_odd<uint4, kBytes>(box, base, pitch, bytes, rows, skip, lane);
   } else if ((mis & 7u) == 0) {
-    rows_out<uint2>(box, r, lane);
+    rows_out_odd<uint2, kBytes>(box, base, pitch, bytes, rows, skip, lane);
   } else if ((mis & 3u) == 0) {
-    rows_out<uint32_t>(box, r, lane);
+    rows_out_odd<uint32_t, kBytes>(box, base, pitch, bytes, rows, skip, lane);
   } else if ((mis & 1u) == 0) {
-    rows_out<uint16_t>(box, r, lane);
+    rows_out_odd<uint16_t, kBytes>(box, base, pitch, bytes, rows, skip, lane);
   } else {
-    rows_out<uint8_t>(box, r, lane);
+    rows_out_odd<uint8_t, kBytes>(box, base, pitch, bytes, rows, skip, lane);
   }
 }
 
-// Hands a warp's output boxes to the TMA (or to the warp's own stores) in turn: a box is written
-// again only when the copy that read it kBoxes boxes earlier has finished reading.
-struct Boxes {
-  uint8_t* mine;
-  int next;
-  __device__ __forceinline__ uint8_t* open() {
-    uint8_t* box = mine + next * kBoxBytes;
-    next = next + 1 == kBoxes ? 0 : next + 1;
-    if (elect_one()) tc::bulk_wait_read<kBoxes - 1>();
-    __syncwarp();
-    return box;
+// Where a warp's part of a result goes: its 32 rows from a first column on, kBytes of each row at a
+// time. What does not change within a tile is worked out once (the addresses of a lane's pieces; that
+// every row is there and every piece whole), since a store costs little more than its instructions.
+template <int kBytes>
+struct Out {
+  static constexpr int kPerRow = kBytes / 16, kAtOnce = 32 / kPerRow;
+  uint8_t* base;
+  uint8_t* mine;    // the lane's first piece
+  long long pitch;  // bytes
+  int bytes, rows;  // from base to the row's end, and rows there are
+  bool whole;
+  // columns col .. of rows row0 .. of M rows and n columns of `size` bytes
+  __device__ __forceinline__ Out(void* matrix, long long ld, int size, int row0, int M, int col, int n, int lane) {
+    pitch = ld * size;
+    base = static_cast<uint8_t*>(matrix) + row0 * pitch + static_cast<long long>(col) * size;
+    bytes = (n - col) * size;
+    rows = min(32, M - row0);
+    mine = base + lane / kPerRow * pitch + 16 * (lane % kPerRow);
+    whole = rows == 32 && ((static_cast<unsigned>(reinterpret_cast<uintptr_t>(base)) | static_cast<unsigned>(pitch)) & 15u) == 0;
   }
-  __device__ __forceinline__ void close(const CUtensorMap* m, uint8_t* box, int col, int row) {
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (elect_one()) {
-      tc::tma_store_2d(m, box, col, row);
-      tc::bulk_commit();
+  // kBytes of each of the box's rows, from byte kSkip on, to byte `at` of the result's rows
+  template <int kSkip>
+  __device__ __forceinline__ void put(uint32_t box, int lane, int at) const {
+    if (whole && at + kBytes <= bytes) {
+      const int q = lane % kPerRow, r0 = lane / kPerRow;
+      uint8_t* p = mine + at;
+#pragma unroll
+      for (int i = 0; i < kPerRow; ++i) {
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(box_piece(box, r0 + i * kAtOnce, kSkip / 16 + q))
+                     : "memory");
+        *reinterpret_cast<uint4*>(p) = v;
+        p += kAtOnce * pitch;
+      }
+    } else if (at < bytes) {
+      rows_out_any<kBytes>(box, base + at, pitch, min(kBytes, bytes - at), rows, kSkip, lane);
     }
-  }
-  __device__ __forceinline__ void close(const Rows& r, uint8_t* box, int lane) {
-    __syncwarp();
-    rows_out(box, r, lane);
-    if (elect_one()) tc::bulk_commit();  // an empty group, so that open()'s count holds
-    __syncwarp();
   }
 };
 
@@ -206,20 +261,32 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uin
       : "memory");
 }
 
-// a(z) = z s(phi(z)) with the logistic s: phi = z (SiLU), or 2 sqrt(2/pi) (z + 0.044715 z^3), which
-// is the tanh form of GELU since (1 + tanh y) / 2 = s(2 y). Beyond |z| = 64 s is 0 or 1 and phi's
-// derivative no longer matters: z is held there inside phi so that no infinity meets a zero.
-__device__ __forceinline__ void gate_of(int act, float z, float& a, float& da) {
-  float phi = z, dphi = 1.0f;
-  if (act == ZOPT_ACT_GELU) {
-    const float c = 1.5957691216057308f;
-    const float zc = fminf(fmaxf(z, -64.0f), 64.0f), z2 = zc * zc;
-    phi = c * zc * (1.0f + 0.044715f * z2);
-    dphi = c * (1.0f + 0.134145f * z2);
+// a(z) = z s(phi(z)) with the logistic s and phi(z) = z (c1 + c3 z^2): c1 = 1, c3 = 0 for SiLU; for the
+// tanh form of GELU c1 = 2 sqrt(2/pi), c3 = 0.044715 c1, since (1 + tanh y) / 2 = s(2 y). Beyond
+// |z| = 100 s is 0 or 1 in fp32: GELU's z is held there inside phi, so that no infinity meets a zero.
+template <int kAct>
+__device__ __forceinline__ void gate(F2 z, F2& a, F2& da) {
+  const F2 one = f2(1.0f, 1.0f);
+  F2 t, dphi = one;
+  if constexpr (kAct == ZOPT_ACT_GELU) {
+    const float c1 = 1.5957691216057308f, c3 = 0.071354816f;
+    const float2 x = f2(z);
+    const F2 zc = f2(fminf(fmaxf(x.x, -100.0f), 100.0f), fminf(fmaxf(x.y, -100.0f), 100.0f)), z2 = zc * zc;
+    dphi = fma2(z2, f2(3.0f * c3, 3.0f * c3), f2(c1, c1));
+    t = zc * fma2(z2, f2(-kLog2e * c3, -kLog2e * c3), f2(-kLog2e * c1, -kLog2e * c1));
+  } else {
+    t = z * f2(-kLog2e, -kLog2e);
   }
-  const float s = __fdividef(1.0f, 1.0f + ex2(-kLog2e * phi));
+  const float2 e = f2(t);
+  const float2 d = f2(f2(ex2(e.x), ex2(e.y)) + one);
+  const F2 s = f2(rcp(d.x), rcp(d.y));
   a = z * s;
-  da = s + a * (1.0f - s) * dphi;
+  da = a * fma2(s, f2(-1.0f, -1.0f), one);
+  if constexpr (kAct == ZOPT_ACT_GELU) {
+    da = fma2(da, dphi, s);
+  } else {
+    da = da + s;
+  }
 }
 
 // ---------------------------------------------------------------------- epilogues
@@ -243,70 +310,65 @@ struct Acc {
   }
   __device__ __forceinline__ void done() const {
     tc::fence_before_sync();
-    __syncwarp();  // every lane's TMEM reads are done: one arrival releases the warp's part
-    if (lane == 0) tc::mbar_arrive_cluster(release_bar);
+    __syncwarp();
+    // Every lane's reads have completed (tcgen05.wait::ld), so nothing has to be released to the
+    // MMAs but the arrival itself; a release here would wait for the warp's stores in flight.
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(release_bar) : "memory");
   }
 };
 __device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
 
 __device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                          Boxes& boxes) {
+                                          uint32_t box) {
   const int row = row0 + lane;
   const float alpha = j.alpha != nullptr && j.splits == 1 ? __ldcg(j.alpha) : 1.0f;
+  const bool wide = j.out_mode == kOutF32;
+  const Out<128> out(wide ? static_cast<void*>(static_cast<float*>(j.out) + w.split * j.split_stride) : j.out, j.ld_out,
+                     wide ? 4 : 2, row0, j.M, w.tj * kTileN + 128 * h, j.N, lane);
 #pragma unroll 1
   for (int half = 0; half < 2; ++half) {
     uint32_t v[2][32];
     acc.read64(128 * h + 64 * half, v);
     if (half == 1) acc.done();
+    const int col0 = w.tj * kTileN + 128 * h + 64 * half;
+    if (col0 >= j.N || row0 >= j.M) continue;  // (warp-uniform)
+    if (j.add != nullptr && row < j.M) {
+      const float* a = j.add + static_cast<long long>(row) * j.ld_add + col0;
+      if (col0 + 64 <= j.N) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = w.tj * kTileN + 128 * h + 64 * half + 32 * c;
-      if (col >= j.N || row0 >= j.M) continue;  // (warp-uniform)
-      float o[32];
-#pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = f(v[c][k]);
-      if (j.add != nullptr && row < j.M) {
-        const float* a = j.add + static_cast<long long>(row) * j.ld_add + col;
-        if (col + 32 <= j.N) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 x = reinterpret_cast<const float4*>(a)[q];
-            o[4 * q] += x.x, o[4 * q + 1] += x.y, o[4 * q + 2] += x.z, o[4 * q + 3] += x.w;
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (col + k < j.N) o[k] += a[k];
+        for (int q = 0; q < 16; ++q) {
+          const float4 x = reinterpret_cast<const float4*>(a)[q];
+          uint32_t* o = &v[q >> 3][4 * (q & 7)];
+          o[0] = __float_as_uint(f(o[0]) + x.x), o[1] = __float_as_uint(f(o[1]) + x.y);
+          o[2] = __float_as_uint(f(o[2]) + x.z), o[3] = __float_as_uint(f(o[3]) + x.w);
         }
-      }
-#pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] *= alpha;
-      if (j.out_mode == kOutF32) {
-        if (row >= j.M) continue;
-        float* p = static_cast<float*>(j.out) + w.split * j.split_stride + static_cast<long long>(row) * j.ld_out + col;
-        if (col + 32 <= j.N) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            reinterpret_cast<float4*>(p)[q] = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (col + k < j.N) p[k] = o[k];
-        }
-        continue;
-      }
-      uint32_t words[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) words[k] = pack2(o[2 * k], o[2 * k + 1]);
-      uint8_t* box = boxes.open();
-      box_row(box, lane, words);
-      if (j.out_mode == kOutTma) {
-        boxes.close(&j.D0, box, col, row0);
       } else {
-        uint16_t* p = static_cast<uint16_t*>(j.out) + static_cast<long long>(row0) * j.ld_out + col;
-        boxes.close(Rows{reinterpret_cast<uint8_t*>(p), j.ld_out * 2, min(32, j.N - col) * 2, min(32, j.M - row0), 0}, box,
-                    lane);
+#pragma unroll
+        for (int k = 0; k < 64; ++k)
+          if (col0 + k < j.N) v[k >> 5][k & 31] = __float_as_uint(f(v[k >> 5][k & 31]) + a[k]);
       }
+    }
+    if (alpha != 1.0f) {
+#pragma unroll
+      for (int k = 0; k < 64; ++k) v[k >> 5][k & 31] = __float_as_uint(f(v[k >> 5][k & 31]) * alpha);
+    }
+    if (wide) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        box_put(box, lane, 0, v[c]);
+        __syncwarp();
+        out.put<0>(box, lane, 256 * half + 128 * c);
+        __syncwarp();
+      }
+    } else {
+      uint32_t words[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) words[k] = pack2(f(v[k >> 4][2 * (k & 15)]), f(v[k >> 4][2 * (k & 15) + 1]));
+      box_put(box, lane, 0, words);
+      __syncwarp();
+      out.put<0>(box, lane, 128 * half);
+      __syncwarp();
     }
   }
 }
@@ -346,16 +408,17 @@ __device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, const Ac
       for (int i = 0; i < d; ++i) top[i] = fmaxf(top[i], top[i + d]);
     const float mn = fmaxf(m, top[0] * kLog2e);
     const float base = mn == -INFINITY ? 0.0f : mn;
-    float part[8];
+    F2 part[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[i] = 0.0f;
+    for (int i = 0; i < 4; ++i) part[i] = f2(0.0f, 0.0f);
+    const F2 scale = f2(kLog2e, kLog2e), minus = f2(-base, -base);
 #pragma unroll
-    for (int k = 0; k < 64; ++k) part[k & 7] += ex2(fmaf(f(v[k >> 5][k & 31]), kLog2e, -base));
-#pragma unroll
-    for (int d = 4; d >= 1; d >>= 1)
-#pragma unroll
-      for (int i = 0; i < d; ++i) part[i] += part[i + d];
-    s = fmaf(s, ex2(m - base), part[0]);
+    for (int k = 0; k < 32; ++k) {
+      const float2 x = f2(fma2(f2(f(v[k >> 4][2 * (k & 15)]), f(v[k >> 4][2 * (k & 15) + 1])), scale, minus));
+      part[k & 3] = part[k & 3] + f2(ex2(x.x), ex2(x.y));
+    }
+    const float2 sum = f2((part[0] + part[1]) + (part[2] + part[3]));
+    s = fmaf(s, ex2(m - base), sum.x + sum.y);
     m = mn;
   }
   if (row < j.M) j.part[static_cast<long long>(2 * w.tj + h) * j.M + row] = make_float2(m, s);
@@ -369,8 +432,9 @@ __device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, const Ac
 // same rounding error, up to 2^-8, into every row (8192 x 2048 x 32000: gradients 2.8e-3 off in
 // 64 bits' norm without the unit).
 __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                           Boxes& boxes) {
+                                           uint32_t box) {
   const int row = row0 + lane;
+  const Out<128> out(j.out, j.ld_out, 2, row0, j.M, w.tj * kTileN + 128 * h, j.N, lane);
   long long tgt = j.ignore;
   float lse2 = 0.0f, dl = 0.0f;
   if (row < j.M) {
@@ -387,25 +451,31 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Ac
     uint32_t v[2][32];
     acc.read64(128 * h + 64 * half, v);
     if (half == 1) acc.done();
+    const int col = w.tj * kTileN + 128 * h + 64 * half;
+    if (col >= j.N || row0 >= j.M) continue;
+    const F2 scale = f2(kLog2e, kLog2e), minus = f2(-lse2, -lse2), weight = f2(dl, dl);
+    uint32_t words[32];
+    if (at < col || at >= col + 64) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = w.tj * kTileN + 128 * h + 64 * half + 32 * c;
-      if (col >= j.N || row0 >= j.M) continue;
-      float o[32];
-#pragma unroll
-      for (int k = 0; k < 32; ++k) o[k] = ex2(fmaf(f(v[c][k]), kLog2e, -lse2));
-      if (at >= col && at < col + 32) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-          if (col + k == at) o[k] -= 1.0f;
+      for (int k = 0; k < 32; ++k) {
+        const float2 x = f2(fma2(f2(f(v[k >> 4][2 * (k & 15)]), f(v[k >> 4][2 * (k & 15) + 1])), scale, minus));
+        words[k] = pack2(f2(ex2(x.x), ex2(x.y)) * weight);
       }
-      uint32_t words[16];
+    } else {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) words[k] = live ? pack2(o[2 * k] * dl, o[2 * k + 1] * dl) : 0u;
-      uint8_t* box = boxes.open();
-      box_row(box, lane, words);
-      boxes.close(&j.D0, box, col, row0);
+      for (int k = 0; k < 32; ++k) {
+        const float2 x = f2(fma2(f2(f(v[k >> 4][2 * (k & 15)]), f(v[k >> 4][2 * (k & 15) + 1])), scale, minus));
+        words[k] = pack2((ex2(x.x) - (col + 2 * k == at ? 1.0f : 0.0f)) * dl, (ex2(x.y) - (col + 2 * k + 1 == at ? 1.0f : 0.0f)) * dl);
+      }
     }
+    if (!live) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) words[k] = 0u;
+    }
+    box_put(box, lane, 0, words);
+    __syncwarp();
+    out.put<0>(box, lane, 128 * half);
+    __syncwarp();
   }
 }
 
@@ -413,15 +483,16 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Ac
 // warp's are 64 h .. 64 h + 63 of each. A tile is one 8-bit block wide: a block's largest magnitude
 // is found within a lane and its partner in the warp that has the other half, through `swap` (two
 // bytes a lane; the two warps share barrier `bar`).
+template <int kAct, int kKept>
 __device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                            Boxes& boxes, uint16_t* swap, int bar) {
-  const int row = row0 + lane, n0 = w.tj * 128, rows = min(32, j.M - row0);
+                                            uint32_t box, uint16_t* swap, int bar) {
+  const int row = row0 + lane, n0 = w.tj * 128;
   if (row0 >= j.M) {  // (the partner warp has the same rows)
     acc.done();
     return;
   }
   float inv[2] = {1.0f, 1.0f};
-  if (j.kept_mode == kKeep8) {
+  if constexpr (kKept == kKeep8) {
     uint32_t e[2];
     uint32_t v[2][32];
 #pragma unroll
@@ -449,64 +520,63 @@ __device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const A
       j.kept_scale[static_cast<long long>(row) * 2 * nb + h * nb + w.tj] = static_cast<uint8_t>(h == 0 ? e[0] : e[1]);
     inv[0] = act8::inv_scale(e[0]), inv[1] = act8::inv_scale(e[1]);
   }
+  constexpr int kSize = kKept == kKeep8 ? 1 : 2;
+  const int first = n0 + 64 * h;
+  const Out<64> out(j.out, j.ld_out, 2, row0, j.M, first, j.hidden, lane);
+  Out<32 * kSize> gate_out(j.kept, j.ld_kept, kSize, row0, j.M, first, j.hidden, lane);
+  Out<32 * kSize> up_out(static_cast<uint8_t*>(j.kept) + static_cast<long long>(j.hidden) * kSize, j.ld_kept, kSize, row0, j.M,
+                         first, j.hidden, lane);
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    const int col = n0 + 64 * h + 32 * c;
     uint32_t g[32], u[32];
     tc::tmem_ld32(acc.base + static_cast<uint32_t>(64 * h + 32 * c), g);
     tc::tmem_ld32(acc.base + static_cast<uint32_t>(128 + 64 * h + 32 * c), u);
     tc::tmem_wait_ld();
     if (c == 1) acc.done();
-    if (col >= j.N) continue;
-    if (j.kept_mode == kKeepTma || j.kept_mode == kKeepBf16) {
+    if (first + 32 * c >= j.hidden) continue;
+    if constexpr (kKept == kKeepBf16) {  // a box: a row's 32 gates, then its 32 ups
+      uint32_t words[32];
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const uint32_t(&x)[32] = part == 0 ? g : u;
-        uint32_t words[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) words[k] = pack2(f(x[2 * k]), f(x[2 * k + 1]));
-        uint8_t* box = boxes.open();
-        box_row(box, lane, words);
-        if (j.kept_mode == kKeepTma) {
-          boxes.close(part == 0 ? &j.D1 : &j.D2, box, col, row0);
-        } else {
-          uint16_t* p = static_cast<uint16_t*>(j.kept) + static_cast<long long>(row0) * j.ld_kept + static_cast<long long>(part) * j.hidden + col;
-          boxes.close(Rows{reinterpret_cast<uint8_t*>(p), j.ld_kept * 2, min(32, j.hidden - col) * 2, rows, 0}, box, lane);
-        }
+      for (int k = 0; k < 16; ++k) {
+        words[k] = pack2(f(g[2 * k]), f(g[2 * k + 1]));
+        words[16 + k] = pack2(f(u[2 * k]), f(u[2 * k + 1]));
       }
-    } else if (j.kept_mode == kKeep8) {  // one box: a row's 32 gate bytes, then its 32 up bytes
+      box_put(box, lane, 0, words);
+      __syncwarp();
+      gate_out.template put<0>(box, lane, 64 * c);
+      up_out.template put<64>(box, lane, 64 * c);
+      __syncwarp();
+    } else if constexpr (kKept == kKeep8) {  // a box: a row's 32 gate bytes, its 32 up bytes, its 32 h
       uint32_t words[16];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         words[q] = act8::encode4(f(g[4 * q]), f(g[4 * q + 1]), f(g[4 * q + 2]), f(g[4 * q + 3]), inv[0]);
         words[8 + q] = act8::encode4(f(u[4 * q]), f(u[4 * q + 1]), f(u[4 * q + 2]), f(u[4 * q + 3]), inv[1]);
       }
-      uint8_t* box = boxes.open();
-      box_row(box, lane, words);
-      uint8_t* p = static_cast<uint8_t*>(j.kept) + static_cast<long long>(row0) * j.ld_kept + col;
-      const int n = min(32, j.hidden - col);
-      __syncwarp();
-      rows_out(box, Rows{p, j.ld_kept, n, rows, 0}, lane);
-      boxes.close(Rows{p + j.hidden, j.ld_kept, n, rows, 32}, box, lane);
+      box_put(box, lane, 0, words);
     }
-    uint32_t words[16];
+    uint32_t hh[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      float a0, a1, da;
-      gate_of(j.act, f(g[2 * k]), a0, da);
-      gate_of(j.act, f(g[2 * k + 1]), a1, da);
-      words[k] = pack2(a0 * f(u[2 * k]), a1 * f(u[2 * k + 1]));
+      F2 a, da;
+      gate<kAct>(f2(f(g[2 * k]), f(g[2 * k + 1])), a, da);
+      hh[k] = pack2(a * f2(f(u[2 * k]), f(u[2 * k + 1])));
     }
-    uint8_t* box = boxes.open();
-    box_row(box, lane, words);
-    boxes.close(&j.D0, box, col, row0);
+    box_put(box, lane, 4, hh);
+    __syncwarp();
+    if constexpr (kKept == kKeep8) {
+      gate_out.template put<0>(box, lane, 32 * c);
+      up_out.template put<32>(box, lane, 32 * c);
+    }
+    out.put<64>(box, lane, 64 * c);
+    __syncwarp();
   }
 }
 
 // The words of 32 kept columns of one row and part as they lie in memory (bf16: 16 words, 8 bits: 8),
-// zero beyond n columns, by the widest loads that the row's start allows.
+// zero beyond `bytes`.
 template <int kWords, typename Piece>
-__device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t (&x)[kWords]) {
+__device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t* x) {
   constexpr int kPiece = sizeof(Piece);
 #pragma unroll
   for (int i = 0; i < 4 * kWords / kPiece; ++i) {
@@ -524,92 +594,106 @@ __device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t (
     }
   }
 }
-template <int kWords>
-__device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t (&x)[kWords]) {
-  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)) | static_cast<unsigned>(bytes);
-  if ((mis & 15u) == 0) {
-    words_in<kWords, uint4>(p, bytes, x);
-  } else if ((mis & 3u) == 0) {
-    words_in<kWords, uint32_t>(p, bytes, x);
-  } else if ((mis & 1u) == 0) {
-    words_in<kWords, uint16_t>(p, bytes, x);
-  } else {
-    words_in<kWords, uint8_t>(p, bytes, x);
-  }
-}
 
-// What gate and up of 32 columns are read as, and their values.
+// Gate and up of 32 columns as they are read. kWide: every row, and up's offset in it, is a multiple
+// of 16 bytes, and so is the last columns' number.
+template <int kKept>
 struct Kept {
-  uint32_t x[2][16];
-  float sc[2];
-};
-__device__ __forceinline__ void kept_load(const Job& j, int row, int col, Kept& k) {
-  const bool in = row < j.M && col < j.hidden;
-  const int n = in ? min(32, j.hidden - col) : 0;
-  const long long off = in ? static_cast<long long>(row) * j.ld_kept + col : 0;
+  static constexpr int kWords = kKept == kKeep8 ? 8 : 16, kSize = kKept == kKeep8 ? 1 : 2;
+  uint32_t x[2][kWords];
+  template <bool kWide>
+  __device__ __forceinline__ void load(const Job& j, int row, int col) {
+    const bool in = row < j.M && col < j.hidden;
+    const int bytes = in ? min(32, j.hidden - col) * kSize : 0;
+    const uint8_t* p = static_cast<const uint8_t*>(j.kept) + (in ? (static_cast<long long>(row) * j.ld_kept + col) * kSize : 0);
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    const long long at = off + (in ? static_cast<long long>(part) * j.hidden : 0);
-    if (j.kept_mode == kKeep8) {
-      const long long nb = act8::blocks_of(j.hidden);
-      uint32_t w8[8];
-      words_in<8>(static_cast<const uint8_t*>(j.kept) + at, n, w8);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) k.x[part][i] = w8[i];
-      k.sc[part] = in ? act8::scale(j.kept_scale[static_cast<long long>(row) * 2 * nb + part * nb + (col >> 7)]) : 1.0f;
-    } else {
-      words_in<16>(static_cast<const uint8_t*>(j.kept) + 2 * at, 2 * n, k.x[part]);
+    for (int part = 0; part < 2; ++part) {
+      const uint8_t* at = p + (in ? static_cast<long long>(part) * j.hidden * kSize : 0);
+      if constexpr (kWide) {
+        words_in<kWords, uint4>(at, bytes, x[part]);
+      } else {
+        const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) | static_cast<unsigned>(bytes);
+        if ((mis & 7u) == 0) {
+          words_in<kWords, uint2>(at, bytes, x[part]);
+        } else if ((mis & 3u) == 0) {
+          words_in<kWords, uint32_t>(at, bytes, x[part]);
+        } else if (kSize == 2) {
+          words_in<kWords, uint16_t>(at, bytes, x[part]);
+        } else {
+          words_in<kWords, uint8_t>(at, bytes, x[part]);
+        }
+      }
     }
   }
-}
-// Values 2 q and 2 q + 1 of a part.
-__device__ __forceinline__ float2 kept_two(bool eight, const Kept& k, int part, int q) {
-  if (eight) return act8::decode2(k.x[part][q >> 1] >> (16 * (q & 1)), k.sc[part]);
-  return make_float2(__uint_as_float(k.x[part][q] << 16), __uint_as_float(k.x[part][q] & 0xFFFF0000u));
-}
+  // Values 2 q and 2 q + 1 of a part.
+  __device__ __forceinline__ F2 two(int part, int q, float sc) const {
+    if constexpr (kKept == kKeep8) {
+      const float2 v = act8::decode2(x[part][q >> 1] >> (16 * (q & 1)));
+      return f2(v.x, v.y) * f2(sc, sc);
+    }
+    return f2(__uint_as_float(x[part][q & (kWords - 1)] << 16), __uint_as_float(x[part][q & (kWords - 1)] & 0xFFFF0000u));
+  }
+};
+// The two powers of the lane's row in the 128 columns from col on (one block of each part).
+struct Scales {
+  float s[2] = {1.0f, 1.0f};
+  __device__ __forceinline__ void load(const Job& j, int row, int col) {
+    if (row >= j.M || col >= j.hidden) return;
+    const long long nb = act8::blocks_of(j.hidden);
+    const uint8_t* p = j.kept_scale + static_cast<long long>(row) * 2 * nb + (col >> 7);
+    s[0] = act8::scale(p[0]);
+    s[1] = act8::scale(p[nb]);
+  }
+};
 
 // dgate = dh up a'(gate), dup = dh a(gate), h = a(gate) up, each rounded to bf16 once: they are
-// operands of the three products that follow. `k` holds the kept values of the first 32 columns,
-// read while the tile's products ran; each later 32 are read while the ones before are worked on.
+// operands of the three products that follow. `first` holds the kept values of the warp's first 32
+// columns, read while the tile's products ran; the next 32 are read before the ones at hand are
+// worked on.
+template <int kAct, int kKept, bool kWide>
 __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                            Boxes& boxes, Kept& k) {
+                                            uint32_t box, const Kept<kKept>& first, const Scales& sc) {
   const int row = row0 + lane;
-  const bool eight = j.kept_mode == kKeep8;
+  const int col0 = w.tj * kTileN + 128 * h;
+  const Out<64> dgate(j.out, j.ld_out, 2, row0, j.M, col0, j.N, lane);
+  const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, j.M, col0, j.N, lane);
+  const Out<64> hout(j.out_h, j.N, 2, row0, j.M, col0, j.N, lane);
+  Kept<kKept> k = first;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
-    const int col = w.tj * kTileN + 128 * h + 32 * c;
+    const int col = col0 + 32 * c;
     uint32_t v[32];
     acc.read32(128 * h + 32 * c, v);
     if (c == 3) acc.done();
     if (col >= j.N || row0 >= j.M) continue;
-    uint32_t dg[16], du[16], hh[16];
+    Kept<kKept> next;
+    next.template load<kWide>(j, c < 3 ? row : j.M, col + 32);
+    uint32_t dgu[32], hh[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
-      const float2 g = kept_two(eight, k, 0, q), u = kept_two(eight, k, 1, q);
-      float a0, a1, da0, da1;
-      gate_of(j.act, g.x, a0, da0);
-      gate_of(j.act, g.y, a1, da1);
-      const float d0 = f(v[2 * q]), d1 = f(v[2 * q + 1]);
-      dg[q] = pack2(d0 * u.x * da0, d1 * u.y * da1);
-      du[q] = pack2(d0 * a0, d1 * a1);
-      hh[q] = pack2(a0 * u.x, a1 * u.y);
+      const F2 g = k.two(0, q, sc.s[0]), u = k.two(1, q, sc.s[1]), d = f2(f(v[2 * q]), f(v[2 * q + 1]));
+      F2 a, da;
+      gate<kAct>(g, a, da);
+      dgu[q] = pack2(d * u * da);
+      dgu[16 + q] = pack2(d * a);
+      hh[q] = pack2(a * u);
     }
-    if (c < 3) kept_load(j, row, col + 32, k);
-    uint8_t* box = boxes.open();
-    box_row(box, lane, dg);
-    boxes.close(&j.D0, box, col, row0);
-    box = boxes.open();
-    box_row(box, lane, du);
-    boxes.close(&j.D1, box, col, row0);
-    box = boxes.open();
-    box_row(box, lane, hh);
-    boxes.close(&j.D2, box, col, row0);
+    box_put(box, lane, 0, dgu);  // a row's 32 dgates, then its 32 dups
+    __syncwarp();
+    dgate.put<0>(box, lane, 64 * c);
+    dup.put<64>(box, lane, 64 * c);
+    __syncwarp();
+    box_put(box, lane, 0, hh);
+    __syncwarp();
+    hout.put<0>(box, lane, 64 * c);
+    __syncwarp();
+    k = next;
   }
 }
 
 // ---------------------------------------------------------------------- the kernel
 
-template <int kKinds>
+template <int kKinds, int kAct, int kKept, bool kWide>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_gemm_kernel(const __grid_constant__ Batch B) {
   extern __shared__ uint8_t smem_raw[];
@@ -617,7 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kHalfBytes;
   uint8_t* sEpi = sB + kStages * kHalfBytes;
-  uint16_t* sSwap = reinterpret_cast<uint16_t*>(sEpi + kEpiWarps * kBoxes * kBoxBytes);
+  uint16_t* sSwap = reinterpret_cast<uint16_t*>(sEpi + kEpiWarps * kBoxBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sSwap) + kSwapBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
@@ -768,7 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int half = (warp - 2) >> 2;   // and takes this half of the columns
     const uint32_t tempty_leader[2] = {tc::map_to_rank(tc::smem_u32(tempty), 0),
                                        tc::map_to_rank(tc::smem_u32(tempty + 1), 0)};
-    Boxes boxes{sEpi + (warp - 2) * kBoxes * kBoxBytes, 0};
+    const uint32_t box = tc::smem_u32(sEpi) + (warp - 2) * kBoxBytes;
     uint16_t* swap = sSwap + 64 * quad;
     const int rows0 = static_cast<int>(rank) * 128 + 32 * quad;  // this warp's rows within a tile
     int it = 0;
@@ -779,21 +863,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Job& j = B.job[ji];
       const Unit w = unit_of(j, t - B.start[ji]);
       const int row0 = w.ti * kTileM + rows0;
-      Kept kept;
-      if constexpr ((kKinds & kGluBwd) != 0) kept_load(j, row0 + lane, w.tj * kTileN + 128 * half, kept);
+      Kept<kKept> kept;
+      Scales scales;
+      if constexpr ((kKinds & kGluBwd) != 0) {
+        const int col = w.tj * kTileN + 128 * half;
+        kept.template load<kWide>(j, row0 + lane, col);
+        if constexpr (kKept == kKeep8) scales.load(j, row0 + lane, col);
+      }
       int ok = 1;
       if (lane == 0) ok = tc::mbar_wait_idle(tfull + b, tph, err) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
       tc::fence_after_sync();
       const Acc acc{tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN), tempty_leader[b], lane};
-      if ((kKinds & kStore) && j.kind == kStore) epi_store(j, w, acc, row0, lane, half, boxes);
+      if ((kKinds & kStore) && j.kind == kStore) epi_store(j, w, acc, row0, lane, half, box);
       if ((kKinds & kCeFwd) && j.kind == kCeFwd) epi_ce_fwd(j, w, acc, row0, lane, half);
-      if ((kKinds & kCeBwd) && j.kind == kCeBwd) epi_ce_bwd(j, w, acc, row0, lane, half, boxes);
-      if constexpr ((kKinds & kGluFwd) != 0) epi_glu_fwd(j, w, acc, row0, lane, half, boxes, swap, 1 + quad);
-      if constexpr ((kKinds & kGluBwd) != 0) epi_glu_bwd(j, w, acc, row0, lane, half, boxes, kept);
+      if ((kKinds & kCeBwd) && j.kind == kCeBwd) epi_ce_bwd(j, w, acc, row0, lane, half, box);
+      if constexpr ((kKinds & kGluFwd) != 0) epi_glu_fwd<kAct, kKept>(j, w, acc, row0, lane, half, box, swap, 1 + quad);
+      if constexpr ((kKinds & kGluBwd) != 0) epi_glu_bwd<kAct, kKept, kWide>(j, w, acc, row0, lane, half, box, kept, scales);
     }
-    if (elect_one()) tc::bulk_wait_all();  // every store has reached global memory
-    __syncwarp();
   }
   tc::fence_before_sync();
   tc::cluster_sync();  // every MMA, copy and remote arrival of the pair is done
@@ -847,12 +934,25 @@ __global__ void __launch_bounds__(256) stage_kernel(uint16_t* dst, long long dst
   }
 }
 
-template <int kKinds>
+template <int kKinds, int kAct = 0, int kKept = kKeepNone, bool kWide = true>
 zopt_status launch_kinds(Batch& b, dim3 grid, cudaStream_t s) {
-  ZOPT_CUDA_TRY(once([] {
-    return cudaFuncSetAttribute(lm_gemm_kernel<kKinds>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  }));
-  return launch_pdl(lm_gemm_kernel<kKinds>, grid, dim3(kThreads), static_cast<size_t>(kSmemBytes), s, b);
+  const auto kernel = lm_gemm_kernel<kKinds, kAct, kKept, kWide>;
+  ZOPT_CUDA_TRY(once([=] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes); }));
+  return launch_pdl(kernel, grid, dim3(kThreads), static_cast<size_t>(kSmemBytes), s, b);
+}
+template <int kAct>
+zopt_status launch_glu(Batch& b, dim3 grid, cudaStream_t s) {
+  const Job& j = b.job[0];
+  if (j.kind == kGluFwd) {
+    if (j.kept_mode == kKeepNone) return launch_kinds<kGluFwd, kAct>(b, grid, s);
+    return j.kept_mode == kKeep8 ? launch_kinds<kGluFwd, kAct, kKeep8>(b, grid, s)
+                                 : launch_kinds<kGluFwd, kAct, kKeepBf16>(b, grid, s);
+  }
+  const int size = j.kept_mode == kKeep8 ? 1 : 2;
+  const bool wide = aligned16(j.kept) && j.ld_kept * size % 16 == 0 && static_cast<long long>(j.hidden) * size % 16 == 0;
+  if (j.kept_mode == kKeep8)
+    return wide ? launch_kinds<kGluBwd, kAct, kKeep8>(b, grid, s) : launch_kinds<kGluBwd, kAct, kKeep8, false>(b, grid, s);
+  return wide ? launch_kinds<kGluBwd, kAct, kKeepBf16>(b, grid, s) : launch_kinds<kGluBwd, kAct, kKeepBf16, false>(b, grid, s);
 }
 
 }  // namespace
@@ -864,30 +964,28 @@ unsigned blocks_for(long long items, int sms) {
 
 // ---------------------------------------------------------------------- host side
 
+namespace {
+// A bf16 row-major matrix [outer][inner] with `pitch` elements between rows, boxes of 64 x box_outer.
 zopt_status make_map(const char* fn, CUtensorMap* m, const void* base, long long inner, long long outer,
-                     long long pitch, int box_inner, int box_outer) {
+                     long long pitch, int box_outer) {
   auto enc = ns::encode_fn();
   if (enc == nullptr) return fail(ZOPT_ECUDA, std::string(fn) + ": cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer)};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_outer)};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(ZOPT_ECUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
   return ok();
 }
+}  // namespace
 
 zopt_status map_operand(const char* fn, CUtensorMap* m, const void* base, long long mn, long long k, long long pitch,
                         bool mn_major) {
-  return mn_major ? make_map(fn, m, base, mn, k, pitch, 64, 64) : make_map(fn, m, base, k, mn, pitch, 64, 128);
-}
-
-zopt_status map_output(const char* fn, CUtensorMap* m, void* base, long long rows, long long cols, long long pitch) {
-  return make_map(fn, m, base, cols, rows, pitch, 32, 32);
+  return mn_major ? make_map(fn, m, base, mn, k, pitch, 64) : make_map(fn, m, base, k, mn, pitch, 128);
 }
 
 void set_tiles(Job& j) {
@@ -937,8 +1035,9 @@ zopt_status launch(const char* fn, Batch& b, int kinds, cudaStream_t s) {
     case kStore: return launch_kinds<kStore>(b, grid, s);
     case kCeFwd: return launch_kinds<kCeFwd>(b, grid, s);
     case kStore | kCeBwd: return launch_kinds<kStore | kCeBwd>(b, grid, s);
-    case kGluFwd: return launch_kinds<kGluFwd>(b, grid, s);
-    case kGluBwd: return launch_kinds<kGluBwd>(b, grid, s);
+    case kGluFwd:
+    case kGluBwd:
+      return b.job[0].act == ZOPT_ACT_GELU ? launch_glu<ZOPT_ACT_GELU>(b, grid, s) : launch_glu<ZOPT_ACT_SILU>(b, grid, s);
   }
   return fail(ZOPT_EINVAL, std::string(fn) + ": internal: no kernel for these epilogues");
 }

@@ -25,10 +25,9 @@ constexpr int kHalfBytes = 128 * kTileK * 2;  // one CTA's half of a stage's P o
 constexpr int kMnBoxBytes = 64 * kTileK * 2;  // one 64 (MN) x 64 (K) box of an MN-major operand
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
-constexpr int kBoxBytes = 32 * 32 * 2;
-constexpr int kBoxes = 2;  // output boxes per epilogue warp
+constexpr int kBoxBytes = 32 * 128;  // an epilogue warp's results on their way to memory: 32 rows of 128 bytes
 constexpr int kSwapBytes = 4 * 64 * 2;  // kGluFwd: two warps' block exponents for each quarter of the rows
-constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxes * kBoxBytes + kSwapBytes + 1024 + 256;
+constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxBytes + kSwapBytes + 1024 + 256;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr int kMaxJobs = 5;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -42,11 +41,11 @@ enum Kind : int {
   kGluBwd = 16  // dgate, dup and h from dh
 };
 
-enum OutMode : int { kOutTma = 0, kOutBf16 = 1, kOutF32 = 2 };          // kStore: through D0, or row stores
-enum KeptMode : int { kKeepNone = 0, kKeepTma = 1, kKeepBf16 = 2, kKeep8 = 3 };  // kGluFwd, kGluBwd
+enum OutMode : int { kOutBf16 = 0, kOutF32 = 1 };                   // kStore
+enum KeptMode : int { kKeepNone = 0, kKeepBf16 = 1, kKeep8 = 2 };  // kGluFwd, kGluBwd
 
 struct Job {
-  CUtensorMap P, Q, D0, D1, D2;
+  CUtensorMap P, Q;
   int kind;
   int M, N, K;
   int a_mn, b_mn;
@@ -55,10 +54,14 @@ struct Job {
   int nk, kb_per_split, splits;
   int whole;      // its inner length is not cut
   int rows_fast;  // consecutive tiles walk down a tile column (else along a tile row)
+  // D, or what the epilogue makes of it: kCeBwd's dl; kGluFwd's h; kGluBwd's dgate, its dup N columns
+  // later, and h (out_h, rows of N)
+  void* out;
+  long long ld_out;
+  void* out_h;
   // kStore
   int out_mode;
-  void* out;
-  long long ld_out, split_stride;  // split_stride: elements between the partial sums of one tile's runs of k
+  long long split_stride;  // split_stride: elements between the partial sums of one tile's runs of k
   const float* add;                // fp32 M x N added to D; null: none
   long long ld_add;
   const float* alpha;  // (D + add) is multiplied by *alpha; null: 1
@@ -87,19 +90,10 @@ struct Batch {
 
 // ------------------------------------------------------------------ host side
 
-// A bf16 row-major matrix [outer][inner] with `pitch` elements between rows, boxes box_inner x
-// box_outer: the 128-byte swizzle for operands (box_inner 64), the 64-byte one for 32 x 32 outputs.
-zopt_status make_map(const char* fn, CUtensorMap* m, const void* base, long long inner, long long outer,
-                     long long pitch, int box_inner, int box_outer);
-// P [M][K] (K contiguous), or stored [K][M]; the same for Q's columns [N][K] or [K][N].
+// The map of an operand's rows (P) or columns (Q), `mn` of them of inner length k: stored [mn][k], or
+// [k][mn] where MN-major, `pitch` elements (a multiple of 8) between the rows as stored.
 zopt_status map_operand(const char* fn, CUtensorMap* m, const void* base, long long mn, long long k, long long pitch,
                         bool mn_major);
-zopt_status map_output(const char* fn, CUtensorMap* m, void* base, long long rows, long long cols, long long pitch);
-// Whether a result's rows of `cols` elements, `pitch` apart, can be stored by the TMA: it moves whole
-// 16-byte pieces, so a row has to end on one or it would overwrite what lies beside the result.
-inline bool tma_out_ok(const void* base, long long cols, long long pitch) {
-  return aligned16(base) && pitch % 8 == 0 && cols % 8 == 0;
-}
 
 // Fills a job's tile counts from kind, M, N, K; k_blocks is its number of 64-deep blocks.
 void set_tiles(Job& j);
