@@ -116,6 +116,12 @@ __device__ __forceinline__ void box_put(uint32_t box, int lane, int q0, const ui
                  : "memory");
 }
 
+__device__ __forceinline__ void box_put4(uint32_t box, int lane, int q, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_piece(box, lane, 0) ^ static_cast<uint32_t>(q << 4)), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
 // Pieces of kPiece bytes, for rows whose start or length is not a multiple of 16 bytes.
 template <typename Piece, int kBytes>
 __device__ __noinline__ void rows_out_odd(uint32_t box, uint8_t* base, long long pitch, int bytes, int rows, int skip, int lane) {
@@ -175,14 +181,15 @@ struct Out {
     if (whole && at + kBytes <= bytes) {
       const int q = lane % kPerRow, r0 = lane / kPerRow;
       uint8_t* p = mine + at;
+      uint4 v[kPerRow];
+#pragma unroll
+      for (int i = 0; i < kPerRow; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                     : "r"(box_piece(box, r0 + i * kAtOnce, kSkip / 16 + q)));
 #pragma unroll
       for (int i = 0; i < kPerRow; ++i) {
-        uint4 v;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(box_piece(box, r0 + i * kAtOnce, kSkip / 16 + q))
-                     : "memory");
-        *reinterpret_cast<uint4*>(p) = v;
+        *reinterpret_cast<uint4*>(p) = v[i];
         p += kAtOnce * pitch;
       }
     } else if (at < bytes) {
@@ -647,48 +654,58 @@ struct Scales {
 };
 
 // dgate = dh up a'(gate), dup = dh a(gate), h = a(gate) up, each rounded to bf16 once: they are
-// operands of the three products that follow. `first` holds the kept values of the warp's first 32
-// columns, read while the tile's products ran; the next 32 are read before the ones at hand are
-// worked on.
+// operands of the three products that follow. `k` holds the kept values of the warp's first 32
+// columns; while 32 columns are worked on the next ones are on their way, at a tile's end the next
+// tile's first (row and column next_row and next_col): gate and up come from HBM, and a tile that
+// began by waiting for them would take longer than its products.
 template <int kAct, int kKept, bool kWide>
 __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                            uint32_t box, const Kept<kKept>& first, const Scales& sc) {
+                                            uint32_t box, Kept<kKept>& k, Scales& sc, int next_row, int next_col) {
   const int row = row0 + lane;
   const int col0 = w.tj * kTileN + 128 * h;
   const Out<64> dgate(j.out, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> hout(j.out_h, j.N, 2, row0, j.M, col0, j.N, lane);
-  Kept<kKept> k = first;
+  Scales next_sc;
+  if constexpr (kKept == kKeep8) next_sc.load(j, next_row, next_col);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     const int col = col0 + 32 * c;
     uint32_t v[32];
     acc.read32(128 * h + 32 * c, v);
     if (c == 3) acc.done();
-    if (col >= j.N || row0 >= j.M) continue;
     Kept<kKept> next;
-    next.template load<kWide>(j, c < 3 ? row : j.M, col + 32);
-    uint32_t dgu[32], hh[16];
+    next.template load<kWide>(j, c < 3 ? row : next_row, c < 3 ? col + 32 : next_col);
+    if (col < j.N && row0 < j.M) {
+      uint32_t hh[16];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const F2 g = k.two(0, q, sc.s[0]), u = k.two(1, q, sc.s[1]), d = f2(f(v[2 * q]), f(v[2 * q + 1]));
-      F2 a, da;
-      gate<kAct>(g, a, da);
-      dgu[q] = pack2(d * u * da);
-      dgu[16 + q] = pack2(d * a);
-      hh[q] = pack2(a * u);
+      for (int q = 0; q < 4; ++q) {  // eight columns: a piece of each result
+        uint32_t dg[4], du[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = 4 * q + i;
+          const F2 g = k.two(0, p, sc.s[0]), u = k.two(1, p, sc.s[1]), d = f2(f(v[2 * p]), f(v[2 * p + 1]));
+          F2 a, da;
+          gate<kAct>(g, a, da);
+          dg[i] = pack2(d * u * da);
+          du[i] = pack2(d * a);
+          hh[p] = pack2(a * u);
+        }
+        box_put4(box, lane, q, dg[0], dg[1], dg[2], dg[3]);  // a row's 32 dgates, then its 32 dups
+        box_put4(box, lane, 4 + q, du[0], du[1], du[2], du[3]);
+      }
+      __syncwarp();
+      dgate.put<0>(box, lane, 64 * c);
+      dup.put<64>(box, lane, 64 * c);
+      __syncwarp();
+      box_put(box, lane, 0, hh);
+      __syncwarp();
+      hout.put<0>(box, lane, 64 * c);
+      __syncwarp();
     }
-    box_put(box, lane, 0, dgu);  // a row's 32 dgates, then its 32 dups
-    __syncwarp();
-    dgate.put<0>(box, lane, 64 * c);
-    dup.put<64>(box, lane, 64 * c);
-    __syncwarp();
-    box_put(box, lane, 0, hh);
-    __syncwarp();
-    hout.put<0>(box, lane, 64 * c);
-    __syncwarp();
     k = next;
   }
+  sc = next_sc;
 }
 
 // ---------------------------------------------------------------------- the kernel
@@ -855,6 +872,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t box = tc::smem_u32(sEpi) + (warp - 2) * kBoxBytes;
     uint16_t* swap = sSwap + 64 * quad;
     const int rows0 = static_cast<int>(rank) * 128 + 32 * quad;  // this warp's rows within a tile
+    Kept<kKept> kept;
+    Scales scales;
+    auto first_of = [&](int t, int& row, int& col) {  // the lane's row and the warp's first column of unit t (kGluBwd)
+      const Unit w = unit_of(B.job[0], t);
+      row = t < total ? w.ti * kTileM + rows0 + lane : B.job[0].M;
+      col = w.tj * kTileN + 128 * half;
+    };
+    if constexpr ((kKinds & kGluBwd) != 0) {
+      int row, col;
+      first_of(pair, row, col);
+      kept.template load<kWide>(B.job[0], row, col);
+      if constexpr (kKept == kKeep8) scales.load(B.job[0], row, col);
+    }
     int it = 0;
     for (int t = pair; t < total; t += npairs, ++it) {
       const int b = it & 1;
@@ -863,13 +893,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Job& j = B.job[ji];
       const Unit w = unit_of(j, t - B.start[ji]);
       const int row0 = w.ti * kTileM + rows0;
-      Kept<kKept> kept;
-      Scales scales;
-      if constexpr ((kKinds & kGluBwd) != 0) {
-        const int col = w.tj * kTileN + 128 * half;
-        kept.template load<kWide>(j, row0 + lane, col);
-        if constexpr (kKept == kKeep8) scales.load(j, row0 + lane, col);
-      }
       int ok = 1;
       if (lane == 0) ok = tc::mbar_wait_idle(tfull + b, tph, err) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
@@ -879,7 +902,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if ((kKinds & kCeFwd) && j.kind == kCeFwd) epi_ce_fwd(j, w, acc, row0, lane, half);
       if ((kKinds & kCeBwd) && j.kind == kCeBwd) epi_ce_bwd(j, w, acc, row0, lane, half, box);
       if constexpr ((kKinds & kGluFwd) != 0) epi_glu_fwd<kAct, kKept>(j, w, acc, row0, lane, half, box, swap, 1 + quad);
-      if constexpr ((kKinds & kGluBwd) != 0) epi_glu_bwd<kAct, kKept, kWide>(j, w, acc, row0, lane, half, box, kept, scales);
+      if constexpr ((kKinds & kGluBwd) != 0) {
+        int row, col;
+        first_of(t + npairs, row, col);
+        epi_glu_bwd<kAct, kKept, kWide>(j, w, acc, row0, lane, half, box, kept, scales, row, col);
+      }
     }
   }
   tc::fence_before_sync();
