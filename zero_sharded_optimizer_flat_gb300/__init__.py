@@ -170,10 +170,26 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """The cheapest way this torch has to the current stream's handle (a Stream object costs a small
+    call more than its kernels do)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    device = torch.cuda.current_device
+    return lambda: raw(device())
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -598,28 +614,42 @@ def new_act8(rows: int, cols: int, parts: int = 1, device="cuda") -> Act8:
 
 def _on_device(*tensors) -> None:
     for t in tensors:
-        if t is not None and not t.is_cuda:
+        if not t.is_cuda:
             raise ValueError("tensors must be on the GPU")
 
 
+_CODES = {}
+
+
+def _code(t) -> int:
+    """_dtype_code from a table (filled on the first call)."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16})
+    return _CODES.get(t.dtype, -1)
+
+
 def _matrix(t, rows: int, cols: int, name: str):
-    """(address, row distance) of a rows x cols bf16 matrix with contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+    """(address, row distance) of a rows x cols matrix with contiguous rows."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be a {rows} x {cols} matrix with a contiguous last dimension")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must be a {rows} x {cols} matrix with a contiguous last dimension")
     if not t.is_cuda:
         raise ValueError("tensors must be on the GPU")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def _same_dtype(*tensors) -> int:
-    code = _dtype_code(tensors[0])
-    return code if all(t.dtype == tensors[0].dtype for t in tensors) else -1
+    code = _code(tensors[0])
+    return code if all(_code(t) == code for t in tensors) else -1
 
 
 def act_pack(x, out: Act8, stream=None) -> None:
     """``zopt_act_pack``: out = the 8-bit checkpoint of the bf16 matrix x."""
     p, ld = _matrix(x, out.rows, out.cols, "x")
-    if _dtype_code(x) != BF16:
+    if _code(x) != BF16:
         raise ValueError("x must be bf16")
     _check(lib().zopt_act_pack(p, ld, out._c, _stream(stream)))
 
@@ -627,42 +657,48 @@ def act_pack(x, out: Act8, stream=None) -> None:
 def act_unpack(packed: Act8, out, stream=None) -> None:
     """``zopt_act_unpack``: out (bf16) = the values the checkpoint stands for."""
     p, ld = _matrix(out, packed.rows, packed.cols, "out")
-    if _dtype_code(out) != BF16:
+    if _code(out) != BF16:
         raise ValueError("out must be bf16")
     _check(lib().zopt_act_unpack(packed._c, p, ld, _stream(stream)))
 
 
-def _ffn_job(x, w_gate_up, w_down, act) -> _FfnJob:
+def _ffn_job(x, w_gate_up, w_down, act, kept=None, y=None, dy=None, dx=None, dw_gate_up=None, dw_down=None) -> _FfnJob:
     hidden, dim = w_down.shape
-    rows = x.rows if isinstance(x, Act8) else x.shape[0]
-    j = _FfnJob()
-    j.tokens, j.dim, j.hidden = rows, dim, hidden
-    j.act = _ACTS.get(act, act if isinstance(act, int) else -1)
-    j.w_gate_up, j.ld_gate_up = _matrix(w_gate_up, dim, 2 * hidden, "w_gate_up")
-    j.w_down, j.ld_down = _matrix(w_down, hidden, dim, "w_down")
+    wgu, wd = _matrix(w_gate_up, dim, 2 * hidden, "w_gate_up"), _matrix(w_down, hidden, dim, "w_down")
+    dtype = _same_dtype(w_gate_up, w_down)
     if isinstance(x, Act8):
-        j.x8 = ctypes.pointer(x._c)
-        j.dtype = _same_dtype(w_gate_up, w_down)
+        rows, xp, x8 = x.rows, (None, 0), ctypes.pointer(x._c)
     else:
-        j.x, j.ld_x = _matrix(x, rows, dim, "x")
-        j.dtype = _same_dtype(x, w_gate_up, w_down)
-    return j
-
-
-def _ffn_kept(j: _FfnJob, kept) -> None:
+        rows, x8 = x.shape[0], None
+        xp = _matrix(x, rows, dim, "x")
+        if _code(x) != dtype:
+            dtype = -1
+    kp, kept8 = (None, 0), None
     if isinstance(kept, Act8):
-        j.kept8 = ctypes.pointer(kept._c)
+        kept8 = ctypes.pointer(kept._c)
     elif kept is not None:
-        if _dtype_code(kept) != BF16:
+        if _code(kept) != BF16:
             raise ValueError("kept must be bf16 or an Act8")
-        j.kept, j.ld_kept = _matrix(kept, j.tokens, 2 * j.hidden, "kept")
+        kp = _matrix(kept, rows, 2 * hidden, "kept")
+    more = []
+    for t, r, c, name in ((y, rows, dim, "y"), (dy, rows, dim, "dy"), (dx, rows, dim, "dx"),
+                          (dw_gate_up, dim, 2 * hidden, "dw_gate_up"), (dw_down, hidden, dim, "dw_down")):
+        if t is None:
+            more += (None, 0)
+        else:
+            more += _matrix(t, r, c, name)
+            if _code(t) != dtype:
+                dtype = -1
+    return _FfnJob(rows, dim, hidden, _ACTS.get(act, act if isinstance(act, int) else -1), dtype, *wgu, *wd, *xp, x8, *kp,
+                   kept8, *more)
 
 
 def ffn_workspace(x, w_gate_up, w_down, backward: bool = True, dy=None) -> int:
     """``zopt_ffn_workspace`` for these operands (x a bf16 matrix or an :class:`Act8`; dy, if it is
     not contiguous)."""
-    j = _ffn_job(x, w_gate_up, w_down, "silu")
-    j.ld_dy = j.dim if dy is None else _matrix(dy, j.tokens, j.dim, "dy")[1]
+    j = _ffn_job(x, w_gate_up, w_down, "silu", dy=dy)
+    if dy is None:
+        j.ld_dy = j.dim
     return int(lib().zopt_ffn_workspace(j, int(bool(backward))))
 
 
@@ -675,43 +711,43 @@ def new_ffn_workspace(x, w_gate_up, w_down, backward: bool = True, dy=None, devi
 def ffn_forward(x, w_gate_up, w_down, y, ws, *, kept=None, act: str = "silu", stream=None) -> None:
     """``zopt_ffn_forward``: y = (a(x Wgate) * (x Wup)) Wdown. ``kept`` takes gate and up for the
     backward: a bf16 matrix [tokens, 2 hidden], an :class:`Act8` of that shape in two parts, or None."""
-    j = _ffn_job(x, w_gate_up, w_down, act)
-    _ffn_kept(j, kept)
-    j.y, j.ld_y = _matrix(y, j.tokens, j.dim, "y")
-    if y.dtype != w_down.dtype:
-        j.dtype = -1
+    j = _ffn_job(x, w_gate_up, w_down, act, kept, y)
     _on_device(ws)
-    _check(lib().zopt_ffn_forward(j, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib().zopt_ffn_forward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def ffn_backward(dy, x, kept, w_gate_up, w_down, dx, dw_gate_up, dw_down, ws, *, act: str = "silu",
                  stream=None) -> None:
     """``zopt_ffn_backward`` from dy, x (bf16 or :class:`Act8`) and what the forward kept."""
-    j = _ffn_job(x, w_gate_up, w_down, act)
-    _ffn_kept(j, kept)
-    j.dy, j.ld_dy = _matrix(dy, j.tokens, j.dim, "dy")
-    j.dx, j.ld_dx = _matrix(dx, j.tokens, j.dim, "dx")
-    j.dw_gate_up, j.ld_dw_gate_up = _matrix(dw_gate_up, j.dim, 2 * j.hidden, "dw_gate_up")
-    j.dw_down, j.ld_dw_down = _matrix(dw_down, j.hidden, j.dim, "dw_down")
-    if _same_dtype(dy, dx, dw_gate_up, dw_down, w_down) != j.dtype:
-        j.dtype = -1
+    j = _ffn_job(x, w_gate_up, w_down, act, kept, None, dy, dx, dw_gate_up, dw_down)
     _on_device(ws)
-    _check(lib().zopt_ffn_backward(j, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib().zopt_ffn_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
-def _linear_ce_job(x, w) -> _LinearCeJob:
-    j = _LinearCeJob()
-    j.tokens, j.dim, j.vocab = x.shape[0], x.shape[1], w.shape[0]
-    j.x, j.ld_x = _matrix(x, j.tokens, j.dim, "x")
-    j.w, j.ld_w = _matrix(w, j.vocab, j.dim, "w")
-    j.dtype = _same_dtype(x, w)
-    return j
-
-
-def _vector(t, n: int, dtype, name: str):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} on the GPU")
+def _vector(t, n: int, code: int, name: str):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or not t.is_cuda or \
+            (_code(t) != code if code >= 0 else t.element_size() != 8 or t.is_floating_point()):
+        raise ValueError(f"{name} must be a contiguous {'fp32' if code >= 0 else 'int64'} vector of {n} on the GPU")
     return t.data_ptr()
+
+
+def _linear_ce_job(x, w, ignore_index=-100, target=None, loss=None, lse=None, dloss=None, dx=None, dw=None) -> _LinearCeJob:
+    tokens, dim = x.shape
+    vocab = w.shape[0]
+    dtype = _same_dtype(x, w)
+    more = []
+    for t, r, name in ((dx, tokens, "dx"), (dw, vocab, "dw")):
+        if t is None:
+            more += (None, 0)
+        else:
+            more += _matrix(t, r, dim, name)
+            if _code(t) != dtype:
+                dtype = -1
+    return _LinearCeJob(tokens, dim, vocab, ignore_index, *_matrix(x, tokens, dim, "x"), *_matrix(w, vocab, dim, "w"),
+                        None if target is None else _vector(target, tokens, -1, "target"),
+                        None if loss is None else _vector(loss, tokens, F32, "loss"),
+                        None if lse is None else _vector(lse, tokens, F32, "lse"),
+                        None if dloss is None else _vector(dloss, tokens, F32, "dloss"), *more, dtype, 0)
 
 
 def linear_ce_workspace(x, w, backward: bool = True) -> int:
@@ -728,33 +764,17 @@ def new_linear_ce_workspace(x, w, backward: bool = True, device="cuda"):
 def linear_ce_forward(x, w, target, loss, lse, ws, *, ignore_index: int = -100, stream=None) -> None:
     """``zopt_linear_ce_forward``: each row's loss and log-sum-exp (fp32) of the logits x w' against
     target (int64), without storing the logits."""
-    import torch
-    j = _linear_ce_job(x, w)
-    j.ignore_index = int(ignore_index)
-    j.target = _vector(target, j.tokens, torch.int64, "target")
-    j.loss = _vector(loss, j.tokens, torch.float32, "loss")
-    j.lse = _vector(lse, j.tokens, torch.float32, "lse")
+    j = _linear_ce_job(x, w, ignore_index, target, loss, lse)
     _on_device(ws)
-    _check(lib().zopt_linear_ce_forward(j, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib().zopt_linear_ce_forward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def linear_ce_backward(x, w, target, lse, dloss, dx, dw, ws, *, ignore_index: int = -100, stream=None) -> None:
     """``zopt_linear_ce_backward``: dx and dw (either may be None) from the forward's lse and the
     gradient dloss (fp32) of each row's loss."""
-    import torch
-    j = _linear_ce_job(x, w)
-    j.ignore_index = int(ignore_index)
-    j.target = _vector(target, j.tokens, torch.int64, "target")
-    j.lse = _vector(lse, j.tokens, torch.float32, "lse")
-    j.dloss = _vector(dloss, j.tokens, torch.float32, "dloss")
-    if dx is not None:
-        j.dx, j.ld_dx = _matrix(dx, j.tokens, j.dim, "dx")
-    if dw is not None:
-        j.dw, j.ld_dw = _matrix(dw, j.vocab, j.dim, "dw")
-    if any(t is not None and t.dtype != x.dtype for t in (dx, dw)):
-        j.dtype = -1
+    j = _linear_ce_job(x, w, ignore_index, target, None, lse, dloss, dx, dw)
     _on_device(ws)
-    _check(lib().zopt_linear_ce_backward(j, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib().zopt_linear_ce_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def take_device_error() -> int:

@@ -1,8 +1,9 @@
 // Packing activations into 8-bit checkpoints and unpacking them (the format: act8.cuh).
 //
-// Both are one pass at HBM's rate: 3 bytes an entry, plus a byte per block of 128. Sixteen lanes
-// own a block, eight columns each: one 16-byte load, the block's largest magnitude by four
-// shuffles, one 8-byte store. A warp takes two blocks side by side.
+// Both are one pass, bound by HBM: 3 bytes an entry, plus a byte per block of 128. A block belongs to
+// 16 lanes (eight columns each: one 16-byte load, four shuffles for its largest magnitude, one 8-byte
+// store) or, where rows or parts do not start on such pieces, to 32 lanes with pieces of four, two
+// or one columns. A warp has kSteps groups of loads in flight before it works on the first.
 #include <cuda_runtime.h>
 
 #include <string>
@@ -16,111 +17,166 @@ namespace zopt {
 namespace act8 {
 namespace {
 
+// n / d for n < 2^31 by a multiplication (division by invariant integers, Granlund and Montgomery).
+struct Divisor {
+  uint32_t d, m, s;
+  explicit Divisor(uint32_t d_ = 1) : d(d_), m(0), s(0) {
+    while (s < 32 && (1ull << s) < d) ++s;
+    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
 struct Args {
   uint16_t* x;  // pack: read; unpack: written
   long long ld;
   uint8_t* q;
   uint8_t* scale;
-  long long rows, cols, width;  // width: a part's columns
-  int parts;
-  long long nb;  // blocks per part
-  int vec;       // every block of a row starts on 16 bytes of x and 8 of q
+  long long cols;
+  uint32_t blocks;  // of all rows
+  int width;        // a part's columns
+  Divisor per_row, per_part;
 };
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+template <int V>
+struct Pieces;  // V bf16 values and V bytes
+template <>
+struct Pieces<8> {
+  using X = uint4;
+  using Q = uint2;
+};
+template <>
+struct Pieces<4> {
+  using X = uint2;
+  using Q = uint32_t;
+};
+template <>
+struct Pieces<2> {
+  using X = uint32_t;
+  using Q = uint16_t;
+};
+template <>
+struct Pieces<1> {
+  using X = uint16_t;
+  using Q = uint8_t;
+};
 
-template <bool kPack>
+// V: the columns of a piece; a lane has 8 columns of a block (V = 8) or 4 (V = 4, 2, 1: 1, 2, 4 pieces).
+template <bool kPack, int V>
 __global__ void __launch_bounds__(256) act8_kernel(const Args a) {
+  using X = typename Pieces<V>::X;
+  using Q = typename Pieces<V>::Q;
+  constexpr int kMine = V == 8 ? 8 : 4, kPieces = kMine / V, kLanes = kBlock / kMine, kPerWarp = 32 / kLanes;
+  constexpr int kSteps = 4;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const long long per_row = a.parts * a.nb, blocks = a.rows * per_row;
-  const int sub = threadIdx.x & 15;
-  const long long step = static_cast<long long>(gridDim.x) * (blockDim.x / 16);
-  // both halves of a warp run the same number of rounds (the shuffles name every lane)
-  long long b = static_cast<long long>(blockIdx.x) * (blockDim.x / 16) + (threadIdx.x >> 4);
-  const long long first = b - ((threadIdx.x >> 4) & 1);
-  for (long long f = first; f < blocks; f += step, b += step) {
-    const bool live = b < blocks;
-    const long long row = live ? b / per_row : 0, r = live ? b - row * per_row : 0;
-    const long long part = r / a.nb, k = r - part * a.nb;
-    const long long c = k * kBlock + 8 * sub;  // the lane's first column within the part
-    const int n = live ? static_cast<int>(min(8LL, max(0LL, a.width - c))) : 0;
-    uint16_t* x = a.x + row * a.ld + part * a.width + c;
-    uint8_t* q = a.q + row * a.cols + part * a.width + c;
-    if (kPack) {
-      float v[8];
-      if (n == 8 && a.vec) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(x));
-        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-        v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-      } else {
+  const int sub = threadIdx.x % kLanes, lane_block = (threadIdx.x & 31) / kLanes;
+  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = (gridDim.x * blockDim.x) >> 5;
+  // (the bound is warp-uniform: the shuffles name every lane)
+  for (uint32_t b0 = warp * kPerWarp; b0 < a.blocks; b0 += kSteps * warps * kPerWarp) {
+    X xv[kSteps][kPieces];
+    Q qv[kSteps][kPieces];
+    long long xo[kSteps], qo[kSteps];  // the lane's first piece
+    int n[kSteps];                     // its columns from there to the part's end
+    uint32_t e[kSteps];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) v[t] = t < n ? __uint_as_float(static_cast<uint32_t>(x[t]) << 16) : 0.0f;
+    for (int i = 0; i < kSteps; ++i) {
+      const uint32_t b = b0 + i * warps * kPerWarp + lane_block;
+      n[i] = 0;
+      e[i] = 1;
+      if (b < a.blocks && b >= b0) {
+        const uint32_t row = a.per_row(b), r = b - row * a.per_row.d, part = a.per_part(r), k = r - part * a.per_part.d;
+        const int c = static_cast<int>(k) * kBlock + V * sub;
+        n[i] = a.width - c;
+        const long long col = static_cast<long long>(part) * a.width + c;
+        xo[i] = row * a.ld + col;
+        qo[i] = row * a.cols + col;
+        if (!kPack) e[i] = __ldg(a.scale + b);
       }
-      float amax = 0.0f;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) amax = amax_step(amax, v[t]);
-#pragma unroll
-      for (int d = 8; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-      const uint32_t e = exponent_byte(amax);
-      const float inv = inv_scale(e);
-      const uint32_t lo = encode4(v[0], v[1], v[2], v[3], inv), hi = encode4(v[4], v[5], v[6], v[7], inv);
-      if (n == 8 && a.vec) {
-        *reinterpret_cast<uint2*>(q) = make_uint2(lo, hi);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (t < n) q[t] = static_cast<uint8_t>((t < 4 ? lo : hi) >> (8 * (t & 3)));
+      for (int p = 0; p < kPieces; ++p) {
+        const int at = p * V * kLanes;
+        if (kPack) {
+          xv[i][p] = X{};
+          if (at + V <= n[i]) xv[i][p] = __ldcs(reinterpret_cast<const X*>(a.x + xo[i] + at));
+        } else {
+          qv[i][p] = Q{};
+          if (at + V <= n[i]) qv[i][p] = __ldcs(reinterpret_cast<const Q*>(a.q + qo[i] + at));
+        }
       }
-      if (live && sub == 0) a.scale[b] = static_cast<uint8_t>(e);
-    } else {
-      const float sc = scale(live ? a.scale[b] : 1u);
-      uint32_t w[2] = {0, 0};
-      if (n == 8 && a.vec) {
-        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
-        w[0] = u.x, w[1] = u.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (kPack) {
+        float v[kMine], amax = 0.0f;
+#pragma unroll
+        for (int t = 0; t < kMine; ++t) {
+          const uint16_t* h = reinterpret_cast<const uint16_t*>(&xv[i][t / V]);
+          v[t] = __uint_as_float(static_cast<uint32_t>(h[t % V]) << 16);
+          amax = amax_step(amax, v[t]);
+        }
+#pragma unroll
+        for (int d = kLanes / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        e[i] = exponent_byte(amax);
+        const float inv = inv_scale(e[i]);
+        uint32_t w[kMine / 4];
+#pragma unroll
+        for (int t = 0; t < kMine / 4; ++t) w[t] = encode4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p) {
+          const int at = p * V * kLanes;
+          if (at + V <= n[i]) *reinterpret_cast<Q*>(a.q + qo[i] + at) = *reinterpret_cast<const Q*>(reinterpret_cast<const uint8_t*>(w) + p * V);
+        }
+        const uint32_t b = b0 + i * warps * kPerWarp + lane_block;
+        if (sub == 0 && b < a.blocks && b >= b0) a.scale[b] = static_cast<uint8_t>(e[i]);
       } else {
+        const float sc = scale(e[i]);
+        uint32_t w[kMine / 4], o[kMine / 2];
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (t < n) w[t >> 2] |= static_cast<uint32_t>(q[t]) << (8 * (t & 3));
-      }
-      uint32_t o[4];
+        for (int p = 0; p < kPieces; ++p) *reinterpret_cast<Q*>(reinterpret_cast<uint8_t*>(w) + p * V) = qv[i][p];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float2 f = decode2(w[t >> 1] >> (16 * (t & 1)));
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-        o[t] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      if (n == 8 && a.vec) {
-        *reinterpret_cast<uint4*>(x) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
+        for (int t = 0; t < kMine / 2; ++t) {
+          const float2 f = decode2(w[t >> 1] >> (16 * (t & 1)));
+          const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+          o[t] = *reinterpret_cast<const uint32_t*>(&h);
+        }
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-          if (t < n) x[t] = static_cast<uint16_t>(o[t >> 1] >> (16 * (t & 1)));
+        for (int p = 0; p < kPieces; ++p) {
+          const int at = p * V * kLanes;
+          if (at + V <= n[i]) *reinterpret_cast<X*>(a.x + xo[i] + at) = *reinterpret_cast<const X*>(reinterpret_cast<const uint8_t*>(o) + 2 * p * V);
+        }
       }
     }
   }
 }
 
+template <int V>
+zopt_status launch(bool pack, const Args& a, int sms, cudaStream_t s) {
+  constexpr long long kPerCta = 8 * (V == 8 ? 2 : 1) * 4;  // blocks a CTA takes at a time
+  const long long want = (a.blocks + kPerCta - 1) / kPerCta, most = 8LL * sms;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+  return pack ? launch_pdl(act8_kernel<true, V>, grid, dim3(256), 0, s, a)
+              : launch_pdl(act8_kernel<false, V>, grid, dim3(256), 0, s, a);
+}
+
 zopt_status run(const char* fn, bool pack, const uint16_t* x, long long ld, const zopt_act8& c, cudaStream_t s) {
-  Args a;
-  a.x = const_cast<uint16_t*>(x);
-  a.ld = ld;
-  a.q = c.q;
-  a.scale = c.scale;
-  a.rows = c.rows;
-  a.cols = c.cols;
-  a.parts = c.parts;
-  a.width = c.cols / c.parts;
-  a.nb = blocks_of(a.width);
-  a.vec = ld % 8 == 0 && c.cols % 8 == 0 && a.width % 8 == 0;
   const int sms = sm_count();
   if (sms < 1) return fail(ZOPT_ECUDA, std::string(fn) + ": no CUDA device");
-  const long long want = (a.rows * a.parts * a.nb + 15) / 16, most = 16LL * sms;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
-  return pack ? launch_pdl(act8_kernel<true>, grid, dim3(256), 0, s, a)
-              : launch_pdl(act8_kernel<false>, grid, dim3(256), 0, s, a);
+  const long long width = c.cols / c.parts, nb = blocks_of(width), per_row = c.parts * nb;
+  const unsigned mis = static_cast<unsigned>(ld | c.cols | width);  // (x and q start on 16 bytes)
+  const long long most_rows = (1LL << 30) / per_row;                // block numbers of a launch stay below 2^30
+  for (long long r0 = 0; r0 < c.rows; r0 += most_rows) {
+    const long long rows = c.rows - r0 < most_rows ? c.rows - r0 : most_rows;
+    Args a{const_cast<uint16_t*>(x) + r0 * ld, ld, c.q + r0 * c.cols, c.scale + r0 * per_row, c.cols,
+           static_cast<uint32_t>(rows * per_row), static_cast<int>(width), Divisor(static_cast<uint32_t>(per_row)),
+           Divisor(static_cast<uint32_t>(nb))};
+    const zopt_status st = mis % 8 == 0   ? launch<8>(pack, a, sms, s)
+                           : mis % 4 == 0 ? launch<4>(pack, a, sms, s)
+                           : mis % 2 == 0 ? launch<2>(pack, a, sms, s)
+                                          : launch<1>(pack, a, sms, s);
+    if (st != ZOPT_OK) return st;
+  }
+  return ok();
 }
 
 zopt_status call(const char* fn, bool pack, const uint16_t* x, int64_t ld, const zopt_act8* c, zopt_stream stream) {
