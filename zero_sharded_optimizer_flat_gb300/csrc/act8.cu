@@ -1,9 +1,10 @@
 // Packing activations into 8-bit checkpoints and unpacking them (the format: act8.cuh).
 //
 // Both are one pass, bound by HBM: 3 bytes an entry, plus a byte per block of 128. A block belongs to
-// 16 lanes (eight columns each: one 16-byte load, four shuffles for its largest magnitude, one 8-byte
-// store) or, where rows or parts do not start on such pieces, to 32 lanes with pieces of four, two
-// or one columns. A warp has kSteps groups of loads in flight before it works on the first.
+// eight lanes, each with pieces of eight columns (16-byte loads, three shuffles for the block's
+// largest magnitude) or, where rows or parts do not start on such pieces, of four columns, to 16
+// lanes with pieces of two or 32 with single ones. A lane's loads for kSteps blocks are in flight
+// before it works on the first.
 #include <cuda_runtime.h>
 
 #include <string>
@@ -61,21 +62,34 @@ struct Pieces<1> {
   using Q = uint8_t;
 };
 
-// V: the columns of a piece; a lane has 8 columns of a block (V = 8) or 4 (V = 4, 2, 1: 1, 2, 4 pieces).
+// The largest magnitude bits of the bf16 values in `w` (two a word), as bf16 bits in both halves.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// V: the columns of a piece; a lane has kMine columns of a block, in pieces V * kLanes apart.
 template <bool kPack, int V>
 __global__ void __launch_bounds__(256) act8_kernel(const Args a) {
   using X = typename Pieces<V>::X;
   using Q = typename Pieces<V>::Q;
-  constexpr int kMine = V == 8 ? 8 : 4, kPieces = kMine / V, kLanes = kBlock / kMine, kPerWarp = 32 / kLanes;
-  constexpr int kSteps = 4;
+  constexpr int kMine = V >= 4 ? 16 : 4 * V, kPieces = kMine / V, kLanes = kBlock / kMine, kPerWarp = 32 / kLanes;
+  constexpr int kSteps = V >= 4 ? 2 : 4;
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int sub = threadIdx.x % kLanes, lane_block = (threadIdx.x & 31) / kLanes;
   const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, warps = (gridDim.x * blockDim.x) >> 5;
   // (the bound is warp-uniform: the shuffles name every lane)
   for (uint32_t b0 = warp * kPerWarp; b0 < a.blocks; b0 += kSteps * warps * kPerWarp) {
-    X xv[kSteps][kPieces];
-    Q qv[kSteps][kPieces];
+    union {
+      X x[kPieces];
+      uint32_t w[(kMine + 1) / 2];
+    } xv[kSteps];
+    union {
+      Q q[kPieces];
+      uint32_t w[kMine / 4];
+    } qv[kSteps];
     long long xo[kSteps], qo[kSteps];  // the lane's first piece
     int n[kSteps];                     // its columns from there to the part's end
     uint32_t e[kSteps];
@@ -97,53 +111,64 @@ __global__ void __launch_bounds__(256) act8_kernel(const Args a) {
       for (int p = 0; p < kPieces; ++p) {
         const int at = p * V * kLanes;
         if (kPack) {
-          xv[i][p] = X{};
-          if (at + V <= n[i]) xv[i][p] = __ldcs(reinterpret_cast<const X*>(a.x + xo[i] + at));
+          xv[i].x[p] = X{};
+          if (at + V <= n[i]) xv[i].x[p] = __ldcs(reinterpret_cast<const X*>(a.x + xo[i] + at));
         } else {
-          qv[i][p] = Q{};
-          if (at + V <= n[i]) qv[i][p] = __ldcs(reinterpret_cast<const Q*>(a.q + qo[i] + at));
+          qv[i].q[p] = Q{};
+          if (at + V <= n[i]) qv[i].q[p] = __ldcs(reinterpret_cast<const Q*>(a.q + qo[i] + at));
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (kPack) {
-        float v[kMine], amax = 0.0f;
+        // magnitudes compare as integers; a block that has an inf or NaN (bits from 0x7F80 on) is
+        // gone through again without them
+        uint32_t top = 0;
 #pragma unroll
-        for (int t = 0; t < kMine; ++t) {
-          const uint16_t* h = reinterpret_cast<const uint16_t*>(&xv[i][t / V]);
-          v[t] = __uint_as_float(static_cast<uint32_t>(h[t % V]) << 16);
-          amax = amax_step(amax, v[t]);
+        for (int t = 0; t < kMine / 2; ++t) top = max2(top, xv[i].w[t] & 0x7FFF7FFFu);
+        top = max2(top, (top >> 16) | (top << 16));
+        const bool odd = (top & 0xFFFFu) >= 0x7F80u;
+        if (odd) {
+          top = 0;
+#pragma unroll
+          for (int t = 0; t < kMine; ++t) {
+            const uint32_t m = (xv[i].w[t / 2] >> (16 * (t & 1))) & 0x7FFFu;
+            if (m < 0x7F80u && m > top) top = m;
+          }
+          top |= top << 16;
         }
 #pragma unroll
-        for (int d = kLanes / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        e[i] = exponent_byte(amax);
+        for (int d = kLanes / 2; d >= 1; d >>= 1) top = max2(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        e[i] = exponent_byte(__uint_as_float(top << 16));
         const float inv = inv_scale(e[i]);
-        uint32_t w[kMine / 4];
 #pragma unroll
-        for (int t = 0; t < kMine / 4; ++t) w[t] = encode4(v[4 * t], v[4 * t + 1], v[4 * t + 2], v[4 * t + 3], inv);
+        for (int t = 0; t < kMine / 4; ++t) {
+          const uint32_t lo = xv[i].w[2 * t], hi = xv[i].w[2 * t + 1];
+          const float x0 = __uint_as_float(lo << 16), x1 = __uint_as_float(lo & 0xFFFF0000u);
+          const float x2 = __uint_as_float(hi << 16), x3 = __uint_as_float(hi & 0xFFFF0000u);
+          qv[i].w[t] = odd ? encode4(x0, x1, x2, x3, inv)
+                           : encode_finite2(x0 * inv, x1 * inv) | (encode_finite2(x2 * inv, x3 * inv) << 16);
+        }
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
           const int at = p * V * kLanes;
-          if (at + V <= n[i]) *reinterpret_cast<Q*>(a.q + qo[i] + at) = *reinterpret_cast<const Q*>(reinterpret_cast<const uint8_t*>(w) + p * V);
+          if (at + V <= n[i]) *reinterpret_cast<Q*>(a.q + qo[i] + at) = qv[i].q[p];
         }
         const uint32_t b = b0 + i * warps * kPerWarp + lane_block;
         if (sub == 0 && b < a.blocks && b >= b0) a.scale[b] = static_cast<uint8_t>(e[i]);
       } else {
         const float sc = scale(e[i]);
-        uint32_t w[kMine / 4], o[kMine / 2];
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) *reinterpret_cast<Q*>(reinterpret_cast<uint8_t*>(w) + p * V) = qv[i][p];
 #pragma unroll
         for (int t = 0; t < kMine / 2; ++t) {
-          const float2 f = decode2(w[t >> 1] >> (16 * (t & 1)));
+          const float2 f = decode2(qv[i].w[t >> 1] >> (16 * (t & 1)));
           const __nv_bfloat162 h = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-          o[t] = *reinterpret_cast<const uint32_t*>(&h);
+          xv[i].w[t] = *reinterpret_cast<const uint32_t*>(&h);
         }
 #pragma unroll
         for (int p = 0; p < kPieces; ++p) {
           const int at = p * V * kLanes;
-          if (at + V <= n[i]) *reinterpret_cast<X*>(a.x + xo[i] + at) = *reinterpret_cast<const X*>(reinterpret_cast<const uint8_t*>(o) + 2 * p * V);
+          if (at + V <= n[i]) *reinterpret_cast<X*>(a.x + xo[i] + at) = xv[i].x[p];
         }
       }
     }
@@ -152,7 +177,7 @@ __global__ void __launch_bounds__(256) act8_kernel(const Args a) {
 
 template <int V>
 zopt_status launch(bool pack, const Args& a, int sms, cudaStream_t s) {
-  constexpr long long kPerCta = 8 * (V == 8 ? 2 : 1) * 4;  // blocks a CTA takes at a time
+  constexpr long long kPerCta = 8 * (V >= 4 ? 4 * 2 : V * 4);  // blocks a CTA takes at a time
   const long long want = (a.blocks + kPerCta - 1) / kPerCta, most = 8LL * sms;
   const dim3 grid(static_cast<unsigned>(want < most ? want : most));
   return pack ? launch_pdl(act8_kernel<true, V>, grid, dim3(256), 0, s, a)

@@ -40,7 +40,11 @@ __device__ __forceinline__ uint32_t exponent_byte(float amax) {
 __device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 __device__ __forceinline__ float scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Two entries as e4m3, the first in the low byte.
+// Two finite entries, already scaled, as e4m3, the first in the low byte.
+__device__ __forceinline__ uint32_t encode_finite2(float a, float b) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
+}
+// Two entries as e4m3, inf and NaN as NaN.
 __device__ __forceinline__ uint32_t encode2(float a, float b, float inv) {
   const float nan = __uint_as_float(0x7FC00000u);
   const float2 v = make_float2(finite(a) ? a * inv : nan, finite(b) ? b * inv : nan);
