@@ -258,10 +258,10 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
     j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.hidden), j.K = static_cast<int>(c.dim);
     j.b_mn = 1;
     j.q_up = static_cast<int>(in.up);
-    set_tiles(j);
     glu_fields(j, c);
-    TRY(map_operand(fn, &j.P, in.x, c.tokens, c.dim, in.px, false));
-    TRY(map_operand(fn, &j.Q, in.gate_up, in.up + c.hidden, c.dim, in.pgu, true));
+    set_tiles(j);
+    TRY(map_p(fn, j, in.x, in.px));
+    TRY(map_q(fn, j, in.gate_up, in.up + c.hidden, in.pgu));
     j.out = h;
     j.ld_out = p.fp;
     TRY(launch(fn, b, kGluFwd, s));
@@ -271,8 +271,8 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
   b.n = 1;
   y_job(c, b.job[0]);
   plan_splits(b.job, 1);
-  TRY(map_operand(fn, &b.job[0].P, h, c.tokens, c.hidden, p.fp, false));
-  TRY(map_operand(fn, &b.job[0].Q, in.down, c.dim, c.hidden, in.pdown, true));
+  TRY(map_p(fn, b.job[0], h, p.fp));
+  TRY(map_q(fn, b.job[0], in.down, c.dim, in.pdown));
   SumBatch sums{};
   float* slab = reinterpret_cast<float*>(ws + p.slab);
   finish(b.job[0], c.y, c.ld_y, slab, sums);
@@ -306,10 +306,10 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
     // over the padded width: down's missing rows read as zero, so the pad columns become zero and
     // may stand in the inner length of dx
     j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(p.fp), j.K = static_cast<int>(c.dim);
-    set_tiles(j);
     glu_fields(j, c);
-    TRY(map_operand(fn, &j.P, in.dy, c.tokens, c.dim, in.pdy, false));
-    TRY(map_operand(fn, &j.Q, in.down, c.hidden, c.dim, in.pdown, false));
+    set_tiles(j);
+    TRY(map_p(fn, j, in.dy, in.pdy));
+    TRY(map_q(fn, j, in.down, c.hidden, in.pdown));
     j.out = dgu;
     j.ld_out = 2 * p.fp;
     j.out_h = h;
@@ -322,17 +322,17 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
   plan_splits(jobs, n);
   SumBatch sums{};
   float* slab = reinterpret_cast<float*>(ws + p.slab);
-  TRY(map_operand(fn, &jobs[0].P, dgu, c.tokens, 2 * p.fp, 2 * p.fp, false));
-  TRY(map_operand(fn, &jobs[0].Q, in.gate_up, c.dim, 2 * p.fp, in.pgu, false));
+  TRY(map_p(fn, jobs[0], dgu, 2 * p.fp));
+  TRY(map_q(fn, jobs[0], in.gate_up, c.dim, in.pgu));
   finish(jobs[0], c.dx, c.ld_dx, slab, sums);
   for (int k = 1; k + 1 < n; ++k) {  // the gate's and up's columns together, or apart
     const int up = k - 1;
-    TRY(map_operand(fn, &jobs[k].P, in.x, c.dim, c.tokens, in.px, true));
-    TRY(map_operand(fn, &jobs[k].Q, dgu + up * p.fp, jobs[k].N, c.tokens, 2 * p.fp, true));
+    TRY(map_p(fn, jobs[k], in.x, in.px));
+    TRY(map_q(fn, jobs[k], dgu + up * p.fp, jobs[k].N, 2 * p.fp));
     finish(jobs[k], c.dw_gate_up + up * c.hidden, c.ld_dw_gate_up, slab, sums);
   }
-  TRY(map_operand(fn, &jobs[n - 1].P, h, c.hidden, c.tokens, p.fp, true));
-  TRY(map_operand(fn, &jobs[n - 1].Q, in.dy, c.dim, c.tokens, in.pdy, true));
+  TRY(map_p(fn, jobs[n - 1], h, p.fp));
+  TRY(map_q(fn, jobs[n - 1], in.dy, c.dim, in.pdy));
   finish(jobs[n - 1], c.dw_down, c.ld_dw_down, slab, sums);
   // The longest units first: the launch's end is then made of short ones.
   const bool dx_first = jobs[0].kb_per_split >= jobs[1].kb_per_split;

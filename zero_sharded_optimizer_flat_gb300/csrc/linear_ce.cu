@@ -76,7 +76,7 @@ CePlan plan(const zopt_linear_ce_job& c, bool backward) {
   if (p.stage_x) p.xs = take(at, T * p.pitch * 2);
   if (p.stage_w) p.ws = take(at, V * p.pitch * 2);
   const size_t shared = at;
-  p.part = take(at, 2 * ((V + kTileN - 1) / kTileN) * T * 8);
+  p.part = take(at, 2 * ((V + 127) / 128) * T * 8);  // (of tiles of 128 columns)
   p.tlogit = take(at, T * 4);
   p.total = at;
   if (!backward) return p;
@@ -264,10 +264,10 @@ zopt_status forward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, c
   ce_fields(j, c);
   j.part = reinterpret_cast<float2*>(ws + p.part);
   j.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
-  TRY(map_operand(fn, &j.P, x, c.tokens, c.dim, px, false));
-  TRY(map_operand(fn, &j.Q, w, c.vocab, c.dim, pw, false));
+  TRY(map_p(fn, j, x, px));
+  TRY(map_q(fn, j, w, c.vocab, pw));
   TRY(launch(fn, b, kCeFwd, s));
-  const int parts = static_cast<int>((c.vocab + 127) / 128);
+  const int parts = static_cast<int>((c.vocab + j.tile_n / 2 - 1) / (j.tile_n / 2));
   return launch_pdl(ce_join_kernel, dim3(static_cast<unsigned>((c.tokens + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
                     static_cast<const float2*>(j.part), parts, static_cast<long long>(c.tokens), c.target,
                     c.ignore_index, c.vocab, static_cast<const float*>(j.tlogit), c.loss, c.lse);
@@ -309,8 +309,8 @@ zopt_status backward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, 
     ce_fields(j, c);
     j.col0 = v0;
     j.unit = unit;
-    TRY(map_operand(fn, &j.P, x, c.tokens, c.dim, px, false));
-    TRY(map_operand(fn, &j.Q, w + v0 * pw, vc, c.dim, pw, false));
+    TRY(map_p(fn, j, x, px));
+    TRY(map_q(fn, j, w + v0 * pw, vc, pw));
     j.out = dl_of(i);
     j.ld_out = p.piece;
     return ok();
@@ -353,11 +353,11 @@ zopt_status backward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, 
       uint16_t* out = is_dw ? c.dw + v0 * c.ld_dw : c.dx;
       const long long ld = is_dw ? c.ld_dw : c.ld_dx;
       if (is_dw) {
-        TRY(map_operand(fn, &j.P, dl_of(i), vc, c.tokens, p.piece, true));
-        TRY(map_operand(fn, &j.Q, xm, c.dim, c.tokens, p.pitch, true));
+        TRY(map_p(fn, j, dl_of(i), p.piece));
+        TRY(map_q(fn, j, xm, c.dim, p.pitch));
       } else {
-        TRY(map_operand(fn, &j.P, dl_of(i), c.tokens, vc, p.piece, false));
-        TRY(map_operand(fn, &j.Q, w + v0 * pw, c.dim, vc, pw, true));
+        TRY(map_p(fn, j, dl_of(i), p.piece));
+        TRY(map_q(fn, j, w + v0 * pw, c.dim, pw));
       }
       if (j.splits > 1) {
         j.out_mode = kOutF32;

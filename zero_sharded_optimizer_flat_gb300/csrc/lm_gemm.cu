@@ -11,6 +11,7 @@
 // row pieces, so softmax statistics and the 8-bit blocks need no exchange between lanes.
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cudaTypedefs.h>
 
@@ -217,6 +218,12 @@ __device__ __forceinline__ Unit unit_of(const Job& j, int u) {
   w.kb1 = min(w.kb0 + j.kb_per_split, j.nk);
   return w;
 }
+// Pair p's i-th unit, or a number beyond the last.
+__device__ __forceinline__ int unit_at(const Batch& b, int pair, int npairs, int i) {
+  if (!b.listed) return pair + i * npairs;
+  const int at = b.first[pair] + i;
+  return at < b.first[pair + 1] ? b.order[at] : 0x7FFFFFFF;
+}
 __device__ __forceinline__ int job_of(const Batch& b, int t) {
   int j = 0;
   while (j + 1 < b.n && t >= b.start[j + 1]) ++j;
@@ -331,14 +338,15 @@ __device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Acc
   const int row = row0 + lane;
   const float alpha = j.alpha != nullptr && j.splits == 1 ? __ldcg(j.alpha) : 1.0f;
   const bool wide = j.out_mode == kOutF32;
+  const int width = j.tile_n >> 1;
   const Out<128> out(wide ? static_cast<void*>(static_cast<float*>(j.out) + w.split * j.split_stride) : j.out, j.ld_out,
-                     wide ? 4 : 2, row0, j.M, w.tj * kTileN + 128 * h, j.N, lane);
+                     wide ? 4 : 2, row0, j.M, w.tj * j.tile_n + width * h, j.N, lane);
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; 64 * half < width; ++half) {
     uint32_t v[2][32];
-    acc.read64(128 * h + 64 * half, v);
-    if (half == 1) acc.done();
-    const int col0 = w.tj * kTileN + 128 * h + 64 * half;
+    acc.read64(width * h + 64 * half, v);
+    if (64 * half + 64 == width) acc.done();
+    const int col0 = w.tj * j.tile_n + width * h + 64 * half;
     if (col0 >= j.N || row0 >= j.M) continue;  // (warp-uniform)
     if (j.add != nullptr && row < j.M) {
       const float* a = j.add + static_cast<long long>(row) * j.ld_add + col0;
@@ -386,12 +394,13 @@ __device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, const Ac
   const int row = row0 + lane;
   const long long tgt = row < j.M ? j.target[row] : -1;
   float m = -INFINITY, s = 0.0f;
+  const int width = j.tile_n >> 1;
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; 64 * half < width; ++half) {
     uint32_t v[2][32];
-    acc.read64(128 * h + 64 * half, v);
-    if (half == 1) acc.done();
-    const int col = w.tj * kTileN + 128 * h + 64 * half;
+    acc.read64(width * h + 64 * half, v);
+    if (64 * half + 64 == width) acc.done();
+    const int col = w.tj * j.tile_n + width * h + 64 * half;
     if (tgt >= col && tgt < col + 64 && tgt < j.N) {
       float t = 0.0f;
 #pragma unroll
@@ -441,7 +450,8 @@ __device__ __forceinline__ void epi_ce_fwd(const Job& j, const Unit& w, const Ac
 __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
                                            uint32_t box) {
   const int row = row0 + lane;
-  const Out<128> out(j.out, j.ld_out, 2, row0, j.M, w.tj * kTileN + 128 * h, j.N, lane);
+  const int width = j.tile_n >> 1;
+  const Out<128> out(j.out, j.ld_out, 2, row0, j.M, w.tj * j.tile_n + width * h, j.N, lane);
   long long tgt = j.ignore;
   float lse2 = 0.0f, dl = 0.0f;
   if (row < j.M) {
@@ -454,11 +464,11 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Ac
   const bool live = tgt != j.ignore;
   const long long at = tgt - j.col0;  // the target's column in this job
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
+  for (int half = 0; 64 * half < width; ++half) {
     uint32_t v[2][32];
-    acc.read64(128 * h + 64 * half, v);
-    if (half == 1) acc.done();
-    const int col = w.tj * kTileN + 128 * h + 64 * half;
+    acc.read64(width * h + 64 * half, v);
+    if (64 * half + 64 == width) acc.done();
+    const int col = w.tj * j.tile_n + width * h + 64 * half;
     if (col >= j.N || row0 >= j.M) continue;
     const F2 scale = f2(kLog2e, kLog2e), minus = f2(-lse2, -lse2), weight = f2(dl, dl);
     uint32_t words[32];
@@ -486,14 +496,15 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Ac
   }
 }
 
-// TMEM columns 0 .. 127 hold the gate, 128 .. 255 the up product of the same 128 hidden columns; the
-// warp's are 64 h .. 64 h + 63 of each. A tile is one 8-bit block wide: a block's largest magnitude
-// is found within a lane and its partner in the warp that has the other half, through `swap` (two
-// bytes a lane; the two warps share barrier `bar`).
+// The first half of a tile's TMEM columns hold the gate, the second the up product of the same 128 (or
+// 64) hidden columns; the warp's are half h of each. Where 8 bits are kept a tile is one block wide
+// (128): a block's largest magnitude is found within a lane and its partner in the warp that has the
+// other half, through `swap` (two bytes a lane; the two warps share barrier `bar`).
 template <int kAct, int kKept>
 __device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
                                             uint32_t box, uint16_t* swap, int bar) {
-  const int row = row0 + lane, n0 = w.tj * 128;
+  const int width = kKept == kKeep8 ? 128 : j.tile_n >> 1;  // hidden columns of a tile
+  const int row = row0 + lane, n0 = w.tj * width;
   if (row0 >= j.M) {  // (the partner warp has the same rows)
     acc.done();
     return;
@@ -528,18 +539,18 @@ __device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const A
     inv[0] = act8::inv_scale(e[0]), inv[1] = act8::inv_scale(e[1]);
   }
   constexpr int kSize = kKept == kKeep8 ? 1 : 2;
-  const int first = n0 + 64 * h;
+  const int first = n0 + (width >> 1) * h;
   const Out<64> out(j.out, j.ld_out, 2, row0, j.M, first, j.hidden, lane);
   Out<32 * kSize> gate_out(j.kept, j.ld_kept, kSize, row0, j.M, first, j.hidden, lane);
   Out<32 * kSize> up_out(static_cast<uint8_t*>(j.kept) + static_cast<long long>(j.hidden) * kSize, j.ld_kept, kSize, row0, j.M,
                          first, j.hidden, lane);
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
+  for (int c = 0; 64 * c < width; ++c) {
     uint32_t g[32], u[32];
-    tc::tmem_ld32(acc.base + static_cast<uint32_t>(64 * h + 32 * c), g);
-    tc::tmem_ld32(acc.base + static_cast<uint32_t>(128 + 64 * h + 32 * c), u);
+    tc::tmem_ld32(acc.base + static_cast<uint32_t>((width >> 1) * h + 32 * c), g);
+    tc::tmem_ld32(acc.base + static_cast<uint32_t>(width + (width >> 1) * h + 32 * c), u);
     tc::tmem_wait_ld();
-    if (c == 1) acc.done();
+    if (64 * c + 64 >= width) acc.done();
     if (first + 32 * c >= j.hidden) continue;
     if constexpr (kKept == kKeepBf16) {  // a box: a row's 32 gates, then its 32 ups
       uint32_t words[32];
@@ -662,20 +673,22 @@ template <int kAct, int kKept, bool kWide>
 __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
                                             uint32_t box, Kept<kKept>& k, Scales& sc, int next_row, int next_col) {
   const int row = row0 + lane;
-  const int col0 = w.tj * kTileN + 128 * h;
+  const int width = j.tile_n >> 1;
+  const int col0 = w.tj * j.tile_n + width * h;
   const Out<64> dgate(j.out, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> hout(j.out_h, j.N, 2, row0, j.M, col0, j.N, lane);
   Scales next_sc;
   if constexpr (kKept == kKeep8) next_sc.load(j, next_row, next_col);
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; 32 * c < width; ++c) {
     const int col = col0 + 32 * c;
+    const bool last = 32 * c + 32 == width;
     uint32_t v[32];
-    acc.read32(128 * h + 32 * c, v);
-    if (c == 3) acc.done();
+    acc.read32(width * h + 32 * c, v);
+    if (last) acc.done();
     Kept<kKept> next;
-    next.template load<kWide>(j, c < 3 ? row : next_row, c < 3 ? col + 32 : next_col);
+    next.template load<kWide>(j, last ? next_row : row, last ? next_col : col + 32);
     if (col < j.N && row0 < j.M) {
       uint32_t hh[16];
 #pragma unroll
@@ -771,7 +784,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t s = 0, ph = 1;
       long long done = 0;  // stages armed so far
       bool ok = true;
-      for (int t = pair; ok && t < total; t += npairs) {
+      for (int i = 0, t; ok && (t = unit_at(B, pair, npairs, i)) < total; ++i) {
         const int ji = job_of(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of(j, t - B.start[ji]);
@@ -779,18 +792,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const CUtensorMap* const Q = &j.Q;
         const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
         const int row0 = w.ti * kTileM + static_cast<int>(rank) * 128;  // this CTA's rows of P
-        int col0 = w.tj * kTileN + static_cast<int>(rank) * 128;        // this CTA's columns of Q
-        if ((kKinds & kGluFwd) && j.kind == kGluFwd) col0 = w.tj * 128 + (leader ? 0 : j.q_up);
+        const int width = j.tile_n >> 1;                                // this CTA's columns of Q
+        const bool wide = width == 128, has_a = leader || j.a_rows == 128;
+        const uint32_t tx = static_cast<uint32_t>(j.tx);
+        int col0 = w.tj * j.tile_n + static_cast<int>(rank) * width;
+        if ((kKinds & kGluFwd) && j.kind == kGluFwd) col0 = w.tj * width + (leader ? 0 : j.q_up);
         const int k_end = w.kb1 * kTileK;
         for (int k = w.kb0 * kTileK; k < k_end; k += kTileK) {
           if (!wait(empty0 + 8 * s, ph, err)) {
             ok = false;
             break;
           }
-          if (leader) tc::mbar_arrive_expect_tx(full + s, 4 * kHalfBytes);  // both CTAs' halves of P and Q
+          if (leader) tc::mbar_arrive_expect_tx(full + s, tx);  // both CTAs' halves of P and Q
           const uint32_t bar = lead0 + 8 * s, a = a0 + s * kHalfBytes, b = b0 + s * kHalfBytes;
           if (!amn) {
-            load_box(a, P, bar, k, row0);
+            // (a single tile of at most 128 rows: the other rows' accumulators are of no use to anyone)
+            if (has_a) load_box(a, P, bar, k, row0);
           } else {
             load_box(a, P, bar, row0, k);
             load_box(a + kMnBoxBytes, P, bar, row0 + 64, k);
@@ -799,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_box(b, Q, bar, k, col0);
           } else {
             load_box(b, Q, bar, col0, k);
-            load_box(b + kMnBoxBytes, Q, bar, col0 + 64, k);
+            if (wide) load_box(b + kMnBoxBytes, Q, bar, col0 + 64, k);
           }
           ++done;
           if (++s == kStages) {
@@ -820,12 +837,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int it = 0;
       bool ok = true;
       const uint32_t tempty0 = tc::smem_u32(tempty);
-      for (int t = pair; ok && t < total; t += npairs, ++it) {
+      for (int t; ok && (t = unit_at(B, pair, npairs, it)) < total; ++it) {
         const int ji = job_of(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of(j, t - B.start[ji]);
         const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
-        const uint32_t idesc = tc::idesc_bf16_f32(kTileM, kTileN, amn, bmn);
+        const uint32_t idesc = tc::idesc_bf16_f32(kTileM, j.tile_n, amn, bmn);
         // a stage's descriptors differ in the address alone (16-byte units), and so do a stage's steps
         const uint64_t ad0 = tc::smem_desc_sw128(tc::smem_u32(sA), amn ? kMnBoxBytes : 16u, 1024u);
         const uint64_t bd0 = tc::smem_desc_sw128(tc::smem_u32(sB), bmn ? kMnBoxBytes : 16u, 1024u);
@@ -875,20 +892,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Kept<kKept> kept;
     Scales scales;
     auto first_of = [&](int t, int& row, int& col) {  // the lane's row and the warp's first column of unit t (kGluBwd)
+      row = B.job[0].M, col = 0;
+      if (t >= total) return;
       const Unit w = unit_of(B.job[0], t);
-      row = t < total ? w.ti * kTileM + rows0 + lane : B.job[0].M;
-      col = w.tj * kTileN + 128 * half;
+      row = w.ti * kTileM + rows0 + lane;
+      col = w.tj * B.job[0].tile_n + (B.job[0].tile_n >> 1) * half;
     };
     if constexpr ((kKinds & kGluBwd) != 0) {
       int row, col;
-      first_of(pair, row, col);
+      first_of(unit_at(B, pair, npairs, 0), row, col);
       kept.template load<kWide>(B.job[0], row, col);
       if constexpr (kKept == kKeep8) scales.load(B.job[0], row, col);
     }
     int it = 0;
-    for (int t = pair; t < total; t += npairs, ++it) {
+    for (int t; (t = unit_at(B, pair, npairs, it)) < total;) {
       const int b = it & 1;
       const uint32_t tph = static_cast<uint32_t>(it >> 1) & 1u;
+      ++it;
       const int ji = job_of(B, t);
       const Job& j = B.job[ji];
       const Unit w = unit_of(j, t - B.start[ji]);
@@ -904,7 +924,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr ((kKinds & kGluFwd) != 0) epi_glu_fwd<kAct, kKept>(j, w, acc, row0, lane, half, box, swap, 1 + quad);
       if constexpr ((kKinds & kGluBwd) != 0) {
         int row, col;
-        first_of(t + npairs, row, col);
+        first_of(unit_at(B, pair, npairs, it), row, col);
         epi_glu_bwd<kAct, kKept, kWide>(j, w, acc, row0, lane, half, box, kept, scales, row, col);
       }
     }
@@ -1010,26 +1030,45 @@ zopt_status make_map(const char* fn, CUtensorMap* m, const void* base, long long
 }
 }  // namespace
 
-zopt_status map_operand(const char* fn, CUtensorMap* m, const void* base, long long mn, long long k, long long pitch,
-                        bool mn_major) {
-  return mn_major ? make_map(fn, m, base, mn, k, pitch, 64) : make_map(fn, m, base, k, mn, pitch, 128);
+zopt_status map_p(const char* fn, Job& j, const void* base, long long pitch) {
+  return j.a_mn ? make_map(fn, &j.P, base, j.M, j.K, pitch, 64) : make_map(fn, &j.P, base, j.K, j.M, pitch, j.a_rows);
+}
+zopt_status map_q(const char* fn, Job& j, const void* base, long long columns, long long pitch) {
+  return j.b_mn ? make_map(fn, &j.Q, base, columns, j.K, pitch, 64)
+                : make_map(fn, &j.Q, base, j.K, columns, pitch, j.tile_n / 2);
 }
 
 void set_tiles(Job& j) {
-  const int width = j.kind == kGluFwd ? 128 : kTileN;
   j.tiles_m = (j.M + kTileM - 1) / kTileM;
-  j.tiles_n = (j.N + width - 1) / width;
   j.nk = (j.K + kTileK - 1) / kTileK;
   j.kb_per_split = j.nk;
   j.splits = 1;
+  auto columns = [&](int tile_n) {
+    const int width = j.kind == kGluFwd ? tile_n / 2 : tile_n;
+    return (j.N + width - 1) / width;
+  };
+  // Tiles half as wide cost more than half as much (P is read again for each: 0.7 of a k-block's
+  // time, and half of an epilogue's, which counts as 16 k-blocks), but where there are few of the
+  // wide ones they keep twice as many pairs busy. kStore cuts its inner length instead, and a tile
+  // that makes 8-bit blocks has to be one block wide.
+  j.tile_n = kTileN;
+  if (j.kind != kStore && !(j.kind == kGluFwd && j.kept_mode == kKeep8)) {
+    auto waves = [&](int tile_n) { return (static_cast<long long>(j.tiles_m) * columns(tile_n) + kPairs - 1) / kPairs; };
+    if (waves(128) * (0.7 * j.nk + 8) < waves(256) * (1.0 * j.nk + 16)) j.tile_n = 128;
+  }
+  j.tiles_n = columns(j.tile_n);
+  // P's rows beyond M are not loaded where a single box holds them all: loads of rows that are not
+  // there take the TMA longer than loads of rows that are.
+  j.a_rows = !j.a_mn && j.M <= 128 ? (j.M + 7) / 8 * 8 : 128;
+  j.tx = (j.a_rows < 128 ? j.a_rows : 256) * kTileK * 2 + j.tile_n * kTileK * 2;
   // The larger operand is streamed once: tiles that run together share its rows (or columns) and
   // walk the smaller one, which stays in L2.
   j.rows_fast = j.N >= j.M ? 1 : 0;
 }
 
 void plan_splits(Job* jobs, int n) {
-  // GB300's 76 CTA pairs. Fewer than four k-blocks a unit is not worth a partial sum.
-  constexpr long long kPairs = 76, kLeast = 4;
+  // Fewer than four k-blocks a unit is not worth a partial sum.
+  constexpr long long kLeast = 4;
   long long work = 0;
   for (int i = 0; i < n; ++i) work += static_cast<long long>(jobs[i].tiles_m) * jobs[i].tiles_n * jobs[i].nk;
   const long long share = (work + kPairs - 1) / kPairs;
@@ -1037,10 +1076,44 @@ void plan_splits(Job* jobs, int n) {
   for (int i = 0; i < n; ++i) {
     Job& j = jobs[i];
     if (j.kind != kStore || j.whole || j.nk <= run) continue;
-    j.kb_per_split = static_cast<int>(run);
+    j.splits = static_cast<int>((j.nk + run - 1) / run);
+    j.kb_per_split = (j.nk + j.splits - 1) / j.splits;
     j.splits = (j.nk + j.kb_per_split - 1) / j.kb_per_split;
   }
 }
+
+namespace {
+// Gives each unit, the longest first, to the pair with the least to do so far (a unit's k-blocks, and
+// 12 for its epilogue).
+void list_units(Batch& b, int total, int pairs) {
+  struct Entry {
+    int cost;
+    uint16_t unit;
+  };
+  Entry e[kMaxListed];
+  for (int i = 0, u = 0; i < b.n; ++i) {
+    const Job& j = b.job[i];
+    for (; u < b.start[i + 1]; ++u) {
+      const int split = (u - b.start[i]) / j.tiles, kb0 = split * j.kb_per_split;
+      e[u] = Entry{std::min(j.kb_per_split, j.nk - kb0) + 12, static_cast<uint16_t>(u)};
+    }
+  }
+  std::stable_sort(e, e + total, [](const Entry& x, const Entry& y) { return x.cost > y.cost; });
+  int load[kPairs] = {}, count[kPairs] = {};
+  uint8_t owner[kMaxListed];
+  for (int u = 0; u < total; ++u) {
+    const int p = static_cast<int>(std::min_element(load, load + pairs) - load);
+    load[p] += e[u].cost;
+    ++count[p];
+    owner[u] = static_cast<uint8_t>(p);
+  }
+  int at[kPairs];
+  b.first[0] = 0;
+  for (int p = 0; p < kPairs; ++p) b.first[p + 1] = static_cast<uint16_t>(b.first[p] + (p < pairs ? count[p] : 0));
+  for (int p = 0; p < pairs; ++p) at[p] = b.first[p];
+  for (int u = 0; u < total; ++u) b.order[at[owner[u]]++] = e[u].unit;
+}
+}  // namespace
 
 zopt_status launch(const char* fn, Batch& b, int kinds, cudaStream_t s) {
   long long total = 0;
@@ -1056,7 +1129,11 @@ zopt_status launch(const char* fn, Batch& b, int kinds, cudaStream_t s) {
   b.start[b.n] = static_cast<int>(total);
   const int sms = sm_count();
   if (sms < 2) return fail(ZOPT_ECUDA, std::string(fn) + ": no CUDA device");
-  const long long pairs = total < sms / 2 ? total : sms / 2;
+  const long long pairs = std::min<long long>(total, std::min(sms / 2, kPairs));
+  // In turn, unequal units would leave pairs idle: 1537 tokens of a 1000 x 2732 block, 188 units of 43
+  // and 25 k-blocks, 125 for the last pair where 86 do.
+  b.listed = b.n > 1 && total > pairs && total <= kMaxListed;
+  if (b.listed) list_units(b, static_cast<int>(total), static_cast<int>(pairs));
   const dim3 grid(static_cast<unsigned>(2 * pairs));
   switch (kinds) {
     case kStore: return launch_kinds<kStore>(b, grid, s);

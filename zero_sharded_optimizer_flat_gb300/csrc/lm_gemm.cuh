@@ -2,9 +2,9 @@
 // epilogue its operator needs: what a launch is made of, on both sides of the launch.
 //
 // A launch is a batch of jobs. A job is one product D = P Q, D of M x N with inner length K,
-// fp32 accumulation over bf16 operands, cut into 256 x 256 tiles (kGluFwd: 256 rows x 128 gate and
-// the matching 128 up columns) and, where a launch would leave most CTA pairs idle, into runs of
-// k-blocks as well. Operands come through 2-D tensor maps: P's rows and Q's columns either with the
+// fp32 accumulation over bf16 operands, cut into tiles of 256 x 256 or 256 x 128 (kGluFwd: 128 or 64
+// gate and the matching up columns) and, where a launch would leave most CTA pairs idle, into runs
+// of k-blocks as well. Operands come through 2-D tensor maps: P's rows and Q's columns either with the
 // inner length contiguous ("K-major") or with the other one ("MN-major", a_mn / b_mn).
 #pragma once
 
@@ -20,6 +20,7 @@ namespace zopt {
 namespace lm {
 
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+constexpr int kPairs = 76;  // GB300's CTA pairs, what work is shared out for
 constexpr int kStages = 6;
 constexpr int kHalfBytes = 128 * kTileK * 2;  // one CTA's half of a stage's P or Q: 16 KiB
 constexpr int kMnBoxBytes = 64 * kTileK * 2;  // one 64 (MN) x 64 (K) box of an MN-major operand
@@ -49,7 +50,10 @@ struct Job {
   int kind;
   int M, N, K;
   int a_mn, b_mn;
-  int q_up;  // kGluFwd: Q's column of up column 0
+  int tile_n;  // columns of a tile: 256 or 128
+  int a_rows;  // rows of P (K-major) a CTA loads at a time: 128, or M rounded up to 8 where M <= 128
+  int tx;      // bytes of a stage, both CTAs'
+  int q_up;    // kGluFwd: Q's column of up column 0
   int tiles_m, tiles_n, tiles;
   int nk, kb_per_split, splits;
   int whole;      // its inner length is not cut
@@ -71,7 +75,7 @@ struct Job {
   const float* lse;
   const float* dloss;
   const float* unit;  // kCeBwd: dl is stored in this unit (it is its products' alpha)
-  float2* part;   // kCeFwd: (max, sum) of 128 columns' logits times kLog2e, at [2 tile column + half][row]
+  float2* part;   // kCeFwd: (max, sum) of half a tile's logits times kLog2e, at [2 tile column + half][row]
   float* tlogit;  // kCeFwd: the target's logit
   // kGluFwd, kGluBwd
   int act, kept_mode;
@@ -81,21 +85,30 @@ struct Job {
   int hidden;           // true width of the gate (N is its padded width in kGluBwd)
 };
 
+// Units of work are numbered job by job, a job's runs of k one after another. Pair p takes units p,
+// p + pairs, ...; or, in a launch of unequal units few enough for it, those that the host gave it:
+// order[first[p]] .. order[first[p + 1] - 1].
+constexpr int kMaxListed = 512;
+
 struct Batch {
   int n;
   int start[kMaxJobs + 1];
+  int listed;
   int* err;
   Job job[kMaxJobs];
+  uint16_t first[kPairs + 1];
+  uint16_t order[kMaxListed];
 };
 
 // ------------------------------------------------------------------ host side
 
-// The map of an operand's rows (P) or columns (Q), `mn` of them of inner length k: stored [mn][k], or
-// [k][mn] where MN-major, `pitch` elements (a multiple of 8) between the rows as stored.
-zopt_status map_operand(const char* fn, CUtensorMap* m, const void* base, long long mn, long long k, long long pitch,
-                        bool mn_major);
+// The maps of a tiled job's operands: P's M rows and Q's columns (`columns` of them as stored), stored
+// with the inner length contiguous, or as its transpose where MN-major; `pitch` elements (a multiple
+// of 8) between the rows as stored.
+zopt_status map_p(const char* fn, Job& j, const void* base, long long pitch);
+zopt_status map_q(const char* fn, Job& j, const void* base, long long columns, long long pitch);
 
-// Fills a job's tile counts from kind, M, N, K; k_blocks is its number of 64-deep blocks.
+// Fills a job's tiling from kind, M, N, K, a_mn, b_mn and kept_mode.
 void set_tiles(Job& j);
 // Cuts the inner length of the batch's kStore jobs so that no pair's run of k-blocks is much longer
 // than the launch's average (none where there are tiles enough). Depends on the shapes alone.
