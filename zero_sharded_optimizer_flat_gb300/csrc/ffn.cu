@@ -24,9 +24,9 @@ namespace {
 constexpr long long kMaxDim = 1LL << 30, kMaxLd = 1LL << 32;
 
 struct FfnPlan {
-  long long dp, fp;  // dim and hidden rounded up to 8
-  bool stage_x, stage_dy, stage_gate_up, stage_down;
-  size_t xs, dys, gate_up, down, h, dgu, slab, total;
+  long long dp, fp, gp;  // dim, hidden and 2 hidden rounded up to 8: row distances in the workspace
+  bool stage_x, stage_dy, stage_gate, stage_up, stage_down;
+  size_t xs, dys, gate, up, down, h, dgu, slab, total;
 };
 
 size_t take(size_t& at, long long bytes) {
@@ -50,27 +50,18 @@ void y_job(const zopt_ffn_job& c, Job& j) {
   set_tiles(j);
 }
 
-// The backward's second launch: dx, dgate_up (one job, or the gate's and up's columns apart where
-// the workspace pads them) and ddown. Returns their number.
-int grad_jobs(const zopt_ffn_job& c, const FfnPlan& p, Job* j) {
+// The backward's second launch: dx, dgate_up and ddown.
+int grad_jobs(const zopt_ffn_job& c, Job* j) {
   const int T = static_cast<int>(c.tokens), D = static_cast<int>(c.dim), F = static_cast<int>(c.hidden);
-  int n = 0;
-  auto add = [&](int m, int nn, int k, bool mn) {
-    j[n] = Job{};
-    j[n].kind = kStore;
-    j[n].M = m, j[n].N = nn, j[n].K = k;
-    j[n].a_mn = j[n].b_mn = mn;
-    set_tiles(j[n++]);
-  };
-  add(T, D, static_cast<int>(2 * p.fp), false);
-  if (p.fp == F) {
-    add(D, 2 * F, T, true);
-  } else {
-    add(D, F, T, true);
-    add(D, F, T, true);
+  const int shape[3][3] = {{T, D, 2 * F}, {D, 2 * F, T}, {F, D, T}};
+  for (int k = 0; k < 3; ++k) {
+    j[k] = Job{};
+    j[k].kind = kStore;
+    j[k].M = shape[k][0], j[k].N = shape[k][1], j[k].K = shape[k][2];
+    j[k].a_mn = j[k].b_mn = k > 0;
+    set_tiles(j[k]);
   }
-  add(F, D, T, true);
-  return n;
+  return 3;
 }
 
 long long slab_elems(Job* j, int n) {
@@ -83,13 +74,15 @@ long long slab_elems(Job* j, int n) {
 FfnPlan plan(const zopt_ffn_job& c, bool backward) {
   FfnPlan p{};
   const long long T = c.tokens, D = c.dim, F = c.hidden;
-  p.dp = round_up(D, 8), p.fp = round_up(F, 8);
+  p.dp = round_up(D, 8), p.fp = round_up(F, 8), p.gp = round_up(2 * F, 8);
   p.stage_x = (backward && c.x8 != nullptr) || c.ld_x % 8 != 0;
   p.stage_dy = backward && c.ld_dy % 8 != 0;
-  p.stage_gate_up = c.ld_gate_up % 8 != 0 || F % 8 != 0;
+  p.stage_gate = c.ld_gate_up % 8 != 0;
+  p.stage_up = p.stage_gate || F % 8 != 0;  // (the forward reads up's columns from column hidden on)
   p.stage_down = c.ld_down % 8 != 0;
   size_t at = 0;
-  if (p.stage_gate_up) p.gate_up = take(at, D * 2 * p.fp * 2);
+  if (p.stage_gate) p.gate = take(at, D * p.gp * 2);
+  if (p.stage_up) p.up = take(at, D * p.fp * 2);
   if (p.stage_down) p.down = take(at, F * p.dp * 2);
   if (p.stage_x) p.xs = take(at, T * p.dp * 2);
   p.h = take(at, T * p.fp * 2);
@@ -104,10 +97,10 @@ FfnPlan plan(const zopt_ffn_job& c, bool backward) {
   if (!backward) return p;
   at = shared;
   if (p.stage_dy) p.dys = take(at, T * p.dp * 2);
-  p.dgu = take(at, T * 2 * p.fp * 2);
+  p.dgu = take(at, T * p.gp * 2);
   p.slab = at;
   if (T > 0) {
-    const long long e = slab_elems(j, grad_jobs(c, p, j));
+    const long long e = slab_elems(j, grad_jobs(c, j));
     if (e) take(at, e * 4);
   }
   p.total = std::max(p.total, at);
@@ -169,37 +162,32 @@ zopt_status check(const char* fn, const zopt_ffn_job* c, bool backward, void* d_
     if (st_ != ZOPT_OK) return st_; \
   } while (0)
 
-// The operands as the TMA reads them: in place, or copied (or unpacked) into the workspace.
+// The operands as the TMA reads them: in place, or copied (or unpacked) into the workspace. The
+// backward reads gate_up's rows whole, the forward its gate and up columns.
 struct Inputs {
-  const uint16_t *x, *gate_up, *down, *dy;
-  long long px, pgu, pdown, pdy;
-  long long up;  // gate_up's column of up column 0
+  const uint16_t *x, *gate_up, *up, *down, *dy;
+  long long px, pgu, pup, pdown, pdy;
 };
-zopt_status stage_inputs(const char* fn, const zopt_ffn_job& c, const FfnPlan& p, uint8_t* ws, Inputs& in, cudaStream_t s) {
-  in = Inputs{c.x, c.w_gate_up, c.w_down, c.dy, c.ld_x, c.ld_gate_up, c.ld_down, c.ld_dy, c.hidden};
-  auto at = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
-  if (p.stage_gate_up) {
-    uint16_t* d = at(p.gate_up);
-    TRY(launch_stage(fn, d, 2 * p.fp, p.fp, c.w_gate_up, c.ld_gate_up, c.dim, c.hidden, s));
-    TRY(launch_stage(fn, d + p.fp, 2 * p.fp, p.fp, c.w_gate_up + c.hidden, c.ld_gate_up, c.dim, c.hidden, s));
-    in.gate_up = d, in.pgu = 2 * p.fp, in.up = p.fp;
+zopt_status stage_inputs(const char* fn, const zopt_ffn_job& c, const FfnPlan& p, bool backward, uint8_t* ws, Inputs& in,
+                         cudaStream_t s) {
+  in = Inputs{c.x, c.w_gate_up, c.w_gate_up + c.hidden, c.w_down, c.dy, c.ld_x, c.ld_gate_up, c.ld_gate_up, c.ld_down, c.ld_dy};
+  auto copy = [&](size_t off, long long pitch, const uint16_t* src, long long ld, long long rows, long long cols,
+                  const uint16_t** to, long long* pitch_to) {
+    uint16_t* d = reinterpret_cast<uint16_t*>(ws + off);
+    *to = d, *pitch_to = pitch;
+    return launch_stage(fn, d, pitch, pitch, src, ld, rows, cols, s);
+  };
+  if (p.stage_gate)
+    TRY(copy(p.gate, p.gp, c.w_gate_up, c.ld_gate_up, c.dim, backward ? 2 * c.hidden : c.hidden, &in.gate_up, &in.pgu));
+  if (p.stage_up && !backward) TRY(copy(p.up, p.fp, c.w_gate_up + c.hidden, c.ld_gate_up, c.dim, c.hidden, &in.up, &in.pup));
+  if (p.stage_down) TRY(copy(p.down, p.dp, c.w_down, c.ld_down, c.hidden, c.dim, &in.down, &in.pdown));
+  if (p.stage_x && c.x8 != nullptr) {
+    in.x = reinterpret_cast<uint16_t*>(ws + p.xs), in.px = p.dp;
+    TRY(act8::unpack(fn, *c.x8, reinterpret_cast<uint16_t*>(ws + p.xs), p.dp, s));
+  } else if (p.stage_x) {
+    TRY(copy(p.xs, p.dp, c.x, c.ld_x, c.tokens, c.dim, &in.x, &in.px));
   }
-  if (p.stage_down) {
-    TRY(launch_stage(fn, at(p.down), p.dp, p.dp, c.w_down, c.ld_down, c.hidden, c.dim, s));
-    in.down = at(p.down), in.pdown = p.dp;
-  }
-  if (p.stage_x) {
-    if (c.x8 != nullptr) {
-      TRY(act8::unpack(fn, *c.x8, at(p.xs), p.dp, s));
-    } else {
-      TRY(launch_stage(fn, at(p.xs), p.dp, p.dp, c.x, c.ld_x, c.tokens, c.dim, s));
-    }
-    in.x = at(p.xs), in.px = p.dp;
-  }
-  if (p.stage_dy) {
-    TRY(launch_stage(fn, at(p.dys), p.dp, p.dp, c.dy, c.ld_dy, c.tokens, c.dim, s));
-    in.dy = at(p.dys), in.pdy = p.dp;
-  }
+  if (p.stage_dy) TRY(copy(p.dys, p.dp, c.dy, c.ld_dy, c.tokens, c.dim, &in.dy, &in.pdy));
   return ok();
 }
 
@@ -247,7 +235,7 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
   const FfnPlan p = plan(c, false);
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
   Inputs in;
-  TRY(stage_inputs(fn, c, p, ws, in, s));
+  TRY(stage_inputs(fn, c, p, false, ws, in, s));
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
   {
     Batch b{};
@@ -257,11 +245,11 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
     j.kind = kGluFwd;
     j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.hidden), j.K = static_cast<int>(c.dim);
     j.b_mn = 1;
-    j.q_up = static_cast<int>(in.up);
     glu_fields(j, c);
     set_tiles(j);
     TRY(map_p(fn, j, in.x, in.px));
-    TRY(map_q(fn, j, in.gate_up, in.up + c.hidden, in.pgu));
+    TRY(map_q(fn, j, in.gate_up, c.hidden, in.pgu));
+    TRY(map_up(fn, j, in.up, c.hidden, in.pup));
     j.out = h;
     j.ld_out = p.fp;
     TRY(launch(fn, b, kGluFwd, s));
@@ -294,7 +282,7 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
   const FfnPlan p = plan(c, true);
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
   Inputs in;
-  TRY(stage_inputs(fn, c, p, ws, in, s));
+  TRY(stage_inputs(fn, c, p, true, ws, in, s));
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
   uint16_t* dgu = reinterpret_cast<uint16_t*>(ws + p.dgu);
   {
@@ -303,37 +291,33 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
     b.n = 1;
     Job& j = b.job[0];
     j.kind = kGluBwd;
-    // over the padded width: down's missing rows read as zero, so the pad columns become zero and
-    // may stand in the inner length of dx
-    j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(p.fp), j.K = static_cast<int>(c.dim);
+    j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.hidden), j.K = static_cast<int>(c.dim);
     glu_fields(j, c);
     set_tiles(j);
     TRY(map_p(fn, j, in.dy, in.pdy));
     TRY(map_q(fn, j, in.down, c.hidden, in.pdown));
     j.out = dgu;
-    j.ld_out = 2 * p.fp;
+    j.ld_out = p.gp;
     j.out_h = h;
+    j.ld_h = p.fp;
     TRY(launch(fn, b, kGluBwd, s));
   }
   Batch b{};
   b.err = err;
   Job jobs[kMaxJobs];
-  const int n = grad_jobs(c, p, jobs);
+  const int n = grad_jobs(c, jobs);
   plan_splits(jobs, n);
   SumBatch sums{};
   float* slab = reinterpret_cast<float*>(ws + p.slab);
-  TRY(map_p(fn, jobs[0], dgu, 2 * p.fp));
+  TRY(map_p(fn, jobs[0], dgu, p.gp));
   TRY(map_q(fn, jobs[0], in.gate_up, c.dim, in.pgu));
   finish(jobs[0], c.dx, c.ld_dx, slab, sums);
-  for (int k = 1; k + 1 < n; ++k) {  // the gate's and up's columns together, or apart
-    const int up = k - 1;
-    TRY(map_p(fn, jobs[k], in.x, in.px));
-    TRY(map_q(fn, jobs[k], dgu + up * p.fp, jobs[k].N, 2 * p.fp));
-    finish(jobs[k], c.dw_gate_up + up * c.hidden, c.ld_dw_gate_up, slab, sums);
-  }
-  TRY(map_p(fn, jobs[n - 1], h, p.fp));
-  TRY(map_q(fn, jobs[n - 1], in.dy, c.dim, in.pdy));
-  finish(jobs[n - 1], c.dw_down, c.ld_dw_down, slab, sums);
+  TRY(map_p(fn, jobs[1], in.x, in.px));
+  TRY(map_q(fn, jobs[1], dgu, 2 * c.hidden, p.gp));
+  finish(jobs[1], c.dw_gate_up, c.ld_dw_gate_up, slab, sums);
+  TRY(map_p(fn, jobs[2], h, p.fp));
+  TRY(map_q(fn, jobs[2], in.dy, c.dim, in.pdy));
+  finish(jobs[2], c.dw_down, c.ld_dw_down, slab, sums);
   // The longest units first: the launch's end is then made of short ones.
   const bool dx_first = jobs[0].kb_per_split >= jobs[1].kb_per_split;
   b.n = n;

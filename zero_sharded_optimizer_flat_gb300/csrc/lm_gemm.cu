@@ -677,7 +677,7 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const A
   const int col0 = w.tj * j.tile_n + width * h;
   const Out<64> dgate(j.out, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, j.M, col0, j.N, lane);
-  const Out<64> hout(j.out_h, j.N, 2, row0, j.M, col0, j.N, lane);
+  const Out<64> hout(j.out_h, j.ld_h, 2, row0, j.M, col0, j.N, lane);
   Scales next_sc;
   if constexpr (kKept == kKeep8) next_sc.load(j, next_row, next_col);
 #pragma unroll 1
@@ -758,6 +758,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int j = 0; j < B.n; ++j) {
       tc::prefetch_tmap(&B.job[j].P);
       tc::prefetch_tmap(&B.job[j].Q);
+      if ((kKinds & kGluFwd) != 0) tc::prefetch_tmap(&B.job[j].Up);
     }
   }
   if (warp == 1) {
@@ -789,14 +790,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Job& j = B.job[ji];
         const Unit w = unit_of(j, t - B.start[ji]);
         const CUtensorMap* const P = &j.P;
-        const CUtensorMap* const Q = &j.Q;
+        const bool up = (kKinds & kGluFwd) != 0 && !leader;  // one CTA has the gate's columns, the other up's
+        const CUtensorMap* const Q = up ? &j.Up : &j.Q;
         const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
         const int row0 = w.ti * kTileM + static_cast<int>(rank) * 128;  // this CTA's rows of P
         const int width = j.tile_n >> 1;                                // this CTA's columns of Q
         const bool wide = width == 128, has_a = leader || j.a_rows == 128;
         const uint32_t tx = static_cast<uint32_t>(j.tx);
-        int col0 = w.tj * j.tile_n + static_cast<int>(rank) * width;
-        if ((kKinds & kGluFwd) && j.kind == kGluFwd) col0 = w.tj * width + (leader ? 0 : j.q_up);
+        const int col0 = (kKinds & kGluFwd) != 0 ? w.tj * width : w.tj * j.tile_n + static_cast<int>(rank) * width;
         const int k_end = w.kb1 * kTileK;
         for (int k = w.kb0 * kTileK; k < k_end; k += kTileK) {
           if (!wait(empty0 + 8 * s, ph, err)) {
@@ -1038,6 +1039,10 @@ zopt_status map_q(const char* fn, Job& j, const void* base, long long columns, l
                 : make_map(fn, &j.Q, base, j.K, columns, pitch, j.tile_n / 2);
 }
 
+zopt_status map_up(const char* fn, Job& j, const void* base, long long columns, long long pitch) {
+  return make_map(fn, &j.Up, base, columns, j.K, pitch, 64);
+}
+
 void set_tiles(Job& j) {
   j.tiles_m = (j.M + kTileM - 1) / kTileM;
   j.nk = (j.K + kTileK - 1) / kTileK;
@@ -1049,8 +1054,9 @@ void set_tiles(Job& j) {
   };
   // Tiles half as wide cost more than half as much (P is read again for each: 0.7 of a k-block's
   // time, and half of an epilogue's, which counts as 16 k-blocks), but where there are few of the
-  // wide ones they keep twice as many pairs busy. kStore cuts its inner length instead, and a tile
-  // that makes 8-bit blocks has to be one block wide.
+  // wide ones they keep twice as many pairs busy. kStore cuts its inner length instead (with narrow
+  // tiles cross entropy backward, 512 x 256 x 4096, took 32 us for 23), and a tile that makes 8-bit
+  // blocks has to be one block wide.
   j.tile_n = kTileN;
   if (j.kind != kStore && !(j.kind == kGluFwd && j.kept_mode == kKeep8)) {
     auto waves = [&](int tile_n) { return (static_cast<long long>(j.tiles_m) * columns(tile_n) + kPairs - 1) / kPairs; };
@@ -1067,15 +1073,23 @@ void set_tiles(Job& j) {
 }
 
 void plan_splits(Job* jobs, int n) {
-  // Fewer than four k-blocks a unit is not worth a partial sum.
+  // A run is at least four k-blocks, and the longest one has to get shorter by more than what adding
+  // up the partial sums takes: a launch, about four k-blocks' time, and their bytes, about one for
+  // every 4 MiB.
   constexpr long long kLeast = 4;
-  long long work = 0;
-  for (int i = 0; i < n; ++i) work += static_cast<long long>(jobs[i].tiles_m) * jobs[i].tiles_n * jobs[i].nk;
-  const long long share = (work + kPairs - 1) / kPairs;
-  const long long run = share < kLeast ? kLeast : share;
+  long long work = 0, longest = 0, bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    work += static_cast<long long>(jobs[i].tiles_m) * jobs[i].tiles_n * jobs[i].nk;
+    if (!jobs[i].whole) longest = std::max<long long>(longest, jobs[i].nk);
+  }
+  const long long run = std::max(kLeast, (work + kPairs - 1) / kPairs);
+  auto cut = [&](const Job& j) { return j.kind == kStore && !j.whole && j.nk > run; };
+  for (int i = 0; i < n; ++i)
+    if (cut(jobs[i])) bytes += (jobs[i].nk + run - 1) / run * jobs[i].M * split_pitch(jobs[i].N) * 4;
+  if (longest - run <= 4 + (bytes >> 22)) return;
   for (int i = 0; i < n; ++i) {
     Job& j = jobs[i];
-    if (j.kind != kStore || j.whole || j.nk <= run) continue;
+    if (!cut(j)) continue;
     j.splits = static_cast<int>((j.nk + run - 1) / run);
     j.kb_per_split = (j.nk + j.splits - 1) / j.splits;
     j.splits = (j.nk + j.kb_per_split - 1) / j.kb_per_split;

@@ -30,7 +30,7 @@ constexpr int kBoxBytes = 32 * 128;  // an epilogue warp's results on their way 
 constexpr int kSwapBytes = 4 * 64 * 2;  // kGluFwd: two warps' block exponents for each quarter of the rows
 constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxBytes + kSwapBytes + 1024 + 256;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-constexpr int kMaxJobs = 5;
+constexpr int kMaxJobs = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // What an epilogue makes of its accumulators.
@@ -46,23 +46,23 @@ enum OutMode : int { kOutBf16 = 0, kOutF32 = 1 };                   // kStore
 enum KeptMode : int { kKeepNone = 0, kKeepBf16 = 1, kKeep8 = 2 };  // kGluFwd, kGluBwd
 
 struct Job {
-  CUtensorMap P, Q;
+  CUtensorMap P, Q, Up;  // Up: kGluFwd's up columns (Q: its gate's)
   int kind;
   int M, N, K;
   int a_mn, b_mn;
   int tile_n;  // columns of a tile: 256 or 128
   int a_rows;  // rows of P (K-major) a CTA loads at a time: 128, or M rounded up to 8 where M <= 128
   int tx;      // bytes of a stage, both CTAs'
-  int q_up;    // kGluFwd: Q's column of up column 0
   int tiles_m, tiles_n, tiles;
   int nk, kb_per_split, splits;
   int whole;      // its inner length is not cut
   int rows_fast;  // consecutive tiles walk down a tile column (else along a tile row)
   // D, or what the epilogue makes of it: kCeBwd's dl; kGluFwd's h; kGluBwd's dgate, its dup N columns
-  // later, and h (out_h, rows of N)
+  // later, and h (out_h, rows of ld_h)
   void* out;
   long long ld_out;
   void* out_h;
+  long long ld_h;
   // kStore
   int out_mode;
   long long split_stride;  // split_stride: elements between the partial sums of one tile's runs of k
@@ -82,7 +82,7 @@ struct Job {
   void* kept;  // gate and up as the caller keeps them: row r's gate at r * ld_kept, its up hidden later
   long long ld_kept;
   uint8_t* kept_scale;  // kKeep8: row r's block exponents at r * 2 blocks, the gate's first
-  int hidden;           // true width of the gate (N is its padded width in kGluBwd)
+  int hidden;           // the gate's width, N
 };
 
 // Units of work are numbered job by job, a job's runs of k one after another. Pair p takes units p,
@@ -107,6 +107,7 @@ struct Batch {
 // of 8) between the rows as stored.
 zopt_status map_p(const char* fn, Job& j, const void* base, long long pitch);
 zopt_status map_q(const char* fn, Job& j, const void* base, long long columns, long long pitch);
+zopt_status map_up(const char* fn, Job& j, const void* base, long long columns, long long pitch);
 
 // Fills a job's tiling from kind, M, N, K, a_mn, b_mn and kept_mode.
 void set_tiles(Job& j);
