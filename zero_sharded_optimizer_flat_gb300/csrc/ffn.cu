@@ -13,6 +13,7 @@
 #include <string>
 
 #include "act8_host.h"
+#include "ffn_few.h"
 #include "launch.cuh"
 #include "lm_gemm.cuh"
 #include "ns_internal.h"
@@ -25,8 +26,8 @@ constexpr long long kMaxDim = 1LL << 30, kMaxLd = 1LL << 32;
 
 struct FfnPlan {
   long long dp, fp, gp;  // dim, hidden and 2 hidden rounded up to 8: row distances in the workspace
-  bool stage_x, stage_dy, stage_gate, stage_up, stage_down;
-  size_t xs, dys, gate, up, down, h, dgu, slab, total;
+  bool stage_x, stage_dy, stage_gate, stage_up, stage_down, few;
+  size_t xs, dys, gate, up, down, h, dgu, slab, few_gate_up, few_y, total;
 };
 
 size_t take(size_t& at, long long bytes) {
@@ -89,7 +90,13 @@ FfnPlan plan(const zopt_ffn_job& c, bool backward) {
   const size_t shared = at;
   Job j[kMaxJobs];
   y_job(c, j[0]);
-  if (T > 0) {
+  p.few = T > 0 && few::takes(c);
+  if (p.few) {
+    long long gate_up, y;
+    few::partial_elems(c, &gate_up, &y);
+    p.few_gate_up = take(at, gate_up * 4);
+    p.few_y = take(at, y * 4);
+  } else if (T > 0) {
     const long long e = slab_elems(j, 1);
     if (e) p.slab = take(at, e * 4);
   }
@@ -234,9 +241,10 @@ zopt_status forward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaStr
   TRY(ns::take_error_word(fn, &err));
   const FfnPlan p = plan(c, false);
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
+  if (p.few) return few::ffn_forward(c, reinterpret_cast<float*>(ws + p.few_gate_up), reinterpret_cast<float*>(ws + p.few_y), s);
   Inputs in;
   TRY(stage_inputs(fn, c, p, false, ws, in, s));
-  uint16_t* h = reinterpret_cast<uint16_t*>(ws + p.h);
   {
     Batch b{};
     b.err = err;

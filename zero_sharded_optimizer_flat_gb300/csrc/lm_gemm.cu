@@ -18,6 +18,7 @@
 #include <string>
 
 #include "act8.cuh"
+#include "f2.cuh"
 #include "launch.cuh"
 #include "lm_gemm.cuh"
 #include "ns_internal.h"
@@ -44,35 +45,6 @@ __device__ __forceinline__ float rcp(float x) {
   return r;
 }
 
-// Two fp32 operations an instruction: the epilogues are bound by the instructions they issue.
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -915,7 +887,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Unit w = unit_of(j, t - B.start[ji]);
       const int row0 = w.ti * kTileM + rows0;
       int ok = 1;
-      if (lane == 0) ok = tc::mbar_wait_idle(tfull + b, tph, err) ? 1 : 0;
+      if (lane == 0) ok = wait(tc::smem_u32(tfull + b), tph, err) ? 1 : 0;
       if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
       tc::fence_after_sync();
       const Acc acc{tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN), tempty_leader[b], lane};
@@ -1073,24 +1045,35 @@ void set_tiles(Job& j) {
 }
 
 void plan_splits(Job* jobs, int n) {
-  // A run is at least four k-blocks, and the longest one has to get shorter by more than what adding
-  // up the partial sums takes: a launch, about four k-blocks' time, and their bytes, about one for
-  // every 4 MiB.
-  constexpr long long kLeast = 4;
-  long long work = 0, longest = 0, bytes = 0;
-  for (int i = 0; i < n; ++i) {
-    work += static_cast<long long>(jobs[i].tiles_m) * jobs[i].tiles_n * jobs[i].nk;
-    if (!jobs[i].whole) longest = std::max<long long>(longest, jobs[i].nk);
-  }
-  const long long run = std::max(kLeast, (work + kPairs - 1) / kPairs);
-  auto cut = [&](const Job& j) { return j.kind == kStore && !j.whole && j.nk > run; };
+  // In k-blocks' time (0.27 us): an epilogue takes about 12; adding up partial sums a launch, about
+  // four, and their bytes, one for every 4 MiB. A run is at least four k-blocks.
+  constexpr long long kLeast = 4, kEpilogue = 12, kSum = 4;
+  long long longest = 0;
   for (int i = 0; i < n; ++i)
-    if (cut(jobs[i])) bytes += (jobs[i].nk + run - 1) / run * jobs[i].M * split_pitch(jobs[i].N) * 4;
-  if (longest - run <= 4 + (bytes >> 22)) return;
+    if (!jobs[i].whole) longest = std::max<long long>(longest, jobs[i].nk);
+  // what a launch with runs of at most `run` takes: a single job's in turn, several jobs' dealt out
+  auto cost = [&](long long run) {
+    long long all = 0, count = 0, most = 0, bytes = 0;
+    for (int i = 0; i < n; ++i) {
+      const Job& j = jobs[i];
+      const long long s = j.kind == kStore && !j.whole ? (j.nk + run - 1) / run : 1, kb = (j.nk + s - 1) / s;
+      const long long tiles = static_cast<long long>(j.tiles_m) * j.tiles_n;
+      all += tiles * s * (kb + kEpilogue), count += tiles * s, most = std::max(most, kb + kEpilogue);
+      if (s > 1) bytes += s * j.M * split_pitch(j.N) * 4;
+    }
+    const long long waves = (count + kPairs - 1) / kPairs;
+    return (n == 1 ? waves * most : std::max(most, all / kPairs + most / 2)) + (bytes > 0 ? kSum + (bytes >> 22) : 0);
+  };
+  long long best = longest, least = cost(std::max(longest, kLeast));
+  for (int s = 2; s <= 64 && longest > kLeast; ++s) {
+    const long long run = std::max(kLeast, (longest + s - 1) / s), c = cost(run);
+    if (c < least) least = c, best = run;
+    if (run == kLeast) break;
+  }
   for (int i = 0; i < n; ++i) {
     Job& j = jobs[i];
-    if (!cut(j)) continue;
-    j.splits = static_cast<int>((j.nk + run - 1) / run);
+    if (j.kind != kStore || j.whole || j.nk <= best) continue;
+    j.splits = static_cast<int>((j.nk + best - 1) / best);
     j.kb_per_split = (j.nk + j.splits - 1) / j.splits;
     j.splits = (j.nk + j.kb_per_split - 1) / j.kb_per_split;
   }
