@@ -533,8 +533,10 @@ ZOPT_API zopt_status zopt_act_unpack(const zopt_act8* in, uint16_t* out, int64_t
  * fp32), or nothing; the backward takes what was kept, and x in bf16 or as a checkpoint (x8). The
  * weight gradients have the weights' layout: zopt_grad_accumulate takes them as they are.
  *
- * Rows that the TMA cannot read in place (ld not a multiple of 8 elements, or F not a multiple of
- * 8) are copied into the workspace first. A result does not depend on the time or place of any
+ * Rows that the TMA cannot read in place (ld not a multiple of 8 elements; the forward's up columns
+ * where F is not a multiple of 8) are copied into the workspace first. Up to four tokens a forward
+ * runs on the CUDA cores instead, with the same roundings. Outputs must not overlap inputs or each
+ * other. A result does not depend on the time or place of any
  * block's execution: a call repeated on the same inputs gives the same bits.
  * ====================================================================================== */
 #define ZOPT_ACT_SILU 0
@@ -571,8 +573,8 @@ typedef struct zopt_ffn_job {
  * other pointer is looked at. 0 for a shape that the calls refuse. */
 ZOPT_API size_t zopt_ffn_workspace(const zopt_ffn_job* job, int32_t backward);
 /* Errors of both: EINVAL for NULL or misaligned pointers (16 bytes; scale bytes any), tokens < 0,
- * dim or hidden < 1, any of them above 2^30, a row distance below the row's length or above 2^32,
- * another act, both or (backward) neither of x / x8 and of kept / kept8, a checkpoint of another
+ * dim or hidden < 1, tokens or dim above 2^30, hidden above 2^29, a matrix above 2^44 elements, a
+ * row distance below the row's length or above 2^32, another act, both or (backward) neither of x / x8 and of kept / kept8, a checkpoint of another
  * shape, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16; ETIMEOUT
  * if a bounded wait of an earlier call's kernel gave up. tokens = 0: the forward does nothing, the
  * backward sets the weight gradients to zero. */
@@ -591,7 +593,8 @@ ZOPT_API zopt_status zopt_ffn_backward(const zopt_ffn_job* job, void* d_ws, size
  * pieces' dl (bf16) in the workspace. A row whose target is ignore_index takes no part: loss, lse
  * and its dx are 0 and its x adds nothing to dw, whatever x holds there. A target that is neither
  * ignore_index nor in [0, vocab) makes its loss NaN and its gradients NaN, for found_inf to skip
- * the step on. dloss is the gradient of each row's loss (1 / the number of counted rows for a
+ * the step on. The products that give dw and dx read dl in bf16, in units of the largest |dloss|.
+ * dloss is the gradient of each row's loss (1 / the number of counted rows for a
  * mean). Repeated on the same inputs a call gives the same bits.
  * ====================================================================================== */
 typedef struct zopt_linear_ce_job {
@@ -618,8 +621,8 @@ typedef struct zopt_linear_ce_job {
  * refuse. */
 ZOPT_API size_t zopt_linear_ce_workspace(const zopt_linear_ce_job* job, int32_t backward);
 /* Errors of both: EINVAL for NULL or misaligned pointers (matrices 16 bytes, vectors their
- * element), tokens < 0, dim or vocab < 1, any of them above 2^30, a row distance below dim or
- * above 2^32, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16;
+ * element), tokens < 0, dim or vocab < 1, any of them above 2^30, a matrix (the logits too) above
+ * 2^44 elements, a row distance below dim or above 2^32, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16;
  * ETIMEOUT as above. tokens = 0: the forward does nothing, the backward sets dw to zero. */
 ZOPT_API zopt_status zopt_linear_ce_forward(const zopt_linear_ce_job* job, void* d_ws, size_t ws_bytes,
                                             zopt_stream stream);

@@ -80,6 +80,7 @@ def test_linear_ce_workspace_keeps_no_logits():
     big = dict(tokens=65536, dim=2048, vocab=131072, ld_x=2048, ld_w=2048)
     assert size(**big) >= size(0, **big)
     assert size(**big) < 65536 * 131072 * 2 / 4  # well under the bf16 logits alone
+    assert size(tokens=1 << 25, vocab=1 << 20) == 0  # logits above 2^44
     odd = dict(dim=33, ld_x=33, ld_w=33)  # staged copies of x and w
     assert size(**odd) - size(dim=33, ld_x=40, ld_w=40) >= 2 * 40 * (64 + 1000)
 
@@ -128,6 +129,7 @@ def test_ffn_workspace_covers_both_directions():
     for kw in ({}, {"tokens": 1}, {"tokens": 8192, "dim": 2048, "hidden": 5632, "ld_gate_up": 11264, "ld_down": 2048,
                                   "ld_x": 2048, "ld_dy": 2048}, {"hidden": 47}):
         assert L.zopt_ffn_workspace(ffn(**kw), 1) >= L.zopt_ffn_workspace(ffn(**kw), 0) > 0
+    assert L.zopt_ffn_workspace(ffn(tokens=1 << 30, dim=1 << 15, ld_down=1 << 15, ld_x=1 << 15, ld_dy=1 << 15), 1) == 0
     assert L.zopt_ffn_workspace(None, 1) == 0 and L.zopt_ffn_workspace(ffn(dim=0), 1) == 0
 
 

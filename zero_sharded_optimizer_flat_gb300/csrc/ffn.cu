@@ -23,6 +23,7 @@ namespace lm {
 namespace {
 
 constexpr long long kMaxDim = 1LL << 30, kMaxLd = 1LL << 32;
+constexpr long long kMaxElems = 1LL << 44;  // of any matrix: tile numbers stay well below 2^31
 
 struct FfnPlan {
   long long dp, fp, gp;  // dim, hidden and 2 hidden rounded up to 8: row distances in the workspace
@@ -36,9 +37,14 @@ size_t take(size_t& at, long long bytes) {
   return here;
 }
 
+bool sizes_ok(const zopt_ffn_job& c) {
+  return c.tokens <= kMaxDim && c.dim <= kMaxDim && c.hidden <= kMaxDim / 2 && c.tokens * c.dim <= kMaxElems &&
+         c.tokens * 2 * c.hidden <= kMaxElems && c.dim * 2 * c.hidden <= kMaxElems;
+}
+
 bool shape_ok(const zopt_ffn_job& c, bool backward) {
   auto ld = [](int64_t v, int64_t least) { return v >= least && v <= kMaxLd; };
-  return c.tokens >= 0 && c.dim >= 1 && c.hidden >= 1 && c.tokens <= kMaxDim && c.dim <= kMaxDim && c.hidden <= kMaxDim / 2 &&
+  return c.tokens >= 0 && c.dim >= 1 && c.hidden >= 1 && sizes_ok(c) &&
          ld(c.ld_gate_up, 2 * c.hidden) && ld(c.ld_down, c.dim) && (c.x8 != nullptr || ld(c.ld_x, c.dim)) &&
          (!backward || ld(c.ld_dy, c.dim));
 }
@@ -121,8 +127,7 @@ zopt_status check(const char* fn, const zopt_ffn_job* c, bool backward, void* d_
   if (c->dtype != ZOPT_BF16) return fail(ZOPT_EUNSUPPORTED, f + ": dtype must be ZOPT_BF16");
   if (c->act != ZOPT_ACT_SILU && c->act != ZOPT_ACT_GELU) return bad("act must be ZOPT_ACT_SILU or ZOPT_ACT_GELU");
   if (c->tokens < 0 || c->dim < 1 || c->hidden < 1) return bad("tokens < 0, dim < 1 or hidden < 1");
-  if (c->tokens > kMaxDim || c->dim > kMaxDim || c->hidden > kMaxDim / 2)
-    return bad("tokens or dim above 2^30, or hidden above 2^29");
+  if (!sizes_ok(*c)) return bad("tokens or dim above 2^30, hidden above 2^29 or a matrix above 2^44 elements");
   const int64_t T = c->tokens, D = c->dim, F = c->hidden;
   auto ld_bad = [](int64_t ld, int64_t least) { return ld < least || ld > kMaxLd; };
   if (ld_bad(c->ld_gate_up, 2 * F) || ld_bad(c->ld_down, D)) return bad("a weight's row distance below its row or above 2^32");

@@ -27,6 +27,7 @@ namespace lm {
 namespace {
 
 constexpr long long kMaxDim = 1LL << 30, kMaxLd = 1LL << 32;
+constexpr long long kMaxElems = 1LL << 44;  // of any matrix, the logits too: tile numbers stay well below 2^31
 // dl of one piece: about 128 MiB (bf16), so that a piece is written and read once each while the
 // products over it run for a few hundred microseconds; at least 4096 entries, below which the dx
 // sum's 8 bytes per row and feature would be noticed.
@@ -47,8 +48,13 @@ size_t take(size_t& at, long long bytes) {
   return here;
 }
 
+bool sizes_ok(const zopt_linear_ce_job& c) {
+  return c.tokens <= kMaxDim && c.dim <= kMaxDim && c.vocab <= kMaxDim && c.tokens * c.dim <= kMaxElems &&
+         c.vocab * c.dim <= kMaxElems && c.tokens * c.vocab <= kMaxElems;
+}
+
 bool shape_ok(const zopt_linear_ce_job& c) {
-  return c.tokens >= 0 && c.dim >= 1 && c.vocab >= 1 && c.tokens <= kMaxDim && c.dim <= kMaxDim && c.vocab <= kMaxDim &&
+  return c.tokens >= 0 && c.dim >= 1 && c.vocab >= 1 && sizes_ok(c) &&
          c.ld_x >= c.dim && c.ld_w >= c.dim && c.ld_x <= kMaxLd && c.ld_w <= kMaxLd;
 }
 
@@ -93,6 +99,7 @@ CePlan plan(const zopt_linear_ce_job& c, bool backward) {
   // partial sums: those of a whole piece or of the last one, whichever takes more
   long long slab = 0;
   for (const long long vc : {std::min(p.piece, V), V - (p.pieces - 1) * p.piece}) {
+    if (T == 0) break;  // (nothing is multiplied)
     for (int both = 0; both < 3; ++both) {  // dx and dw, or one of them alone
       Job j[2];
       piece_jobs(c, vc, j[0], j[1]);
@@ -192,8 +199,7 @@ zopt_status check(const char* fn, const zopt_linear_ce_job* c, bool backward, vo
   if (c == nullptr) return fail(ZOPT_EINVAL, f + ": NULL job");
   if (c->dtype != ZOPT_BF16) return fail(ZOPT_EUNSUPPORTED, f + ": dtype must be ZOPT_BF16");
   if (c->tokens < 0 || c->dim < 1 || c->vocab < 1) return fail(ZOPT_EINVAL, f + ": tokens < 0, dim < 1 or vocab < 1");
-  if (c->tokens > kMaxDim || c->dim > kMaxDim || c->vocab > kMaxDim)
-    return fail(ZOPT_EINVAL, f + ": tokens, dim or vocab above 2^30");
+  if (!sizes_ok(*c)) return fail(ZOPT_EINVAL, f + ": tokens, dim or vocab above 2^30, or a matrix above 2^44 elements");
   auto ld_bad = [&](int64_t ld) { return ld < c->dim || ld > kMaxLd; };
   if (ld_bad(c->ld_x) || ld_bad(c->ld_w) || (backward && c->dx && ld_bad(c->ld_dx)) || (backward && c->dw && ld_bad(c->ld_dw)))
     return fail(ZOPT_EINVAL, f + ": row distance below dim or above 2^32");

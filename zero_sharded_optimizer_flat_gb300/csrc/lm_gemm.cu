@@ -1056,7 +1056,7 @@ void plan_splits(Job* jobs, int n) {
     long long all = 0, count = 0, most = 0, bytes = 0;
     for (int i = 0; i < n; ++i) {
       const Job& j = jobs[i];
-      const long long s = j.kind == kStore && !j.whole ? (j.nk + run - 1) / run : 1, kb = (j.nk + s - 1) / s;
+      const long long s = j.kind == kStore && !j.whole ? std::max<long long>(1, (j.nk + run - 1) / run) : 1, kb = (j.nk + s - 1) / s;
       const long long tiles = static_cast<long long>(j.tiles_m) * j.tiles_n;
       all += tiles * s * (kb + kEpilogue), count += tiles * s, most = std::max(most, kb + kEpilogue);
       if (s > 1) bytes += s * j.M * split_pitch(j.N) * 4;
