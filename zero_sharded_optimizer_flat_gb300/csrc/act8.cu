@@ -11,22 +11,13 @@
 
 #include "act8.cuh"
 #include "act8_host.h"
+#include "divisor.cuh"
 #include "launch.cuh"
 #include "tc.cuh"
 
 namespace zopt {
 namespace act8 {
 namespace {
-
-// n / d for n < 2^31 by a multiplication (division by invariant integers, Granlund and Montgomery).
-struct Divisor {
-  uint32_t d, m, s;
-  explicit Divisor(uint32_t d_ = 1) : d(d_), m(0), s(0) {
-    while (s < 32 && (1ull << s) < d) ++s;
-    m = static_cast<uint32_t>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
-};
 
 struct Args {
   uint16_t* x;  // pack: read; unpack: written

@@ -4,8 +4,8 @@
 //
 // A cluster of two CTAs computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA holds its
 // 128 rows of P and its 128 columns of Q, so a 64-deep k-block brings 32 KiB per SM and the ring
-// holds six stages. Warp 0 of each CTA streams the operands by TMA (all complete on the leader's
-// stage barrier), one thread of the leader issues the M=256, N=256, K=16 MMAs into one of two TMEM
+// holds six stages. A thread of each CTA for each operand streams it by TMA (all complete on the
+// leader's stage barrier), one thread of the leader issues the M=256, N=256, K=16 MMAs into one of two TMEM
 // accumulators, and eight epilogue warps (two per quarter of the TMEM lanes, each 128 of the 256
 // columns) turn the other accumulator into the operator's outputs meanwhile. A lane holds whole
 // row pieces, so softmax statistics and the 8-bit blocks need no exchange between lanes.
@@ -177,15 +177,11 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_of(const Job& j, int u) {
   Unit w;
-  w.split = u / j.tiles;
+  w.split = static_cast<int>(j.per_split(static_cast<uint32_t>(u)));
   u -= w.split * j.tiles;
-  if (j.rows_fast) {
-    w.tj = u / j.tiles_m;
-    w.ti = u - w.tj * j.tiles_m;
-  } else {
-    w.ti = u / j.tiles_n;
-    w.tj = u - w.ti * j.tiles_n;
-  }
+  const int line = static_cast<int>(j.per_line(static_cast<uint32_t>(u))), at = u - line * static_cast<int>(j.per_line.d);
+  w.ti = j.rows_fast ? at : line;
+  w.tj = j.rows_fast ? line : at;
   w.kb0 = w.split * j.kb_per_split;
   w.kb1 = min(w.kb0 + j.kb_per_split, j.nk);
   return w;
@@ -746,13 +742,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   int* const err = B.err;
   const uint32_t full0 = tc::smem_u32(full), empty0 = tc::smem_u32(empty);
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     if (elect_one()) {
-      // ---------------------------------------------------------------- TMA producer (both CTAs)
-      // Every cycle of this loop counts: a k-block takes the MMAs 512 cycles, and the thread has to
-      // wait for a stage, arm it and issue two to four loads in less. So everything that a job fixes
-      // is in registers before its k-loop.
-      const uint32_t a0 = tc::smem_u32(sA), b0 = tc::smem_u32(sB);
+      // ---------------------------------------------------------------- TMA producers (both CTAs)
+      // One thread loads P, one Q. Every cycle of this loop counts: a k-block takes the MMAs 512
+      // cycles, and a copy takes its thread about 100 (one thread for both operands, two boxes each
+      // where they are MN-major, needed 600 a k-block). So everything that a job fixes is in
+      // registers before its k-loop.
+      const bool is_p = warp == 0;
+      const uint32_t s0 = tc::smem_u32(is_p ? sA : sB);
       const uint32_t lead0 = tc::map_to_rank(full0, 0);  // all loads complete on the leader's barriers
       uint32_t s = 0, ph = 1;
       long long done = 0;  // stages armed so far
@@ -761,35 +759,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int ji = job_of(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of(j, t - B.start[ji]);
-        const CUtensorMap* const P = &j.P;
         const bool up = (kKinds & kGluFwd) != 0 && !leader;  // one CTA has the gate's columns, the other up's
-        const CUtensorMap* const Q = up ? &j.Up : &j.Q;
-        const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
-        const int row0 = w.ti * kTileM + static_cast<int>(rank) * 128;  // this CTA's rows of P
-        const int width = j.tile_n >> 1;                                // this CTA's columns of Q
-        const bool wide = width == 128, has_a = leader || j.a_rows == 128;
+        const CUtensorMap* const map = is_p ? &j.P : up ? &j.Up : &j.Q;
+        const bool mn = (is_p ? j.a_mn : j.b_mn) != 0;
+        const int width = j.tile_n >> 1;  // this CTA's columns of Q
+        // this CTA's first row of P, or column of Q
+        const int first = is_p                        ? w.ti * kTileM + static_cast<int>(rank) * 128
+                          : (kKinds & kGluFwd) != 0 ? w.tj * width
+                                                    : w.tj * j.tile_n + static_cast<int>(rank) * width;
+        // (a single tile of at most 128 rows: the other rows' accumulators are of no use to anyone)
+        const bool any = !is_p || leader || j.a_rows == 128, two = is_p || width == 128;
         const uint32_t tx = static_cast<uint32_t>(j.tx);
-        const int col0 = (kKinds & kGluFwd) != 0 ? w.tj * width : w.tj * j.tile_n + static_cast<int>(rank) * width;
         const int k_end = w.kb1 * kTileK;
         for (int k = w.kb0 * kTileK; k < k_end; k += kTileK) {
           if (!wait(empty0 + 8 * s, ph, err)) {
             ok = false;
             break;
           }
-          if (leader) tc::mbar_arrive_expect_tx(full + s, tx);  // both CTAs' halves of P and Q
-          const uint32_t bar = lead0 + 8 * s, a = a0 + s * kHalfBytes, b = b0 + s * kHalfBytes;
-          if (!amn) {
-            // (a single tile of at most 128 rows: the other rows' accumulators are of no use to anyone)
-            if (has_a) load_box(a, P, bar, k, row0);
+          if (is_p && leader) tc::mbar_arrive_expect_tx(full + s, tx);  // both operands' bytes, both CTAs'
+          const uint32_t bar = lead0 + 8 * s, to = s0 + s * kHalfBytes;
+          if (!mn) {
+            if (any) load_box(to, map, bar, k, first);
           } else {
-            load_box(a, P, bar, row0, k);
-            load_box(a + kMnBoxBytes, P, bar, row0 + 64, k);
-          }
-          if (!bmn) {
-            load_box(b, Q, bar, k, col0);
-          } else {
-            load_box(b, Q, bar, col0, k);
-            if (wide) load_box(b + kMnBoxBytes, Q, bar, col0 + 64, k);
+            load_box(to, map, bar, first, k);
+            if (two) load_box(to + kMnBoxBytes, map, bar, first + 64, k);
           }
           ++done;
           if (++s == kStages) {
@@ -798,7 +791,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok && leader) {  // the leader's stage barriers count both CTAs' copies: leave none in flight
+      if (!ok && is_p && leader) {  // the leader's stage barriers count all copies: leave none in flight
         for (long long q = done > kStages ? done - kStages : 0; q < done; ++q)
           wait_drain(full0 + 8 * static_cast<uint32_t>(q % kStages), static_cast<uint32_t>(q / kStages) & 1u);
       }
@@ -854,12 +847,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       wait_drain(tc::smem_u32(drain), 0);
     }
   } else {
-    // ------------------------------------------------------------------ epilogue (warps 2..9)
+    // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3;          // this warp may read TMEM lanes [32 quad, 32 quad + 32)
-    const int half = (warp - 2) >> 2;   // and takes this half of the columns
+    const int half = (warp - kFirstEpi) >> 2;   // and takes this half of the columns
     const uint32_t tempty_leader[2] = {tc::map_to_rank(tc::smem_u32(tempty), 0),
                                        tc::map_to_rank(tc::smem_u32(tempty + 1), 0)};
-    const uint32_t box = tc::smem_u32(sEpi) + (warp - 2) * kBoxBytes;
+    const uint32_t box = tc::smem_u32(sEpi) + (warp - kFirstEpi) * kBoxBytes;
     uint16_t* swap = sSwap + 64 * quad;
     const int rows0 = static_cast<int>(rank) * 128 + 32 * quad;  // this warp's rows within a tile
     Kept<kKept> kept;
@@ -1120,6 +1113,8 @@ zopt_status launch(const char* fn, Batch& b, int kinds, cudaStream_t s) {
     const long long units = tiles * j.splits;
     if (tiles < 1 || total + units > 0x7FFFFFFFLL) return fail(ZOPT_EINVAL, std::string(fn) + ": too many tiles");
     j.tiles = static_cast<int>(tiles);
+    j.per_split = Divisor(static_cast<uint32_t>(tiles));
+    j.per_line = Divisor(static_cast<uint32_t>(j.rows_fast ? j.tiles_m : j.tiles_n));
     b.start[i] = static_cast<int>(total);
     total += units;
   }

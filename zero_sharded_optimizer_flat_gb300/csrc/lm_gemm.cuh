@@ -14,6 +14,7 @@
 
 #include <cstdint>
 
+#include "divisor.cuh"
 #include "internal.h"
 
 namespace zopt {
@@ -25,7 +26,8 @@ constexpr int kStages = 6;
 constexpr int kHalfBytes = 128 * kTileK * 2;  // one CTA's half of a stage's P or Q: 16 KiB
 constexpr int kMnBoxBytes = 64 * kTileK * 2;  // one 64 (MN) x 64 (K) box of an MN-major operand
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 TMA, warp 1 MMA, warps 2..9 epilogue
+constexpr int kFirstEpi = 3;  // warp 0 loads P, warp 1 issues the MMAs, warp 2 loads Q, warps 3 .. 10 epilogue
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kBoxBytes = 32 * 128;  // an epilogue warp's results on their way to memory: 32 rows of 128 bytes
 constexpr int kSwapBytes = 4 * 64 * 2;  // kGluFwd: two warps' block exponents for each quarter of the rows
 constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxBytes + kSwapBytes + 1024 + 256;
@@ -54,6 +56,7 @@ struct Job {
   int a_rows;  // rows of P (K-major) a CTA loads at a time: 128, or M rounded up to 8 where M <= 128
   int tx;      // bytes of a stage, both CTAs'
   int tiles_m, tiles_n, tiles;
+  Divisor per_split, per_line;  // by tiles; by the tiles that follow one another (set at the launch)
   int nk, kb_per_split, splits;
   int whole;      // its inner length is not cut
   int rows_fast;  // consecutive tiles walk down a tile column (else along a tile row)
