@@ -80,10 +80,12 @@ __device__ __forceinline__ bool elect_one() {
 //
 // A warp's results are 32 rows, one lane each; memory wants consecutive lanes along a row. So a lane
 // writes its row (128 bytes) into the warp's 4 KiB box and the warp stores the box row by row. The
-// box's 16-byte piece q of row r lies at piece q ^ (r & 7): neither side meets a bank twice. (Through
-// 2 KiB boxes handed to the TMA a tile of bf16 results took its warps 6000 cycles, this way 3700.)
+// box's 16-byte piece q of row r lies at piece q ^ r', r' the low three bits of r in reverse: eight
+// lanes at a time meet every bank once, whether they are eight rows' one piece, one row's eight, two
+// rows' four or four rows' two. (Through 2 KiB boxes handed to the TMA a tile of bf16 results took its
+// warps 6000 cycles, this way 3700.)
 __device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int q) {
-  return box + static_cast<uint32_t>(row * 128 + ((q ^ (row & 7)) << 4));
+  return box + static_cast<uint32_t>(row * 128) + ((static_cast<uint32_t>(q) ^ (__brev(static_cast<uint32_t>(row & 7)) >> 29)) << 4);
 }
 // Pieces q0 .. of the lane's row. (box is a multiple of 128.)
 template <int kWords>
@@ -575,9 +577,7 @@ __device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t* 
   for (int i = 0; i < 4 * kWords / kPiece; ++i) {
     Piece v{};
     if ((i + 1) * kPiece <= bytes) v = __ldg(reinterpret_cast<const Piece*>(p) + i);
-    if constexpr (kPiece == 16) {
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    } else if constexpr (kPiece == 8) {
+    if constexpr (kPiece == 8) {
       x[2 * i] = v.x, x[2 * i + 1] = v.y;
     } else if constexpr (kPiece == 4) {
       x[i] = v;
@@ -588,33 +588,71 @@ __device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t* 
   }
 }
 
-// Gate and up of 32 columns as they are read. kWide: every row, and up's offset in it, is a multiple
-// of 16 bytes, and so is the last columns' number.
-template <int kKept>
+// Gate and up of 32 rows' 32 columns. Where every row, and up's offset in it, is a multiple of 16 bytes
+// (kWide) consecutive lanes load along a row, and the warp's box turns the pieces into rows, a lane
+// each, when they are used: a load that takes 16 bytes of 32 rows keeps the L1 data path, which
+// the epilogue shares with the MMAs' operands, busy four times as long. Else each lane loads its row.
+template <int kKept, bool kWide>
 struct Kept {
   static constexpr int kWords = kKept == kKeep8 ? 8 : 16, kSize = kKept == kKeep8 ? 1 : 2;
+  static constexpr int kPerRow = kWords / 4, kAtOnce = 32 / kPerRow;  // pieces of a row's part, rows of a load
   uint32_t x[2][kWords];
-  template <bool kWide>
-  __device__ __forceinline__ void load(const Job& j, int row, int col) {
+  // from row row0 and column col on
+  __device__ __forceinline__ void load(const Job& j, int row0, int col, int lane) {
+    if constexpr (kWide) {
+      const int at = col * kSize + 16 * (lane % kPerRow);
+      const long long pitch = j.ld_kept * kSize, up = static_cast<long long>(j.hidden) * kSize;
+      int row = row0 + lane / kPerRow;
+      const uint8_t* p = static_cast<const uint8_t*>(j.kept) + row * pitch + at;
+#pragma unroll
+      for (int i = 0; i < kPerRow; ++i) {
+        uint4 g = make_uint4(0, 0, 0, 0), u = g;
+        if (at < up && row < j.M) g = __ldg(reinterpret_cast<const uint4*>(p)), u = __ldg(reinterpret_cast<const uint4*>(p + up));
+        x[0][4 * i] = g.x, x[0][4 * i + 1] = g.y, x[0][4 * i + 2] = g.z, x[0][4 * i + 3] = g.w;
+        x[1][4 * i] = u.x, x[1][4 * i + 1] = u.y, x[1][4 * i + 2] = u.z, x[1][4 * i + 3] = u.w;
+        row += kAtOnce, p += kAtOnce * pitch;
+      }
+    } else {
+      load_row(j, row0 + lane, col);
+    }
+  }
+  // What was loaded becomes the lane's row (through the warp's box).
+  __device__ __forceinline__ void turn(uint32_t box, int lane) {
+    if constexpr (kWide) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int i = 0; i < kPerRow; ++i)
+          box_put4(box, lane / kPerRow + i * kAtOnce, part * kPerRow + lane % kPerRow, x[part][4 * i], x[part][4 * i + 1],
+                   x[part][4 * i + 2], x[part][4 * i + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int i = 0; i < kPerRow; ++i)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[part][4 * i]), "=r"(x[part][4 * i + 1]), "=r"(x[part][4 * i + 2]), "=r"(x[part][4 * i + 3])
+                       : "r"(box_piece(box, lane, part * kPerRow + i))
+                       : "memory");
+      __syncwarp();
+    }
+  }
+  __device__ __forceinline__ void load_row(const Job& j, int row, int col) {
     const bool in = row < j.M && col < j.hidden;
     const int bytes = in ? min(32, j.hidden - col) * kSize : 0;
     const uint8_t* p = static_cast<const uint8_t*>(j.kept) + (in ? (static_cast<long long>(row) * j.ld_kept + col) * kSize : 0);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const uint8_t* at = p + (in ? static_cast<long long>(part) * j.hidden * kSize : 0);
-      if constexpr (kWide) {
-        words_in<kWords, uint4>(at, bytes, x[part]);
+      const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) | static_cast<unsigned>(bytes);
+      if ((mis & 7u) == 0) {
+        words_in<kWords, uint2>(at, bytes, x[part]);
+      } else if ((mis & 3u) == 0) {
+        words_in<kWords, uint32_t>(at, bytes, x[part]);
+      } else if (kSize == 2) {
+        words_in<kWords, uint16_t>(at, bytes, x[part]);
       } else {
-        const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(at)) | static_cast<unsigned>(bytes);
-        if ((mis & 7u) == 0) {
-          words_in<kWords, uint2>(at, bytes, x[part]);
-        } else if ((mis & 3u) == 0) {
-          words_in<kWords, uint32_t>(at, bytes, x[part]);
-        } else if (kSize == 2) {
-          words_in<kWords, uint16_t>(at, bytes, x[part]);
-        } else {
-          words_in<kWords, uint8_t>(at, bytes, x[part]);
-        }
+        words_in<kWords, uint8_t>(at, bytes, x[part]);
       }
     }
   }
@@ -642,19 +680,18 @@ struct Scales {
 // dgate = dh up a'(gate), dup = dh a(gate), h = a(gate) up, each rounded to bf16 once: they are
 // operands of the three products that follow. `k` holds the kept values of the warp's first 32
 // columns; while 32 columns are worked on the next ones are on their way, at a tile's end the next
-// tile's first (row and column next_row and next_col): gate and up come from HBM, and a tile that
+// tile's first (from row next_row0 and column next_col on): gate and up come from HBM, and a tile that
 // began by waiting for them would take longer than its products.
 template <int kAct, int kKept, bool kWide>
 __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                            uint32_t box, Kept<kKept>& k, Scales& sc, int next_row, int next_col) {
-  const int row = row0 + lane;
+                                            uint32_t box, Kept<kKept, kWide>& k, Scales& sc, int next_row0, int next_col) {
   const int width = j.tile_n >> 1;
   const int col0 = w.tj * j.tile_n + width * h;
   const Out<64> dgate(j.out, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, j.M, col0, j.N, lane);
   const Out<64> hout(j.out_h, j.ld_h, 2, row0, j.M, col0, j.N, lane);
   Scales next_sc;
-  if constexpr (kKept == kKeep8) next_sc.load(j, next_row, next_col);
+  if constexpr (kKept == kKeep8) next_sc.load(j, next_row0 + lane, next_col);
 #pragma unroll 1
   for (int c = 0; 32 * c < width; ++c) {
     const int col = col0 + 32 * c;
@@ -662,9 +699,10 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const A
     uint32_t v[32];
     acc.read32(width * h + 32 * c, v);
     if (last) acc.done();
-    Kept<kKept> next;
-    next.template load<kWide>(j, last ? next_row : row, last ? next_col : col + 32);
+    Kept<kKept, kWide> next;
+    next.load(j, last ? next_row0 : row0, last ? next_col : col + 32, lane);
     if (col < j.N && row0 < j.M) {
+      k.turn(box, lane);
       uint32_t hh[16];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {  // eight columns: a piece of each result
@@ -862,20 +900,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t box = tc::smem_u32(sEpi) + (warp - kFirstEpi) * kBoxBytes;
     uint16_t* swap = sSwap + 64 * quad;
     const int rows0 = static_cast<int>(rank) * 128 + 32 * quad;  // this warp's rows within a tile
-    Kept<kKept> kept;
+    Kept<kKept, kWide> kept;
     Scales scales;
-    auto first_of = [&](int t, int& row, int& col) {  // the lane's row and the warp's first column of unit t (kGluBwd)
+    auto first_of = [&](int t, int& row, int& col) {  // the warp's first row and column of unit t (kGluBwd)
       row = B.job[0].M, col = 0;
       if (t >= total) return;
       const Unit w = unit_of(B.job[0], t);
-      row = w.ti * kTileM + rows0 + lane;
+      row = w.ti * kTileM + rows0;
       col = w.tj * B.job[0].tile_n + (B.job[0].tile_n >> 1) * half;
     };
     if constexpr ((kKinds & kGluBwd) != 0) {
       int row, col;
       first_of(unit_at(B, pair, npairs, 0), row, col);
-      kept.template load<kWide>(B.job[0], row, col);
-      if constexpr (kKept == kKeep8) scales.load(B.job[0], row, col);
+      kept.load(B.job[0], row, col, lane);
+      if constexpr (kKept == kKeep8) scales.load(B.job[0], row + lane, col);
     }
     int it = 0;
     for (int t; (t = unit_at(B, pair, npairs, it)) < total;) {
