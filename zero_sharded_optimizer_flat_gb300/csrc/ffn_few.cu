@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(T)) down_kernel(const Ma
       phi = 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.0f);
     }
     const float h = in && live ? g / (1.0f + __expf(-phi)) * u : 0.0f;
-    if (t < T) hs[i * T + t] = __bfloat162float(__float2bfloat16_rn(h));  // as the other path hands it on
+    if (t < T) hs[i * T + t] = h;  // in fp32: nothing here needs the bf16 operand that the tensor cores do
   }
   __syncthreads();
   F2 acc[T][4];
