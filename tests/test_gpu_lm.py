@@ -120,6 +120,43 @@ def test_cross_entropy(zopt, t, d, v, ld):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("t,d,v,ld", [(1, 1, 3, None), (1, 520, 20001, None), (2, 264, 5000, None), (1, 2049, 61, None),
+                                      (2, 767, 2049, 771), (2, 100, 9, 104), (1, 250, 4863, 253)])
+def test_cross_entropy_of_few_tokens(zopt, t, d, v, ld):
+    """One and two tokens, rows of less and more than a warp's pieces, the last entry the target."""
+    x, w, target, dloss = ce_case(40 + t + d + v, t, d, v, ld, ignored=0.0)
+    target[0] = v - 1
+    got = run_ce(zopt, x, w, target, dloss, ld_out=d + 3 if ld else None)
+    check_ce(x, w, target, dloss, got)
+    again = run_ce(zopt, x, w, target, dloss, ld_out=d + 3 if ld else None)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    if t == 2:  # the other row's overflow, and its being ignored, leave this one as it is
+        x2, y2 = x.clone(), target.clone()
+        x2[1] = float("inf")
+        loss, lse = run_ce(zopt, x2, w, target, dloss)[:2]
+        assert torch.equal(loss[0], got[0][0]) and torch.equal(lse[0], got[1][0]) and torch.isnan(loss[1])
+        y2[1] = -100
+        loss, lse = run_ce(zopt, x2, w, y2, dloss)[:2]
+        assert torch.equal(loss[0], got[0][0]) and torch.equal(lse[0], got[1][0]) and loss[1] == 0 and lse[1] == 0
+
+
+@pytest.mark.parametrize("t", [1, 2])
+def test_cross_entropy_of_few_tokens_large_and_infinite_logits(zopt, t):
+    """Logits of +-2e4, and weights of the lowest value and minus infinity: entries that take no part."""
+    gen = torch.Generator(device="cuda").manual_seed(12 + t)
+    x, w = rows(gen, t, 64, 40.0).abs(), rows(gen, 700, 64, 40.0)
+    w[5], w[699] = float("-inf"), torch.finfo(torch.bfloat16).min
+    target = torch.randint(6, 699, (t,), generator=gen, device="cuda")
+    loss, lse = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+    zopt.linear_ce_forward(x, w, target, loss, lse, zopt.new_linear_ce_workspace(x, w, backward=False))
+    keep = [v for v in range(700) if v not in (5, 699)]
+    shifted = target.cpu().numpy() - 1  # (entry 5 lies below every target)
+    rl, re = lm.ce_forward(f64(x), f64(w)[keep], shifted)
+    size = 1 + (np.abs(f64(x)) @ np.abs(f64(w)[keep]).T).max(axis=1)
+    assert np.all(np.abs(f64(loss) - rl) <= 2.0 ** -20 * size + 2.0 ** -23 * np.abs(rl))
+    assert np.all(np.abs(f64(lse) - re) <= 2.0 ** -20 * size + 2.0 ** -23 * np.abs(re))
+
+
 def test_cross_entropy_outputs_end_inside_a_16_byte_piece(zopt):
     """Rows whose distance the TMA could move but whose width it could not end at."""
     x, w, target, dloss = ce_case(5, 70, 44, 300)

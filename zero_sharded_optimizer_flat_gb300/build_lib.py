@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libzopt.so")
 
 SOURCES = ["common.cpp", "layout.cpp", "norm.cu", "norm_noalloc.cu", "adamw.cu", "rescale.cu", "accum.cu", "ns.cu", "ns_gemm.cu",
            "ns_prep.cu", "ns_fused.cu", "ns_simt.cu", "muon.cu", "lm_gemm.cu", "act8.cu", "ffn.cu",
-           "ffn_few.cu", "linear_ce.cu"]
+           "ffn_few.cu", "linear_ce.cu", "linear_ce_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -2,7 +2,8 @@
 //
 // Forward: one product launch whose epilogue turns each row's 128 logits of a tile into a maximum
 // and a sum (base 2), and one launch that joins a row's pieces: 2 T V D flops, and 8 bytes a row and
-// 128 logits of partial results instead of the logits' 2 to 4 bytes each.
+// 128 logits of partial results instead of the logits' 2 to 4 bytes each. One or two tokens take
+// linear_ce_few.cu in place of the first launch.
 //
 // Backward: dl needs each row's whole lse, so the logits are computed a second time: 6 T V D flops in
 // all. The vocabulary is walked in pieces: piece i's dl is written to a workspace buffer in bf16
@@ -13,8 +14,7 @@
 // fp32 sum.
 //
 // Measured (GB300): forward 4096 x 768 x 50304 187 us = 1.69 PFLOP/s, the rate of a large bf16 product
-// under the power cap; backward 8192 x 2048 x 32000 1.98 ms = 1.63 PFLOP/s; one token forward, 2048 x
-// 32000, 33 us = 4.0 TB/s.
+// under the power cap; backward 8192 x 2048 x 32000 1.98 ms = 1.63 PFLOP/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,6 +22,7 @@
 
 #include "act8_host.h"
 #include "launch.cuh"
+#include "linear_ce_few.h"
 #include "lm_gemm.cuh"
 #include "ns_internal.h"
 #include "tc.cuh"
@@ -38,6 +39,7 @@ constexpr long long kMaxElems = 1LL << 44;  // of any matrix, the logits too: ti
 constexpr long long kPieceBytes = 128LL << 20, kPieceLeast = 4096;
 
 struct CePlan {
+  bool few;  // the forward on the CUDA cores
   bool stage_x, stage_w;
   long long pitch;  // staged rows: dim rounded up to 8
   long long piece;  // vocabulary entries per piece, a multiple of 256
@@ -80,6 +82,12 @@ CePlan plan(const zopt_linear_ce_job& c, bool backward) {
   CePlan p{};
   const long long T = c.tokens, D = c.dim, V = c.vocab;
   p.pitch = round_up(D, 8);
+  if (!backward && few::takes(c)) {
+    p.few = true;
+    p.part = take(p.total, few::ce_parts(c) * T * 8);
+    p.tlogit = take(p.total, T * 4);
+    return p;
+  }
   p.stage_x = c.ld_x % 8 != 0;
   p.stage_w = c.ld_w % 8 != 0;
   size_t at = 0;
@@ -122,10 +130,9 @@ CePlan plan(const zopt_linear_ce_job& c, bool backward) {
 }
 
 // What the backward's products need beside the logits' gradient (12.5 us for 8192 x 2048, of 1.98 ms).
-// Block 0: *unit = the largest finite
-// |dloss| of a counted row (1 if there is none). The others: xm = x with its ignored rows zero, the
-// operand of dw, which must not meet whatever such rows hold (0 times inf is not 0): 4 bytes an
-// entry of x beside 6 V flops.
+// Block 0: *unit = the largest finite |dloss| of a counted row (1 if there is none). The others: xm =
+// x with its ignored rows zero, the operand of dw, which must not meet whatever such rows hold (0
+// times inf is not 0): 4 bytes an entry of x beside 6 V flops.
 __global__ void __launch_bounds__(256)
     ce_prep_kernel(float* unit, const float* dloss, const int64_t* target, int64_t ignore, long long tokens,
                    uint16_t* xm, long long pitch, const uint16_t* x, long long ld_x, long long rows, long long dim) {
@@ -158,11 +165,12 @@ __global__ void __launch_bounds__(256)
 }
 
 // A row's pieces joined: lse = (M + log2 sum_p s_p 2^(m_p - M)) / kLog2e. Lanes are rows, the block's
-// warps share the pieces. The last steps are in fp64, once a row: in fp32 the sum of a maximum near
-// 15 and a logarithm is rounded by 1e-6, which a loss much smaller than lse shows (1.3e-6 against
-// the 1e-7 of the rest); dividing by the very constant that scaled the logits undoes its rounding. Bound by reading the pieces
-// once: 12 us for the 13 MB of 4096 rows and 393 pieces.
-constexpr int kJoinWarps = 16;
+// warps share the pieces. The last sum is in fp64, once a row: in fp32 the sum of a maximum near 15
+// and a logarithm is rounded by 1e-6, which a loss much smaller than lse shows (1.3e-6 against the 1e-7
+// of the rest; the logarithm itself is then small, and its own fp32 rounding with it); dividing by the
+// very constant that scaled the logits undoes its rounding. Bound by its loads' latency, so a warp has
+// kJoinAhead pieces in flight (one at a time: 12 us for the 13 MB of 4096 rows and 393 pieces, for 7.6).
+constexpr int kJoinWarps = 16, kJoinAhead = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     ce_join_kernel(const float2* part, int parts, long long tokens, const int64_t* target, int64_t ignore,
                    int64_t vocab, const float* tlogit, float* loss, float* lse) {
@@ -173,29 +181,40 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const long long row = static_cast<long long>(blockIdx.x) * 32 + lane;
   float m = -INFINITY, s = 0.0f;
   if (row < tokens) {
-    for (int p = warp; p < parts; p += kJoinWarps) {
-      const float2 v = part[static_cast<long long>(p) * tokens + row];
-      const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
-      s = s * exp2f(m - base) + v.y * exp2f(v.x - base);
+    for (int p0 = warp; p0 < parts; p0 += kJoinAhead * kJoinWarps) {
+      float2 v[kJoinAhead];
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) {
+        const int p = p0 + i * kJoinWarps;
+        v[i] = p < parts ? part[static_cast<long long>(p) * tokens + row] : make_float2(-INFINITY, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) mn = fmaxf(mn, v[i].x);
+      const float base = mn == -INFINITY ? 0.0f : mn;
+      s *= exp2f(m - base);
+#pragma unroll
+      for (int i = 0; i < kJoinAhead; ++i) s = fmaf(v[i].y, exp2f(v[i].x - base), s);
       m = mn;
     }
   }
   sh[warp][lane] = make_float2(m, s);
   __syncthreads();
   if (warp != 0 || row >= tokens) return;
-  for (int w = 1; w < kJoinWarps; ++w) {
-    const float2 v = sh[w][lane];
-    const float mn = fmaxf(m, v.x), base = mn == -INFINITY ? 0.0f : mn;
-    s = s * exp2f(m - base) + v.y * exp2f(v.x - base);
-    m = mn;
-  }
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, sh[w][lane].x);
+  const float base = m == -INFINITY ? 0.0f : m;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) s = fmaf(sh[w][lane].y, exp2f(sh[w][lane].x - base), s);
   const int64_t t = target[row];
   if (t == ignore) {
     loss[row] = 0.0f;
     lse[row] = 0.0f;
     return;
   }
-  const double l = (static_cast<double>(m) + log2(static_cast<double>(s))) / static_cast<double>(kLog2e);
+  constexpr double kLn2 = 1.0 / static_cast<double>(kLog2e);
+  const double l = (static_cast<double>(m) + static_cast<double>(log2f(s))) * kLn2;
   lse[row] = static_cast<float>(l);
   loss[row] = t >= 0 && t < vocab ? static_cast<float>(l - static_cast<double>(tlogit[row])) : __uint_as_float(0x7FC00000u);
 }
@@ -265,24 +284,32 @@ zopt_status forward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, c
   TRY(ns::take_error_word(fn, &b.err));
   const CePlan p = plan(c, false);
   uint8_t* ws = static_cast<uint8_t*>(d_ws);
-  const uint16_t *x, *w;
-  long long px, pw;
-  TRY(stage_inputs(fn, c, p, ws, &x, &px, &w, &pw, s));
-  b.n = 1;
-  Job& j = b.job[0];
-  j.kind = kCeFwd;
-  j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.vocab), j.K = static_cast<int>(c.dim);
-  set_tiles(j);
-  ce_fields(j, c);
-  j.part = reinterpret_cast<float2*>(ws + p.part);
-  j.tlogit = reinterpret_cast<float*>(ws + p.tlogit);
-  TRY(map_p(fn, j, x, px));
-  TRY(map_q(fn, j, w, c.vocab, pw));
-  TRY(launch(fn, b, kCeFwd, s));
-  const int parts = static_cast<int>((c.vocab + j.tile_n / 2 - 1) / (j.tile_n / 2));
+  float2* part = reinterpret_cast<float2*>(ws + p.part);
+  float* tlogit = reinterpret_cast<float*>(ws + p.tlogit);
+  int parts;
+  if (p.few) {
+    TRY(few::ce_logits(c, part, tlogit, s));
+    parts = few::ce_parts(c);
+  } else {
+    const uint16_t *x, *w;
+    long long px, pw;
+    TRY(stage_inputs(fn, c, p, ws, &x, &px, &w, &pw, s));
+    b.n = 1;
+    Job& j = b.job[0];
+    j.kind = kCeFwd;
+    j.M = static_cast<int>(c.tokens), j.N = static_cast<int>(c.vocab), j.K = static_cast<int>(c.dim);
+    set_tiles(j);
+    ce_fields(j, c);
+    j.part = part;
+    j.tlogit = tlogit;
+    TRY(map_p(fn, j, x, px));
+    TRY(map_q(fn, j, w, c.vocab, pw));
+    TRY(launch(fn, b, kCeFwd, s));
+    parts = static_cast<int>((c.vocab + j.tile_n / 2 - 1) / (j.tile_n / 2));
+  }
   return launch_pdl(ce_join_kernel, dim3(static_cast<unsigned>((c.tokens + 31) / 32)), dim3(32 * kJoinWarps), 0, s,
-                    static_cast<const float2*>(j.part), parts, static_cast<long long>(c.tokens), c.target,
-                    c.ignore_index, c.vocab, static_cast<const float*>(j.tlogit), c.loss, c.lse);
+                    static_cast<const float2*>(part), parts, static_cast<long long>(c.tokens), c.target,
+                    c.ignore_index, c.vocab, static_cast<const float*>(tlogit), c.loss, c.lse);
 }
 
 zopt_status backward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, cudaStream_t s) {
