@@ -8,9 +8,9 @@
 // and writes dgate, dup and h; then dx, dgate_up and ddown in one launch, longest units first, so
 // that only one launch's last wave runs short. 18 T D F flops for both directions.
 //
-// Measured (GB300, 8192 x 2048 x 5632): forward 361 us = 1.57 PFLOP/s (gate and up 202, y 110 by
-// themselves); both directions with 8-bit checkpoints 1.10 ms = 1.54 PFLOP/s (the backward's two
-// launches 147 and 495 by themselves), at the power cap, where a plain bf16 product runs at 1.70.
+// Measured (GB300, 8192 x 2048 x 5632): forward 361 us = 1.57 PFLOP/s (gate and up 200, y 109 by
+// themselves); both directions with 8-bit checkpoints 1.10 ms = 1.55 PFLOP/s (the backward's two
+// launches 139 and 495 by themselves), at the power cap, where a plain bf16 product runs at 1.70.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -167,11 +167,12 @@ __global__ void __launch_bounds__(256)
 // A row's pieces joined: lse = (M + log2 sum_p s_p 2^(m_p - M)) / kLog2e. Lanes are rows and the block's
 // warps share the pieces; or, up to as many rows as such blocks make one wave (kJoinOneRow, four an
 // SM), a block's threads share one row's: one token and 304 pieces 8.2 us for 4.1, cross entropy
-// forward of 300 x 768 x 50304 33.7 us for 31.0, of 600 x 256 x 4096 11.1 for 11.3. The last sum is in fp64, once a row: in fp32 the sum of a maximum near 15
-// and a logarithm is rounded by 1e-6, which a loss much smaller than lse shows (1.3e-6 against the 1e-7
-// of the rest; the logarithm itself is then small, and its own fp32 rounding with it); dividing by the
-// very constant that scaled the logits undoes its rounding. Bound by its loads' latency, so a warp has
-// kJoinAhead pieces in flight (one at a time: 12 us for the 13 MB of 4096 rows and 393 pieces, for 7.6).
+// forward of 300 x 768 x 50304 33.7 us for 31.0, of 600 x 256 x 4096 11.1 for 11.3.
+// The last sum is in fp64, once a row: in fp32 the sum of a maximum near 15 and a logarithm is rounded
+// by 1e-6, which a loss much smaller than lse shows (1.3e-6 against the 1e-7 of the rest; the logarithm
+// itself is then small, and its own fp32 rounding with it); dividing by the very constant that scaled
+// the logits undoes its rounding. Bound by its loads' latency, so a warp has kJoinAhead pieces in
+// flight (one at a time: 12 us for the 13 MB of 4096 rows and 393 pieces, for 7.6).
 constexpr int kJoinWarps = 16, kJoinAhead = 8, kJoinOneRow = 608;
 template <bool kOneRow>
 __global__ void __launch_bounds__(32 * kJoinWarps)

@@ -14,7 +14,7 @@
 // Bound by the tensor cores where the inner length is long enough to hide a tile's epilogue (12 to 30
 // k-blocks' time): 521 cycles a k-block of 512, tensor pipe 92 % of elapsed in the cross entropy's
 // forward (4096 x 768 x 50304), 89 % in the block's first product and 90 % in its backward's second
-// launch (8192 x 2048 x 5632), all three at the clock that the power cap leaves; 60 % in the
+// launch (8192 x 2048 x 5632), all three at the clock that the power cap leaves; 61 % in the
 // backward's first launch, whose epilogue (three results and two kept inputs an entry) outlasts its
 // 32 k-blocks; 76 % in y, 256 tiles over 76 pairs.
 #include <cuda_fp16.h>
@@ -590,9 +590,9 @@ __device__ __forceinline__ void words_in(const uint8_t* p, int bytes, uint32_t* 
 
 // Gate and up of 32 rows' 32 columns. Where every row, and up's offset in it, is a multiple of 16 bytes
 // (kWide) consecutive lanes load along a row, and the warp's box turns the pieces into rows, a lane
-// each, when they are used: a load that takes 16 bytes of 32 rows keeps the L1 data path, which
-// the epilogue shares with the MMAs' operands, busy four times as long (backward's first launch of 8192 x
-// 2048 x 5632, 8 bits kept: 144 us for 139). Else each lane loads its row.
+// each, when they are used: a load that takes 16 bytes of 32 rows keeps the L1 data path, which the
+// epilogue shares with the MMAs' operands, busy four times as long (the backward's first launch of
+// 8192 x 2048 x 5632, 8 bits kept: 144 us for 139). Else each lane loads its row.
 template <int kKept, bool kWide>
 struct Kept {
   static constexpr int kWords = kKept == kKeep8 ? 8 : 16, kSize = kKept == kKeep8 ? 1 : 2;
