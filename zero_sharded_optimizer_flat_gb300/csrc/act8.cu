@@ -13,6 +13,7 @@
 #include "act8.cuh"
 #include "act8_host.h"
 #include "divisor.cuh"
+#include "guarded.h"
 #include "launch.cuh"
 #include "tc.cuh"
 

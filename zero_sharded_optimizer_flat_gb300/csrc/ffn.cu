@@ -18,6 +18,7 @@
 
 #include "act8_host.h"
 #include "ffn_few.h"
+#include "guarded.h"
 #include "launch.cuh"
 #include "lm_gemm.cuh"
 #include "ns_internal.h"

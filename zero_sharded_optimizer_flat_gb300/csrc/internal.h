@@ -15,17 +15,6 @@ zopt_status fail(zopt_status st, const std::string& msg);
 // Clears the last error and returns ZOPT_OK.
 zopt_status ok();
 
-// Runs an entry point's body; a C++ exception (an allocation that fails while a message is built)
-// becomes a status, since none may leave a C function.
-template <typename F>
-zopt_status guarded(F body) noexcept {
-  try {
-    return body();
-  } catch (...) {
-    return ZOPT_ECUDA;
-  }
-}
-
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // SM count of the current device (cached per device ordinal); 0 on error.

@@ -21,6 +21,7 @@
 #include <string>
 
 #include "act8_host.h"
+#include "guarded.h"
 #include "launch.cuh"
 #include "linear_ce_few.h"
 #include "lm_gemm.cuh"
