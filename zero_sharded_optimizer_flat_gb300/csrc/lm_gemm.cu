@@ -493,6 +493,20 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Ac
   }
 }
 
+// Whether both of the two warps that share barrier `bar` bring ok. Every lane of both has to come.
+__device__ __forceinline__ bool both_warps(int ok, int bar) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok), "r"(bar)
+      : "memory");
+  return r != 0;
+}
+
 // The first half of a tile's TMEM columns hold the gate, the second the up product of the same 128 (or
 // 64) hidden columns; the warp's are half h of each. Where 8 bits are kept a tile is one block wide
 // (128): a block's largest magnitude is found within a lane and its partner in the warp that has the
@@ -527,8 +541,7 @@ __device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const A
     }
     swap[32 * h + lane] = static_cast<uint16_t>(e[0] | (e[1] << 8));
     asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
-    const uint32_t other = swap[32 * (1 - h) + lane];
-    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // read before the next tile's are written
+    const uint32_t other = swap[32 * (1 - h) + lane];  // (both_warps comes between this and the next tile's)
     e[0] = max(e[0], other & 255u), e[1] = max(e[1], other >> 8);  // the byte grows with the magnitude
     const long long nb = act8::blocks_of(j.hidden);
     if (row < j.M)
@@ -947,7 +960,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row0 = w.ti * kTileM + rows0;
       int ok = 1;
       if (lane == 0) ok = wait(tc::smem_u32(tfull + b), tph, err) ? 1 : 0;
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      // Two warps wait for one another within such a tile: if one's wait has run out, neither begins it.
+      if constexpr ((kKinds & kGluFwd) != 0 && kKept == kKeep8) ok = both_warps(ok, 1 + quad);
+      if (!ok) break;
       tc::fence_after_sync();
       const Acc acc{tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN), tempty_leader[b], lane};
       if ((kKinds & kStore) && j.kind == kStore) epi_store(j, w, acc, row0, lane, half, box);
