@@ -260,6 +260,20 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int*
 // their memory is given up.
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) { wait(bar, parity, nullptr); }
 
+// A thread that gives up leaves the others to their own waits, so one of the four threads that load may
+// have sent copies that no barrier was armed for and nobody waits for. Whoever gives up says so in both
+// CTAs, and when no thread of the pair loads any more (behind the last cluster barrier) both stay for a
+// millisecond, hundreds of times what a copy takes, before their shared memory is given up.
+constexpr unsigned long long kSettleNs = 1000000ull;
+__device__ __forceinline__ void tell_pair(uint32_t* word) {
+  for (uint32_t r = 0; r < 2; ++r)
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(tc::map_to_rank(tc::smem_u32(word), r)), "r"(1u) : "memory");
+}
+__device__ __forceinline__ void settle() {
+  const unsigned long long t0 = tc::globaltimer();
+  while (tc::globaltimer() - t0 < kSettleNs) __nanosleep(1000);
+}
+
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
@@ -785,6 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint32_t* gave_up = tslot + 1;  // some thread of the pair has stopped waiting
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_rank();
@@ -801,6 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(tempty + b, 2 * kEpiWarps);  // both CTAs' epilogue warps, one arrival each (used in the leader)
     }
     tc::mbar_init(drain, 1);
+    *gave_up = 0;
     tc::fence_mbar_init();
     for (int j = 0; j < B.n; ++j) {
       tc::prefetch_tmap(&B.job[j].P);
@@ -870,6 +886,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (!ok) tell_pair(gave_up);
       if (!ok && is_p && leader) {  // the leader's stage barriers count all copies: leave none in flight
         for (long long q = done > kStages ? done - kStages : 0; q < done; ++q)
           wait_drain(full0 + 8 * static_cast<uint32_t>(q % kStages), static_cast<uint32_t>(q / kStages) & 1u);
@@ -922,6 +939,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc::umma_commit_pair(tfull + b, 3);  // both CTAs' accumulator b is complete
       }
+      if (!ok) tell_pair(gave_up);
       tc::umma_commit_pair(drain, 1);
       wait_drain(tc::smem_u32(drain), 0);
     }
@@ -963,7 +981,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       // Two warps wait for one another within such a tile: if one's wait has run out, neither begins it.
       if constexpr ((kKinds & kGluFwd) != 0 && kKept == kKeep8) ok = both_warps(ok, 1 + quad);
-      if (!ok) break;
+      if (!ok) {
+        if (lane == 0) tell_pair(gave_up);
+        break;
+      }
       tc::fence_after_sync();
       const Acc acc{tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN), tempty_leader[b], lane};
       if ((kKinds & kStore) && j.kind == kStore) epi_store(j, w, acc, row0, lane, half, box);
@@ -979,6 +1000,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc::fence_before_sync();
   tc::cluster_sync();  // every MMA, copy and remote arrival of the pair is done
+  if (*reinterpret_cast<volatile uint32_t*>(gave_up) != 0) settle();
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc_pair(tmem, 2 * kTileN);
