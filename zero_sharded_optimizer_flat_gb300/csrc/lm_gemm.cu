@@ -30,6 +30,7 @@
 #include "launch.cuh"
 #include "lm_gemm.cuh"
 #include "ns_internal.h"
+#include "row_bytes.h"
 #include "tc.cuh"
 
 namespace zopt {
@@ -146,13 +147,13 @@ struct Out {
   uint8_t* base;
   uint8_t* mine;    // the lane's first piece
   long long pitch;  // bytes
-  int bytes, rows;  // from base to the row's end, and rows there are
+  int bytes, rows;  // from base to the row's end (or the warp's part's), and rows there are
   bool whole;
   // columns col .. of rows row0 .. of M rows and n columns of `size` bytes
   __device__ __forceinline__ Out(void* matrix, long long ld, int size, int row0, int M, int col, int n, int lane) {
     pitch = ld * size;
     base = static_cast<uint8_t*>(matrix) + row0 * pitch + static_cast<long long>(col) * size;
-    bytes = (n - col) * size;
+    bytes = row_bytes(n, col, size);
     rows = min(32, M - row0);
     mine = base + lane / kPerRow * pitch + 16 * (lane % kPerRow);
     whole = rows == 32 && ((static_cast<unsigned>(reinterpret_cast<uintptr_t>(base)) | static_cast<unsigned>(pitch)) & 15u) == 0;
