@@ -573,11 +573,12 @@ typedef struct zopt_ffn_job {
  * other pointer is looked at. 0 for a shape that the calls refuse. */
 ZOPT_API size_t zopt_ffn_workspace(const zopt_ffn_job* job, int32_t backward);
 /* Errors of both: EINVAL for NULL or misaligned pointers (16 bytes; scale bytes any), tokens < 0,
- * dim or hidden < 1, tokens or dim above 2^30, hidden above 2^29, a matrix above 2^44 elements, a
- * row distance below the row's length or above 2^32, another act, both or (backward) neither of x / x8 and of kept / kept8, a checkpoint of another
- * shape, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16; ETIMEOUT
- * if a bounded wait of an earlier call's kernel gave up. tokens = 0: the forward does nothing, the
- * backward sets the weight gradients to zero. */
+ * dim or hidden < 1, tokens above 2^30 (backward: 2^26), dim above 2^26, hidden above 2^25 (longer
+ * inner lengths could outlast the kernels' bounded waits), a matrix above 2^44 elements, a row
+ * distance below the row's length or above 2^32, another act, both or (backward) neither of x / x8
+ * and of kept / kept8, a checkpoint of another shape, a short or misaligned workspace; EUNSUPPORTED
+ * for a dtype other than ZOPT_BF16; ETIMEOUT if a bounded wait of an earlier call's kernel gave up.
+ * tokens = 0: the forward does nothing, the backward sets the weight gradients to zero. */
 ZOPT_API zopt_status zopt_ffn_forward(const zopt_ffn_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream);
 ZOPT_API zopt_status zopt_ffn_backward(const zopt_ffn_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream);
 
@@ -621,9 +622,10 @@ typedef struct zopt_linear_ce_job {
  * refuse. */
 ZOPT_API size_t zopt_linear_ce_workspace(const zopt_linear_ce_job* job, int32_t backward);
 /* Errors of both: EINVAL for NULL or misaligned pointers (matrices 16 bytes, vectors their
- * element), tokens < 0, dim or vocab < 1, any of them above 2^30, a matrix (the logits too) above
- * 2^44 elements, a row distance below dim or above 2^32, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16;
- * ETIMEOUT as above. tokens = 0: the forward does nothing, the backward sets dw to zero. */
+ * element), tokens < 0, dim or vocab < 1, tokens or vocab above 2^30, dim or (backward) tokens above
+ * 2^26 (as above), a matrix (the logits too) above 2^44 elements, a row distance below dim or above
+ * 2^32, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16; ETIMEOUT as
+ * above. tokens = 0: the forward does nothing, the backward sets dw to zero. */
 ZOPT_API zopt_status zopt_linear_ce_forward(const zopt_linear_ce_job* job, void* d_ws, size_t ws_bytes,
                                             zopt_stream stream);
 ZOPT_API zopt_status zopt_linear_ce_backward(const zopt_linear_ce_job* job, void* d_ws, size_t ws_bytes,

@@ -47,9 +47,14 @@ bool sizes_ok(const zopt_ffn_job& c) {
          c.tokens * 2 * c.hidden <= kMaxElems && c.dim * 2 * c.hidden <= kMaxElems;
 }
 
+// The inner lengths of the products: dim and hidden, the backward's 2 hidden and tokens too.
+bool inner_ok(const zopt_ffn_job& c, bool backward) {
+  return c.dim <= kMaxInner && c.hidden <= kMaxInner / 2 && (!backward || c.tokens <= kMaxInner);
+}
+
 bool shape_ok(const zopt_ffn_job& c, bool backward) {
   auto ld = [](int64_t v, int64_t least) { return v >= least && v <= kMaxLd; };
-  return c.tokens >= 0 && c.dim >= 1 && c.hidden >= 1 && sizes_ok(c) &&
+  return c.tokens >= 0 && c.dim >= 1 && c.hidden >= 1 && sizes_ok(c) && inner_ok(c, backward) &&
          ld(c.ld_gate_up, 2 * c.hidden) && ld(c.ld_down, c.dim) && (c.x8 != nullptr || ld(c.ld_x, c.dim)) &&
          (!backward || ld(c.ld_dy, c.dim));
 }
@@ -133,6 +138,7 @@ zopt_status check(const char* fn, const zopt_ffn_job* c, bool backward, void* d_
   if (c->act != ZOPT_ACT_SILU && c->act != ZOPT_ACT_GELU) return bad("act must be ZOPT_ACT_SILU or ZOPT_ACT_GELU");
   if (c->tokens < 0 || c->dim < 1 || c->hidden < 1) return bad("tokens < 0, dim < 1 or hidden < 1");
   if (!sizes_ok(*c)) return bad("tokens or dim above 2^30, hidden above 2^29 or a matrix above 2^44 elements");
+  if (!inner_ok(*c, backward)) return bad("dim above 2^26, hidden above 2^25 or, in the backward, tokens above 2^26");
   const int64_t T = c->tokens, D = c->dim, F = c->hidden;
   auto ld_bad = [](int64_t ld, int64_t least) { return ld < least || ld > kMaxLd; };
   if (ld_bad(c->ld_gate_up, 2 * F) || ld_bad(c->ld_down, D)) return bad("a weight's row distance below its row or above 2^32");

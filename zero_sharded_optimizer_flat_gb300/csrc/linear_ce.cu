@@ -60,8 +60,15 @@ bool sizes_ok(const zopt_linear_ce_job& c) {
          c.vocab * c.dim <= kMaxElems && c.tokens * c.vocab <= kMaxElems;
 }
 
-bool shape_ok(const zopt_linear_ce_job& c) {
-  return c.tokens >= 0 && c.dim >= 1 && c.vocab >= 1 && sizes_ok(c) &&
+// The inner lengths of the products: dim, the backward's tokens, and a piece of the vocabulary (2^26
+// entries at most: kPieceBytes).
+bool inner_ok(const zopt_linear_ce_job& c, bool backward) {
+  return c.dim <= kMaxInner && (!backward || c.tokens <= kMaxInner);
+}
+static_assert(kPieceBytes / 2 <= kMaxInner, "a piece is dx's inner length");
+
+bool shape_ok(const zopt_linear_ce_job& c, bool backward) {
+  return c.tokens >= 0 && c.dim >= 1 && c.vocab >= 1 && sizes_ok(c) && inner_ok(c, backward) &&
          c.ld_x >= c.dim && c.ld_w >= c.dim && c.ld_x <= kMaxLd && c.ld_w <= kMaxLd;
 }
 
@@ -240,6 +247,7 @@ zopt_status check(const char* fn, const zopt_linear_ce_job* c, bool backward, vo
   if (c->dtype != ZOPT_BF16) return fail(ZOPT_EUNSUPPORTED, f + ": dtype must be ZOPT_BF16");
   if (c->tokens < 0 || c->dim < 1 || c->vocab < 1) return fail(ZOPT_EINVAL, f + ": tokens < 0, dim < 1 or vocab < 1");
   if (!sizes_ok(*c)) return fail(ZOPT_EINVAL, f + ": tokens, dim or vocab above 2^30, or a matrix above 2^44 elements");
+  if (!inner_ok(*c, backward)) return fail(ZOPT_EINVAL, f + ": dim above 2^26 or, in the backward, tokens above 2^26");
   auto ld_bad = [&](int64_t ld) { return ld < c->dim || ld > kMaxLd; };
   if (ld_bad(c->ld_x) || ld_bad(c->ld_w) || (backward && c->dx && ld_bad(c->ld_dx)) || (backward && c->dw && ld_bad(c->ld_dw)))
     return fail(ZOPT_EINVAL, f + ": row distance below dim or above 2^32");
@@ -448,7 +456,7 @@ zopt_status backward(const zopt_linear_ce_job* cp, void* d_ws, size_t ws_bytes, 
 }  // namespace zopt
 
 extern "C" size_t zopt_linear_ce_workspace(const zopt_linear_ce_job* job, int32_t backward) {
-  if (job == nullptr || !zopt::lm::shape_ok(*job)) return 0;
+  if (job == nullptr || !zopt::lm::shape_ok(*job, backward != 0)) return 0;
   const size_t n = zopt::lm::plan(*job, backward != 0).total;
   return n < 16 ? 16 : n;
 }

@@ -34,6 +34,11 @@ constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxBytes + kS
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr int kMaxJobs = 3;
 constexpr float kLog2e = 1.4426950408889634f;
+// The longest inner length: an epilogue waits for a whole tile's products (those that are not cut) with a
+// limit (tc::kWaitLimitNs, 4 s), so they have to end well before it. These are 2^20 k-blocks: 0.43 s where
+// all pairs share one operand and read the other from HBM (cross entropy forward, 256 x 2^19 x 19456:
+// 0.41 us a k-block), twice that if they shared none.
+constexpr long long kMaxInner = 1LL << 26;
 
 // What an epilogue makes of its accumulators.
 enum Kind : int {
