@@ -33,3 +33,32 @@ def test_row_bytes_of_long_rows(tmp_path, size):
         want = (n - col) * size  # in Python's integers
         # a warp's part is 128 columns at most: how many of its bytes lie in the row
         assert min(max(int(g), 0), 128 * size) == min(max(want, 0), 128 * size), (n, col, g)
+
+
+def test_set_up_once_on_every_device(tmp_path):
+    """A kernel's shared-memory attribute is set on each device's first call, and again after a failure:
+    against a fake of the runtime's current device."""
+    got = run(tmp_path, r"""
+#include <cstdio>
+#include "per_device.h"
+static int device = 0, calls = 0;
+static cudaError_t answer = cudaSuccess, device_answer = cudaSuccess;
+extern "C" cudaError_t CUDARTAPI cudaGetDevice(int* d) { *d = device; return device_answer; }
+template <int kSite> static int call() { return zopt::once_per_device([] { ++calls; return answer; }); }
+#define SAY(site) do { const int e = call<site>(); std::printf("%d %d\n", e, calls); } while (0)
+int main() {
+  SAY(0);                                            // set up on device 0
+  SAY(0);                                            // done already
+  device = 1; SAY(0);                                // a second device
+  device = 0; SAY(0);
+  SAY(1);                                            // another kernel
+  device = 2; answer = cudaErrorInvalidValue; SAY(0);  // fails,
+  answer = cudaSuccess; SAY(0);                      // is tried again,
+  SAY(0);                                            // and then is done
+  device = 70; SAY(0); SAY(0);
+  device_answer = cudaErrorNoDevice; SAY(0);
+}
+""")
+    bad, none = 1, 100  # cudaErrorInvalidValue, cudaErrorNoDevice
+    assert [tuple(map(int, g.split())) for g in got] == [(0, 1), (0, 1), (0, 2), (0, 2), (0, 3), (bad, 4), (0, 5), (0, 5),
+                                                         (0, 6), (0, 7), (none, 7)]

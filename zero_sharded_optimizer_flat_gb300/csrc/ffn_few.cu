@@ -24,6 +24,7 @@
 #include "f2.cuh"
 #include "ffn_few.h"
 #include "launch.cuh"
+#include "per_device.h"
 #include "tc.cuh"
 
 namespace zopt {
@@ -266,7 +267,7 @@ template <int T>
 zopt_status run(const zopt_ffn_job& c, const Plan& p, float* gate_up, float* y, cudaStream_t s) {
   const int tokens = static_cast<int>(c.tokens);
   constexpr size_t smem = static_cast<size_t>(kWarps) * T * kCols * 4;
-  ZOPT_CUDA_TRY(once([] {
+  ZOPT_CUDA_TRY(once_per_device([] {
     cudaError_t e = cudaSuccess;
     for (const void* k : {reinterpret_cast<const void*>(gate_up_kernel<T>), reinterpret_cast<const void*>(down_kernel<T, ZOPT_ACT_SILU>),
                           reinterpret_cast<const void*>(down_kernel<T, ZOPT_ACT_GELU>)})

@@ -30,6 +30,7 @@
 #include "launch.cuh"
 #include "lm_gemm.cuh"
 #include "ns_internal.h"
+#include "per_device.h"
 #include "row_bytes.h"
 #include "tc.cuh"
 
@@ -1057,7 +1058,7 @@ __global__ void __launch_bounds__(256) stage_kernel(uint16_t* dst, long long dst
 template <int kKinds, int kAct = 0, int kKept = kKeepNone, bool kWide = true>
 zopt_status launch_kinds(Batch& b, dim3 grid, cudaStream_t s) {
   const auto kernel = lm_gemm_kernel<kKinds, kAct, kKept, kWide>;
-  ZOPT_CUDA_TRY(once([=] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes); }));
+  ZOPT_CUDA_TRY(once_per_device([=] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes); }));
   return launch_pdl(kernel, grid, dim3(kThreads), static_cast<size_t>(kSmemBytes), s, b);
 }
 template <int kAct>
