@@ -33,3 +33,14 @@ def test_block_of_few_tokens_keeps_nothing(zopt, t, act):
     zopt.ffn_forward(x, wgu, wd, y, zopt.new_ffn_workspace(x, wgu, wd, backward=False), act=act)
     torch.cuda.synchronize()
     assert torch.equal(y, kept)
+
+
+@pytest.mark.parametrize("t", [3, 4])
+def test_few_tokens_of_large_weights_run_as_more_do(zopt, t):
+    """Weights past the few-token path's size: a token's result is that of a larger batch, bit for bit."""
+    x, _, wgu, wd = ffn_case(9, 5, 1536, 4096)
+    y5, y = torch.empty_like(x), torch.empty_like(x[:t])
+    zopt.ffn_forward(x, wgu, wd, y5, zopt.new_ffn_workspace(x, wgu, wd, backward=False))
+    zopt.ffn_forward(x[:t], wgu, wd, y, zopt.new_ffn_workspace(x[:t], wgu, wd, backward=False))
+    torch.cuda.synchronize()
+    assert torch.equal(y, y5[:t])

@@ -294,11 +294,25 @@ zopt_status run(const zopt_ffn_job& c, const Plan& p, float* gate_up, float* y, 
                     static_cast<long long>(c.ld_y));
 }
 
+// With three and four tokens a CTA's sums take the registers of two, and this path's time grows faster
+// with the weights' bytes (0.36 us a MB) than the tensor cores' (0.09, and 2.4 us for every 1024 of dim,
+// which a tile walks alone, on 12 to start with); so it takes weights up to 16 MiB and 12 KiB for each of
+// dim. Four tokens, this path against the other: 1000 x 2732 13.5 us for 19.6, 1024 x 4096 14.4 for 17.1,
+// 1536 x 4096 20.5 for 19.5, 2048 x 5632 30.8 for 25.8, 4096 x 2048 22.2 for 26.3, 4096 x 4096 40.6 for 31.6,
+// 8192 x 2048 38.6 for 41.7, 8192 x 4096 72.6 for 50.6. Weights that the TMA cannot read in place are
+// read here once, there twice after a copy: 1999 x 4001 39.7 for 51.2, down alone copied 2047 x 5632 38.0
+// for 37.4. One and two tokens (2048 x 5632 20.1 and 24.2 for 25.7) lose at 3000 x 8000 alone, of those
+// measured (two tokens: 40.1 for 36.1).
+bool few_bytes(const zopt_ffn_job& c) {
+  const bool in_place = c.ld_gate_up % 8 == 0 && c.ld_down % 8 == 0 && c.hidden % 8 == 0;
+  return c.tokens <= 2 || !in_place || 6 * c.dim * c.hidden <= (16LL << 20) + (12LL << 10) * c.dim;
+}
+
 }  // namespace
 
 bool takes(const zopt_ffn_job& c) {
   const Plan p = plan(c);
-  return c.tokens <= kFewTokens && p.splits <= 65535 && p.blocks <= 65535;  // (a grid's second dimension)
+  return c.tokens <= kFewTokens && few_bytes(c) && p.splits <= 65535 && p.blocks <= 65535;  // (a grid's second dimension)
 }
 
 void partial_elems(const zopt_ffn_job& c, long long* gate_up, long long* y) {
