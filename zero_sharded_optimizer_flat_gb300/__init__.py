@@ -618,6 +618,7 @@ def _on_device(*tensors) -> None:
             raise ValueError("tensors must be on the GPU")
 
 
+I64 = 64  # not a zopt_dtype: no matrix may have it
 _CODES = {}
 
 
@@ -625,7 +626,7 @@ def _code(t) -> int:
     """_dtype_code from a table (filled on the first call)."""
     if not _CODES:
         import torch
-        _CODES.update({torch.float32: F32, torch.bfloat16: BF16})
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int64: I64})
     return _CODES.get(t.dtype, -1)
 
 
@@ -725,9 +726,8 @@ def ffn_backward(dy, x, kept, w_gate_up, w_down, dx, dw_gate_up, dw_down, ws, *,
 
 
 def _vector(t, n: int, code: int, name: str):
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or not t.is_cuda or \
-            (_code(t) != code if code >= 0 else t.element_size() != 8 or t.is_floating_point()):
-        raise ValueError(f"{name} must be a contiguous {'fp32' if code >= 0 else 'int64'} vector of {n} on the GPU")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1) or not t.is_cuda or _code(t) != code:
+        raise ValueError(f"{name} must be a contiguous {'fp32' if code == F32 else 'int64'} vector of {n} on the GPU")
     return t.data_ptr()
 
 
@@ -744,7 +744,7 @@ def _linear_ce_job(x, w, ignore_index=-100, target=None, loss=None, lse=None, dl
             if _code(t) != dtype:
                 dtype = -1
     return _LinearCeJob(tokens, dim, vocab, ignore_index, *_matrix(x, tokens, dim, "x"), *_matrix(w, vocab, dim, "w"),
-                        None if target is None else _vector(target, tokens, -1, "target"),
+                        None if target is None else _vector(target, tokens, I64, "target"),
                         None if loss is None else _vector(loss, tokens, F32, "loss"),
                         None if lse is None else _vector(lse, tokens, F32, "lse"),
                         None if dloss is None else _vector(dloss, tokens, F32, "dloss"), *more, dtype, 0)
