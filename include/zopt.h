@@ -528,16 +528,19 @@ ZOPT_API zopt_status zopt_act_unpack(const zopt_act8* in, uint16_t* out, int64_t
  *   dh = dy down';  dg = dh u a'(g);  du = dh a(g)
  *   dx = dg | du gate_up';  dgate_up = x' (dg | du);  ddown = h' dy.
  * Tensors are bf16, rows ld_* elements apart; products accumulate in fp32; h, dg and du are
- * rounded to bf16 once, as operands of the next product, and each result once. The forward keeps
+ * rounded to bf16 once, as operands of the next product (but for a few tokens' h, below), and each
+ * result once. The forward keeps
  * g | u in bf16 (kept, one rounding) or as an 8-bit checkpoint (kept8, parts = 2, rounded from
  * fp32), or nothing; the backward takes what was kept, and x in bf16 or as a checkpoint (x8). The
  * weight gradients have the weights' layout: zopt_grad_accumulate takes them as they are.
  *
  * Rows that the TMA cannot read in place (ld not a multiple of 8 elements; the forward's up columns
- * where F is not a multiple of 8) are copied into the workspace first. Up to four tokens a forward
- * runs on the CUDA cores instead, with the same roundings. Outputs must not overlap inputs or each
- * other. A result does not depend on the time or place of any
- * block's execution: a call repeated on the same inputs gives the same bits.
+ * where F is not a multiple of 8) are copied into the workspace first. A forward of one or two
+ * tokens, and of three or four where the weights are small or would have to be copied, runs on the
+ * CUDA cores instead, which read them in place and keep h in fp32: a token's y may differ there from
+ * its y in a larger batch by h's rounding. Outputs must not overlap inputs or each other. A result
+ * does not depend on the time or place of any block's execution: a call repeated on the same inputs
+ * gives the same bits.
  * ====================================================================================== */
 #define ZOPT_ACT_SILU 0
 #define ZOPT_ACT_GELU 1

@@ -2,7 +2,8 @@
 //
 // Forward, two products: gate and up in one kernel whose epilogue applies the activation and the
 // product (and keeps gate and up, in bf16 or in 8 bits), then y = h down. h takes one pass through
-// memory in bf16; the gate and up themselves only where they are kept.
+// memory in bf16; the gate and up themselves only where they are kept. (A few tokens take ffn_few.cu,
+// where h stays in fp32.)
 //
 // Backward, four products in two launches: dh = dy down', whose epilogue reads the kept gate and up
 // and writes dgate, dup and h; then dx, dgate_up and ddown in one launch, longest units first, so

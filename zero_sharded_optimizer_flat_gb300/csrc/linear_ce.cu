@@ -1,8 +1,8 @@
 // Linear cross entropy over a vocabulary, forward and backward, without keeping the logits.
 //
-// Forward: one product launch whose epilogue turns each row's 128 logits of a tile into a maximum
-// and a sum (base 2), and one launch that joins a row's pieces: 2 T V D flops, and 8 bytes a row and
-// 128 logits of partial results instead of the logits' 2 to 4 bytes each. One or two tokens take
+// Forward: one product launch whose epilogue turns 128 of a row's logits (64 in narrow tiles) into a
+// maximum and a sum (base 2), and one launch that joins a row's pieces: 2 T V D flops, and 8 bytes a row
+// and 128 (64) logits of partial results instead of the logits' 2 to 4 bytes each. One or two tokens take
 // linear_ce_few.cu in place of the first launch.
 //
 // Backward: dl needs each row's whole lse, so the logits are computed a second time: 6 T V D flops in
