@@ -2,7 +2,7 @@
  * zopt.h — C ABI of libzopt, the rank-local optimizer step of a ZeRO-sharded trainer on one
  * GB300 (sm_103a).
  *
- * Eight parts, each a few calls:
+ * Ten parts, each a few calls:
  *   1. the flat bucketed shard layout            (zopt_shard_layout and accessors, host only)
  *   2. the gradient norm / clip / found_inf stats (zopt_grad_norm_clip, zopt_clip_finalize,
  *      zopt_grad_accumulate / zopt_grad_accumulate2 for micro-step sums with the stats fused;
@@ -14,6 +14,8 @@
  *   6. 8-bit activation checkpoints               (zopt_act_pack, zopt_act_unpack)
  *   7. the gated feed-forward block, both ways    (zopt_ffn_forward, zopt_ffn_backward)
  *   8. linear cross entropy, both ways            (zopt_linear_ce_forward, zopt_linear_ce_backward)
+ *   9. routing tokens to experts, both ways       (zopt_route_forward, zopt_route_backward)
+ *  10. the experts' feed-forward block, both ways (zopt_experts_forward, zopt_experts_backward)
  *
  * Conventions shared by every call:
  *   - Pointers named d_* and every tensor argument are DEVICE pointers owned by the caller,
@@ -633,6 +635,131 @@ ZOPT_API zopt_status zopt_linear_ce_forward(const zopt_linear_ce_job* job, void*
                                             zopt_stream stream);
 ZOPT_API zopt_status zopt_linear_ce_backward(const zopt_linear_ce_job* job, void* d_ws, size_t ws_bytes,
                                              zopt_stream stream);
+
+/* ======================================================================================
+ * 9. Routing tokens to experts
+ *
+ * For T = tokens rows l of E = experts logits:
+ *   s = softmax(l), or the logistic function of each l;  c = s + bias (bias may be NULL: 0)
+ *   with groups > 1 the experts are cut into that many equal runs; a run's score is the sum of its
+ *   two largest c (of the one, where there is one), and only the top_groups best runs take part;
+ *   index = the top_k experts with the largest c, best first;
+ *   weight = s of those (without the bias), over their sum where renormalise, times scale.
+ * The order is that of the exact numbers (without a bias: of the logits), the lowest index (of
+ * experts, of runs) first among equal ones. An expert with a logit of -inf is never chosen; a slot
+ * that no expert is left for has index -1 and weight 0, and so has every slot of a row whose live
+ * byte is 0, whatever its logits hold. A NaN ranks above every number and makes its weight NaN (its
+ * row's, for softmax or where renormalised), and so does +inf for softmax, so that found_inf sees it.
+ * counts (may be NULL) = how many slots each expert got: what a bias for balance is corrected by.
+ *
+ * The backward gives dlogits from dweight, the gradient of each weight, and index and weight as the
+ * forward gave them (the choice itself, and so the bias, has no gradient). A slot with index -1 adds
+ * nothing; a row with an index that is neither -1 nor in [0, experts) becomes NaN. Logits and
+ * dlogits are fp32 or bf16, all else is fp32; sums are kept in fp32. A call repeated on the same
+ * inputs gives the same bits.
+ * ====================================================================================== */
+#define ZOPT_SCORE_SOFTMAX 0
+#define ZOPT_SCORE_SIGMOID 1
+
+typedef struct zopt_route_job {
+  int64_t tokens;
+  int32_t experts, top_k;
+  int32_t groups, top_groups; /* 1, 1: no groups */
+  int32_t score;              /* ZOPT_SCORE_SOFTMAX or ZOPT_SCORE_SIGMOID */
+  int32_t renormalise;        /* 0 or 1 */
+  float scale;
+  int32_t dtype; /* a zopt_dtype, of logits and dlogits */
+  const void* logits;
+  int64_t ld_logits;
+  const float* bias;    /* [experts] or NULL */
+  const uint8_t* live;  /* [tokens], 0: a padding token; or NULL */
+  int32_t* index;       /* [tokens][top_k] forward: written; backward: read */
+  float* weight;        /* [tokens][top_k] forward: written; backward: read */
+  int32_t* counts;      /* [experts] forward: written; or NULL */
+  const float* dweight; /* [tokens][top_k] backward, from here on */
+  void* dlogits;
+  int64_t ld_dlogits;
+  int32_t reserved[2]; /* 0 */
+} zopt_route_job; /* 128 bytes */
+
+/* Errors of both: EINVAL for NULL pointers or ones not aligned to their element, tokens < 0 or above
+ * 2^30, experts outside 1 .. 1024, groups outside 1 .. 32 or not dividing experts, top_groups outside
+ * 1 .. groups, top_k outside 1 .. 32 or above the experts of top_groups runs, another score, a scale
+ * that is not positive and finite, a row distance below experts or above 2^32; EUNSUPPORTED for
+ * another dtype. tokens = 0: the forward sets counts to zero, the backward does nothing. The
+ * backward looks at neither bias, live, groups (but for these checks) nor counts. */
+ZOPT_API zopt_status zopt_route_forward(const zopt_route_job* job, zopt_stream stream);
+ZOPT_API zopt_status zopt_route_backward(const zopt_route_job* job, zopt_stream stream);
+
+/* ======================================================================================
+ * 10. The experts' feed-forward block
+ *
+ * For T = tokens rows x of D = dim features, each with top_k slots (index, weight) as
+ * zopt_route_forward gives them, and the experts' matrices gate_up [E][D][2 F] (the gate's columns
+ * first) and down [E][F][D], each expert's as in part 7:
+ *   slot (t, j), e = index[t][j], w = weight[t][j]:  g | u = x_t gate_up_e;  h = w a(g) * u
+ *   y_t = sum over j of h down_e
+ * and, given dy, with g and u as they were kept:
+ *   dh = dy_t down_e';  dweight = <dh, a(g) * u>;  dg = w dh u a'(g);  du = w dh a(g)
+ *   dx_t = sum over j of (dg | du) gate_up_e'
+ *   dgate_up_e = sum over e's slots of x_t' (dg | du);  ddown_e = sum over e's slots of h' dy_t.
+ * A slot with index -1 takes no part: its weight is not looked at, its dweight is 0, its row of kept
+ * is neither written nor read; a token without experts has y = 0 and dx = 0, whatever its x and dy
+ * hold. An index that is neither -1 nor in [0, experts) makes its token's y and dx and its own
+ * dweight NaN. A token may name an expert twice. An expert without slots has zero gradients.
+ *
+ * Types and roundings are part 7's, with w part of h, dg and du before they are rounded; a slot's
+ * part of y and of dx is rounded to bf16 once, and the parts are added in fp32 in the order of the
+ * slots. kept and kept8 have a row for every slot, row t top_k + j. Experts' matrices lie stride_*
+ * elements apart (any distance that keeps them apart). Rows that the TMA cannot read in place (ld or
+ * stride not a multiple of 8 elements; the forward's up columns where F is not) are copied into the
+ * workspace first. Outputs must not overlap inputs or each other. Repeated on the same inputs a call
+ * gives the same bits.
+ * ====================================================================================== */
+typedef struct zopt_experts_job {
+  int64_t tokens, dim, hidden;
+  int32_t experts, top_k;
+  int32_t act;   /* ZOPT_ACT_SILU or ZOPT_ACT_GELU */
+  int32_t dtype; /* a zopt_dtype: ZOPT_BF16 */
+  const int32_t* index; /* [tokens][top_k] */
+  const float* weight;  /* [tokens][top_k] */
+  const uint16_t* w_gate_up;
+  int64_t ld_gate_up, stride_gate_up;
+  const uint16_t* w_down;
+  int64_t ld_down, stride_down;
+  const uint16_t* x; /* NULL in a backward call that is given x8 */
+  int64_t ld_x;
+  const zopt_act8* x8; /* backward: x as a checkpoint (tokens x dim, parts = 1), else NULL */
+  uint16_t* kept;      /* g | u, tokens top_k x 2 hidden (forward: written; backward: read), or NULL */
+  int64_t ld_kept;
+  const zopt_act8* kept8; /* g | u as a checkpoint (tokens top_k x 2 hidden, parts = 2), or NULL */
+  uint16_t* y;            /* forward */
+  int64_t ld_y;
+  const uint16_t* dy; /* backward, from here on */
+  int64_t ld_dy;
+  uint16_t* dx;
+  int64_t ld_dx;
+  float* dweight; /* [tokens][top_k] */
+  uint16_t* dw_gate_up;
+  int64_t ld_dw_gate_up, stride_dw_gate_up;
+  uint16_t* dw_down;
+  int64_t ld_dw_down, stride_dw_down;
+} zopt_experts_job; /* 256 bytes */
+
+/* Workspace bytes for a forward (backward = 0) or backward call, or either (backward = 1 covers
+ * both), of a job: from its tokens, dim, hidden, experts, top_k and the ld_* and stride_* of the
+ * direction's inputs; no pointer is looked at. 0 for a shape that the calls refuse. */
+ZOPT_API size_t zopt_experts_workspace(const zopt_experts_job* job, int32_t backward);
+/* Errors of both: EINVAL for NULL or misaligned pointers (matrices 16 bytes, vectors their element,
+ * scale bytes any), tokens < 0, dim, hidden, experts or top_k < 1, experts above 1024, top_k above 32,
+ * tokens top_k above 2^26, dim above 2^26, hidden above 2^25, a matrix (all experts' together) above 2^44 elements,
+ * a row distance below the row's length or above 2^32, a stride below a matrix's extent or above 2^38,
+ * another act, both or (backward) neither of x / x8 and of kept / kept8, a checkpoint of another
+ * shape, a short or misaligned workspace; EUNSUPPORTED for a dtype other than ZOPT_BF16; ETIMEOUT if
+ * a bounded wait of an earlier call's kernel gave up. tokens = 0: the forward does nothing, the
+ * backward sets the weight gradients to zero. */
+ZOPT_API zopt_status zopt_experts_forward(const zopt_experts_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream);
+ZOPT_API zopt_status zopt_experts_backward(const zopt_experts_job* job, void* d_ws, size_t ws_bytes, zopt_stream stream);
 
 #ifdef __cplusplus
 }

@@ -5,8 +5,8 @@ Argument marshalling only: every step of the path runs in the library's CUDA ker
 calls keep the C names: ``zopt_shard_layout`` (as :class:`ShardLayout`),
 ``zopt_grad_norm_clip``, ``zopt_adamw_step``, ``zopt_ns_orthogonalize``, and the training
 operators whose gradients the step takes: ``zopt_ffn_forward`` / ``_backward``,
-``zopt_linear_ce_forward`` / ``_backward``, ``zopt_act_pack`` / ``_unpack``. PyTorch provides
-device memory and streams. The library must be built (``build_lib.build()``); if it is
+``zopt_linear_ce_forward`` / ``_backward``, ``zopt_act_pack`` / ``_unpack``, ``zopt_route_forward`` /
+``_backward``, ``zopt_experts_forward`` / ``_backward``. PyTorch provides device memory and streams. The library must be built (``build_lib.build()``); if it is
 missing every call raises — there is no fallback.
 """
 from __future__ import annotations
@@ -77,6 +77,30 @@ class _LinearCeJob(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class _RouteJob(ctypes.Structure):
+    """``zopt_route_job``: routing tokens to experts, either direction."""
+    _fields_ = [("tokens", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("experts", "top_k", "groups", "top_groups", "score", "renormalise")] + [
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld_logits", ctypes.c_int64)] + [
+        (n, ctypes.c_void_p) for n in ("bias", "live", "index", "weight", "counts", "dweight", "dlogits")] + [
+        ("ld_dlogits", ctypes.c_int64), ("reserved", ctypes.c_int32 * 2)]
+
+
+class _ExpertsJob(ctypes.Structure):
+    """``zopt_experts_job``: the experts' feed-forward block, either direction."""
+    _fields_ = [("tokens", ctypes.c_int64), ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("experts", "top_k", "act", "dtype")] + [
+        ("index", ctypes.c_void_p), ("weight", ctypes.c_void_p)] + [
+        f for n in ("gate_up", "down") for f in
+        (("w_" + n, ctypes.c_void_p), ("ld_" + n, ctypes.c_int64), ("stride_" + n, ctypes.c_int64))] + [
+        ("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("x8", ctypes.POINTER(_Act8)), ("kept", ctypes.c_void_p),
+        ("ld_kept", ctypes.c_int64), ("kept8", ctypes.POINTER(_Act8))] + [
+        f for n in ("y", "dy", "dx") for f in ((n, ctypes.c_void_p), ("ld_" + n, ctypes.c_int64))] + [
+        ("dweight", ctypes.c_void_p)] + [
+        f for n in ("dw_gate_up", "dw_down") for f in
+        ((n, ctypes.c_void_p), ("ld_" + n, ctypes.c_int64), ("stride_" + n, ctypes.c_int64))]
+
+
 def lib() -> ctypes.CDLL:
     """The loaded library; raises if it has not been built."""
     global _lib
@@ -143,6 +167,11 @@ def lib() -> ctypes.CDLL:
         "zopt_linear_ce_workspace": (sz, [ctypes.POINTER(_LinearCeJob), i32]),
         "zopt_linear_ce_forward": (ctypes.c_int, [ctypes.POINTER(_LinearCeJob), vp, sz, vp]),
         "zopt_linear_ce_backward": (ctypes.c_int, [ctypes.POINTER(_LinearCeJob), vp, sz, vp]),
+        "zopt_route_forward": (ctypes.c_int, [ctypes.POINTER(_RouteJob), vp]),
+        "zopt_route_backward": (ctypes.c_int, [ctypes.POINTER(_RouteJob), vp]),
+        "zopt_experts_workspace": (sz, [ctypes.POINTER(_ExpertsJob), i32]),
+        "zopt_experts_forward": (ctypes.c_int, [ctypes.POINTER(_ExpertsJob), vp, sz, vp]),
+        "zopt_experts_backward": (ctypes.c_int, [ctypes.POINTER(_ExpertsJob), vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -775,6 +804,159 @@ def linear_ce_backward(x, w, target, lse, dloss, dx, dw, ws, *, ignore_index: in
     j = _linear_ce_job(x, w, ignore_index, target, None, lse, dloss, dx, dw)
     _on_device(ws)
     _check(lib().zopt_linear_ce_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+I32, U8 = 65, 66  # not zopt_dtypes either
+_ELEMENTS = {F32: "fp32", I32: "int32", U8: "bool or byte"}
+
+
+def _array(t, shape, code: int, name: str):
+    """The address of a contiguous array on the GPU."""
+    if I32 not in _CODES.values():
+        import torch
+        _code(t)
+        _CODES.update({torch.int32: I32, torch.uint8: U8, torch.bool: U8})
+    if t.shape != shape or not t.is_contiguous() or not t.is_cuda or _code(t) != code:
+        raise ValueError(f"{name} must be a contiguous {_ELEMENTS[code]} array of {' x '.join(map(str, shape))} on the GPU")
+    return t.data_ptr()
+
+
+def _one_device(*tensors) -> None:
+    """The calls launch on the current device: everything has to be there."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors must be on the current device, cuda:{here}")
+
+
+def _route_job(logits, index, weight, counts, bias, live, score, groups, top_groups, renormalise, scale, dweight=None,
+               dlogits=None) -> _RouteJob:
+    tokens, experts = logits.shape
+    top_k = index.shape[-1]
+    dtype = _code(logits)
+    slots = (tokens, top_k)
+    j = _RouteJob(tokens, experts, top_k, int(groups), int(top_groups),
+                  _SCORES.get(score, score if isinstance(score, int) else -1), int(bool(renormalise)), float(scale),
+                  dtype if dtype in (F32, BF16) else -1, *_matrix(logits, tokens, experts, "logits"))
+    j.index = _array(index, slots, I32, "index")
+    j.weight = _array(weight, slots, F32, "weight")
+    if counts is not None:
+        j.counts = _array(counts, (experts,), I32, "counts")
+    if bias is not None:
+        j.bias = _array(bias, (experts,), F32, "bias")
+    if live is not None:
+        j.live = _array(live, (tokens,), U8, "live")
+    if dlogits is not None:
+        j.dweight = _array(dweight, slots, F32, "dweight")
+        j.dlogits, j.ld_dlogits = _matrix(dlogits, tokens, experts, "dlogits")
+        if _code(dlogits) != dtype:
+            j.dtype = -1
+    _one_device(logits, index, weight, counts, bias, live, dweight, dlogits)
+    return j
+
+
+def route_forward(logits, index, weight, counts=None, *, bias=None, live=None, score: str = "softmax", groups: int = 1,
+                  top_groups: int = 1, renormalise: bool = True, scale: float = 1.0, stream=None) -> None:
+    """``zopt_route_forward``: index (int32) and weight (fp32), [tokens, top_k], of the experts that each
+    row of logits (fp32 or bf16) chooses, and counts (int32), how many slots each expert got. ``live``
+    (bool, [tokens]) is false for padding tokens, ``bias`` (fp32, [experts]) is added for the choice alone."""
+    j = _route_job(logits, index, weight, counts, bias, live, score, groups, top_groups, renormalise, scale)
+    _check(lib().zopt_route_forward(j, _stream(stream)))
+
+
+def route_backward(logits, index, weight, dweight, dlogits, *, score: str = "softmax", renormalise: bool = True,
+                   scale: float = 1.0, stream=None) -> None:
+    """``zopt_route_backward``: dlogits from dweight (fp32), the gradient of each weight, and what the
+    forward gave."""
+    j = _route_job(logits, index, weight, None, None, None, score, 1, 1, renormalise, scale, dweight, dlogits)
+    _check(lib().zopt_route_backward(j, _stream(stream)))
+
+
+def _stack(t, n: int, rows: int, cols: int, name: str):
+    """(address, row distance, stride) of n rows x cols matrices with contiguous rows."""
+    if t.shape != (n, rows, cols) or not t.is_cuda:
+        raise ValueError(f"{name} must be {n} matrices of {rows} x {cols} on the GPU")
+    stride, ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    ld = ld if rows > 1 else cols
+    return t.data_ptr(), ld, stride if n > 1 else rows * ld
+
+
+def _experts_job(x, index, weight, w_gate_up, w_down, act, kept=None, y=None, dy=None, dx=None, dweight=None,
+                 dw_gate_up=None, dw_down=None) -> _ExpertsJob:
+    experts, hidden, dim = w_down.shape
+    top_k = index.shape[-1]
+    wgu = _stack(w_gate_up, experts, dim, 2 * hidden, "w_gate_up")
+    wd = _stack(w_down, experts, hidden, dim, "w_down")
+    dtype = _same_dtype(w_gate_up, w_down)
+    if isinstance(x, Act8):
+        rows, xp, x8 = x.rows, (None, 0), ctypes.pointer(x._c)
+    else:
+        rows, x8 = x.shape[0], None
+        xp = _matrix(x, rows, dim, "x")
+        if _code(x) != dtype:
+            dtype = -1
+    slots = (rows, top_k)
+    j = _ExpertsJob(rows, dim, hidden, experts, top_k, _ACTS.get(act, act if isinstance(act, int) else -1), dtype,
+                    _array(index, slots, I32, "index"), None if weight is None else _array(weight, slots, F32, "weight"),
+                    *wgu, *wd, *xp, x8)
+    if isinstance(kept, Act8):
+        j.kept8 = ctypes.pointer(kept._c)
+    elif kept is not None:
+        if _code(kept) != BF16:
+            raise ValueError("kept must be bf16 or an Act8")
+        j.kept, j.ld_kept = _matrix(kept, rows * top_k, 2 * hidden, "kept")
+    for t, name in ((y, "y"), (dy, "dy"), (dx, "dx")):
+        if t is not None:
+            p, ld = _matrix(t, rows, dim, name)
+            setattr(j, name, p)
+            setattr(j, "ld_" + name, ld)
+            if _code(t) != dtype:
+                j.dtype = -1
+    if dweight is not None:
+        j.dweight = _array(dweight, slots, F32, "dweight")
+    if dw_gate_up is not None:
+        j.dw_gate_up, j.ld_dw_gate_up, j.stride_dw_gate_up = _stack(dw_gate_up, experts, dim, 2 * hidden, "dw_gate_up")
+        j.dw_down, j.ld_dw_down, j.stride_dw_down = _stack(dw_down, experts, hidden, dim, "dw_down")
+        if _same_dtype(dw_gate_up, dw_down) != dtype:
+            j.dtype = -1
+    _one_device(x.q if x8 is not None else x, index, weight, w_gate_up, w_down, kept.q if isinstance(kept, Act8) else kept, y, dy, dx,
+                dweight, dw_gate_up, dw_down)
+    return j
+
+
+def experts_workspace(x, index, w_gate_up, w_down, backward: bool = True) -> int:
+    """``zopt_experts_workspace`` for these operands (x a bf16 matrix or an :class:`Act8`)."""
+    return int(lib().zopt_experts_workspace(_experts_job(x, index, None, w_gate_up, w_down, "silu"), int(bool(backward))))
+
+
+def new_experts_workspace(x, index, w_gate_up, w_down, backward: bool = True, device="cuda"):
+    """A workspace for :func:`experts_forward` and (``backward``) :func:`experts_backward`."""
+    import torch
+    return torch.empty(max(experts_workspace(x, index, w_gate_up, w_down, backward), 16), dtype=torch.uint8, device=device)
+
+
+def experts_forward(x, index, weight, w_gate_up, w_down, y, ws, *, kept=None, act: str = "silu", stream=None) -> None:
+    """``zopt_experts_forward``: y = the sum over a token's slots of weight (a(x Wgate) * (x Wup)) Wdown with
+    the matrices of expert index, [experts, dim, 2 hidden] and [experts, hidden, dim]. ``kept`` takes gate and
+    up for the backward: a bf16 matrix [tokens top_k, 2 hidden], an :class:`Act8` of that shape in two parts, or
+    None."""
+    j = _experts_job(x, index, weight, w_gate_up, w_down, act, kept, y)
+    _one_device(ws)
+    _check(lib().zopt_experts_forward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+def experts_backward(dy, x, index, weight, kept, w_gate_up, w_down, dx, dweight, dw_gate_up, dw_down, ws, *,
+                     act: str = "silu", stream=None) -> None:
+    """``zopt_experts_backward`` from dy, x (bf16 or :class:`Act8`) and what the forward kept; dweight (fp32)
+    is what :func:`route_backward` takes."""
+    j = _experts_job(x, index, weight, w_gate_up, w_down, act, kept, None, dy, dx, dweight, dw_gate_up, dw_down)
+    _one_device(ws)
+    _check(lib().zopt_experts_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
 
 
 def take_device_error() -> int:

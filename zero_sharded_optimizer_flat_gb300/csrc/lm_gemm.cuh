@@ -91,6 +91,22 @@ struct Job {
   long long ld_kept;
   uint8_t* kept_scale;  // kKeep8: row r's block exponents at r * 2 blocks, the gate's first
   int hidden;           // the gate's width, N
+  // grouped batches
+  int by_inner;          // the experts' rows are the inner length (else the rows of D)
+  long long out_stride;  // by_inner: elements between the experts' D
+  float* dots;           // kGluBwd: the parts of dh . h, at [2 tile column + half][row]
+  long long dots_ld;
+};
+
+// The rows of a grouped batch's operands: each expert's one after another, filled up with rows of zeros to
+// a multiple of 64 (a k-block, and the 32 rows of an epilogue's warp, are then one expert's). What is
+// not known before the tokens have chosen is read from device memory.
+struct Groups {
+  const int* head;    // [0] row tiles, [1] rows
+  const int4* tiles;  // a row tile's expert, first row, and where its expert's rows (with the zeros) end
+  const int2* info;   // an expert's first row and its number of rows (without the zeros)
+  const int2* row;    // a row's slot (-1: zeros) and its weight's bits
+  int experts;
 };
 
 // Units of work are numbered job by job, a job's runs of k one after another. Pair p takes units p,
@@ -106,6 +122,7 @@ struct Batch {
   Job job[kMaxJobs];
   uint16_t first[kPairs + 1];
   uint16_t order[kMaxListed];
+  Groups groups;
 };
 
 // ------------------------------------------------------------------ host side
