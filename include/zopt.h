@@ -709,8 +709,8 @@ ZOPT_API zopt_status zopt_route_backward(const zopt_route_job* job, zopt_stream 
  * dweight NaN. A token may name an expert twice. An expert without slots has zero gradients.
  *
  * Types and roundings are part 7's, with w part of h, dg and du before they are rounded; a slot's
- * part of y and of dx is rounded to bf16 once, and the parts are added in fp32 in the order of the
- * slots. kept and kept8 have a row for every slot, row t top_k + j. Experts' matrices lie stride_*
+ * part of y and of dx is kept in 12 significant bits (an fp16 times a power of two that 64 columns
+ * share), and the parts are added in fp32 in the order of the slots. kept and kept8 have a row for every slot, row t top_k + j. Experts' matrices lie stride_*
  * elements apart (any distance that keeps them apart). Rows that the TMA cannot read in place (ld or
  * stride not a multiple of 8 elements; the forward's up columns where F is not) are copied into the
  * workspace first. Outputs must not overlap inputs or each other. Repeated on the same inputs a call

@@ -9,6 +9,7 @@
 //              dup, h and the parts of dweight; dx's parts, dgate_up and ddown in one launch; every
 //              token's parts added up.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -204,16 +205,17 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
 }
 
 struct CombineArgs {
-  const uint16_t* parts;  // rows of `pitch` elements
+  const uint16_t* parts;  // rows of `pitch` elements, fp16 in units of `scale`, at [64 columns][row]
   long long pitch;
+  const float* scale;
+  long long rows_ld;
   const int* row_of;
   uint16_t* out;
   long long ld;
   long long tokens, cols;
   int top_k, chunks;  // chunks: of 256 columns
-  // the weights' gradient (backward): dots parts of each row's, ld_dots apart
+  // the weights' gradient (backward): n_dots parts of each row's, rows_ld apart
   const float* dots;
-  long long ld_dots;
   int n_dots;
   float* dweight;
 };
@@ -236,11 +238,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
       const int r = __shfl_sync(0xFFFFFFFFu, mine, j);
       if (r >= 0 && col < a.cols) {
         const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.parts + r * a.pitch + col));
+        const float unit = __ldcg(a.scale + (col >> 6) * a.rows_ld + r);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          acc[2 * k] += __uint_as_float(w[k] << 16);
-          acc[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          acc[2 * k] = fmaf(x.x, unit, acc[2 * k]);
+          acc[2 * k + 1] = fmaf(x.y, unit, acc[2 * k + 1]);
         }
       }
     }
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
       float s = mine == -2 ? __uint_as_float(0x7FC00000u) : 0.0f;
       if (mine >= 0) {
 #pragma unroll 8
-        for (int p = 0; p < a.n_dots; ++p) s += __ldcg(a.dots + p * a.ld_dots + mine);
+        for (int p = 0; p < a.n_dots; ++p) s += __ldcg(a.dots + p * a.rows_ld + mine);
       }
       a.dweight[t * a.top_k + lane] = s;
     }
@@ -305,7 +309,7 @@ struct Layout {
   long long dp, fp, gp;  // dim, hidden and 2 hidden rounded up to 8
   long long slots, rows, tiles;
   bool stage_gate, stage_up, stage_down;
-  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, dots, total;
+  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, total;
   int dot_parts;
 };
 
@@ -363,6 +367,7 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   if (p.stage_down) p.down = take(at, E * F * p.dp * 2);
   p.xs = take(at, p.rows * p.dp * 2);
   p.h = take(at, p.rows * p.fp * 2);
+  p.scales = take(at, p.rows * ((D + 63) / 64) * 4);
   p.total = at;
   if (p.stage_up) p.up = take(p.total, E * D * p.fp * 2);
   p.parts = p.xs;  // the forward's y parts, when x has been read
@@ -501,17 +506,24 @@ struct Call {
   zopt_status combine(bool backward) const {
     CombineArgs a{};
     a.parts = at<uint16_t>(p.parts), a.pitch = p.dp;
+    a.scale = at<float>(p.scales), a.rows_ld = p.rows;
     a.row_of = at<int>(p.row_of);
     a.out = backward ? c.dx : c.y, a.ld = backward ? c.ld_dx : c.ld_y;
     a.tokens = c.tokens, a.cols = c.dim;
     a.top_k = c.top_k, a.chunks = static_cast<int>((c.dim + 255) / 256);
-    if (backward) a.dots = at<float>(p.dots), a.ld_dots = p.rows, a.n_dots = p.dot_parts, a.dweight = c.dweight;
+    if (backward) a.dots = at<float>(p.dots), a.n_dots = p.dot_parts, a.dweight = c.dweight;
     return launch_pdl(combine_kernel, dim3(blocks_for(32 * a.tokens * a.chunks, sms)), dim3(256), 0, s, a);
   }
   void begin(Batch& b, int n) const {
     b.err = err;
     b.n = n;
     b.groups = Groups{at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), c.experts};
+  }
+  void parts(Job& j) const {
+    j.out = at<uint16_t>(p.parts);
+    j.ld_out = p.dp;
+    j.part_scale = at<float>(p.scales);
+    j.rows_ld = p.rows;
   }
   void glu(Job& j) const {
     j.act = c.act;
@@ -555,8 +567,7 @@ struct Call {
     j.b_mn = 1;
     TRY(map_rows(fn, j, &j.P, at<uint16_t>(p.h), p.rows, F, p.fp, 0, 128));
     TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 1, 0));
-    j.out = at<uint16_t>(p.parts);
-    j.ld_out = p.dp;
+    parts(j);
     TRY(launch_grouped(fn, b, kStore, p.tiles, s));
     return combine(false);
   }
@@ -579,7 +590,7 @@ struct Call {
       TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 0, j.tile_n / 2));
       j.out = dgu, j.ld_out = p.gp;
       j.out_h = h, j.ld_h = p.fp;
-      j.dots = at<float>(p.dots), j.dots_ld = p.rows;
+      j.dots = at<float>(p.dots), j.rows_ld = p.rows;
       TRY(launch_grouped(fn, b, kGluBwd, p.tiles, s));
     }
     Batch b{};
@@ -589,7 +600,7 @@ struct Call {
       group_job(j, p, kStore, false, 0, D, 2 * F, c.experts);
       TRY(map_rows(fn, j, &j.P, dgu, p.rows, 2 * F, p.gp, 0, 128));
       TRY(map_weights(fn, j, &j.Q, w.gate, D, 2 * F, w.pg, c.experts, w.sg, 0, j.tile_n / 2));
-      j.out = at<uint16_t>(p.parts), j.ld_out = p.dp;
+      parts(j);
     }
     {
       Job& j = b.job[1];  // dgate_up

@@ -94,8 +94,9 @@ struct Job {
   // grouped batches
   int by_inner;          // the experts' rows are the inner length (else the rows of D)
   long long out_stride;  // by_inner: elements between the experts' D
+  float* part_scale;     // kStore by rows: D is fp16 in units of powers of two, at [64 columns][row]
   float* dots;           // kGluBwd: the parts of dh . h, at [2 tile column + half][row]
-  long long dots_ld;
+  long long rows_ld;     // what these two's rows of rows are apart
 };
 
 // The rows of a grouped batch's operands: each expert's one after another, filled up with rows of zeros to

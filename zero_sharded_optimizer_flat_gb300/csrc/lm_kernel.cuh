@@ -470,6 +470,26 @@ struct Acc {
 };
 __device__ __forceinline__ float f(uint32_t x) { return __uint_as_float(x); }
 
+// The parts of a token's sum are not rounded to bf16, which would add as much error as the sum's own
+// rounding: 64 columns of a row share a power of two that brings the largest finite magnitude to
+// 2^14 .. 2^15, and an entry is fp16 in that unit, three bits more in the same two bytes (2^-12 of an entry
+// down to 2^-29 of the largest, a fixed step below). Returns the unit.
+__device__ __forceinline__ float half_words(const uint32_t (&v)[2][32], uint32_t (&words)[32]) {
+  float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < 64; ++k) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
+  const uint32_t e = __float_as_uint(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) >> 23;
+  const uint32_t up = min(127u + 127u + 14u - max(e, 1u), 253u);  // 2^(14 - exponent), at most 2^126
+  const F2 scale = f2(__uint_as_float(up << 23), __uint_as_float(up << 23));
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float2 x = f2(f2(f(v[k >> 4][2 * (k & 15)]), f(v[k >> 4][2 * (k & 15) + 1])) * scale);
+    const __half2 h = __floats2half2_rn(x.x, x.y);
+    words[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return __uint_as_float((254u - up) << 23);
+}
+
 template <bool kGrouped>
 __device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
                                           uint32_t box) {
@@ -512,7 +532,14 @@ __device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Acc
 #pragma unroll
       for (int k = 0; k < 64; ++k) v[k >> 5][k & 31] = __float_as_uint(f(v[k >> 5][k & 31]) * alpha);
     }
-    if (wide) {
+    if (kGrouped && j.part_scale != nullptr) {
+      uint32_t words[32];
+      j.part_scale[static_cast<long long>(col0 >> 6) * j.rows_ld + row] = half_words(v, words);
+      box_put(box, lane, 0, words);
+      __syncwarp();
+      out.template put<0>(box, lane, 128 * half);
+      __syncwarp();
+    } else if (wide) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         box_put(box, lane, 0, v[c]);
@@ -954,7 +981,7 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const A
   if constexpr (kGrouped) {
     if (mine.slot >= 0) {
       const float2 two = f2(dot);
-      j.dots[(2 * w.tj + h) * j.dots_ld + row0 + lane] = two.x + two.y;
+      j.dots[(2 * w.tj + h) * j.rows_ld + row0 + lane] = two.x + two.y;
     }
   }
 }

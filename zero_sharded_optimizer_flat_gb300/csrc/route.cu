@@ -1,14 +1,17 @@
 // Routing tokens to experts, forward and backward.
 //
-// A warp takes a token's row: lane l holds experts l, l + 32, ... in registers. Ranking is in exact
-// order (of the score plus the bias as real numbers, the lowest index first among equal ones), so that
-// a choice never depends on how an exponential rounds. Without a bias that is the logits' own order.
-// With one, or with groups, scores are formed in fp32 and every comparison that decides something is
-// held against their error; a row that has a closer one is ranked again in fp64 (one row in some
-// thousands).
+// A warp takes a token's row, a lane V experts that follow one another. Ranking is in exact order (of the
+// score plus the bias as real numbers, the lowest index first among equal ones), so that a choice never
+// depends on how an exponential rounds. An expert is one word: 22 bits that do not decrease with its
+// rank's number, above 10 that fall with its index. A lane sorts its words once (a fixed network); the
+// warp's largest word, an integer maximum, is the next choice, and its lane moves its words up. Without a
+// bias the 22 bits are the logit's own leading ones (a bf16 logit's are all of it), with one, or with
+// groups, the score's and the bias's sum in fixed point over the row's range. Neighbours in the
+// order that come closer than those bits and the score's error tell apart, if they are not the same
+// numbers, are told apart in fp64, together with what the border of the choice may have left out (one
+// row in some hundreds).
 //
-// The largest of a row is found by an integer maximum over the warp of an order-preserving key, its
-// index by a minimum, top_k times.
+// Bound by the instructions of a row, some 200 for eight of 256 experts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -43,12 +46,96 @@ struct Args {
   int experts, top_k, groups, top_groups;
   Divisor per_group;
   int bf16, renormalise, alone;  // alone: one block has all rows, counts need no sum over blocks
+  int vec, vec_d;                // a lane's experts can be loaded (stored) at once
+  int lanes_per_group;           // where a group is a power of two of whole lanes' experts, else 0
   float scale;
 };
 
 __device__ __forceinline__ float load(const Args& a, long long row, int i) {
   const long long at = row * a.ld + i;
   return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
+}
+// The lane's V logits, -inf behind the last expert.
+template <int V>
+__device__ __forceinline__ void load_row(const Args& a, long long row, int first, float (&l)[V]) {
+  if (V >= 2 && a.vec && first + V <= a.experts) {
+    if (a.bf16) {
+      const uint16_t* const p = static_cast<const uint16_t*>(a.logits) + row * a.ld + first;
+      if constexpr (V >= 8) {
+#pragma unroll
+        for (int q = 0; q < V / 8; ++q) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + q);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l[8 * q + 2 * k] = __uint_as_float(w[k] << 16), l[8 * q + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+      } else if constexpr (V == 4) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        l[0] = __uint_as_float(x.x << 16), l[1] = __uint_as_float(x.x & 0xFFFF0000u);
+        l[2] = __uint_as_float(x.y << 16), l[3] = __uint_as_float(x.y & 0xFFFF0000u);
+      } else if constexpr (V == 2) {
+        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(p));
+        l[0] = __uint_as_float(x << 16), l[1] = __uint_as_float(x & 0xFFFF0000u);
+      }
+    } else {
+      const float* const p = static_cast<const float*>(a.logits) + row * a.ld + first;
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(p) + q);
+          l[4 * q] = x.x, l[4 * q + 1] = x.y, l[4 * q + 2] = x.z, l[4 * q + 3] = x.w;
+        }
+      } else if constexpr (V == 2) {
+        const float2 x = __ldg(reinterpret_cast<const float2*>(p));
+        l[0] = x.x, l[1] = x.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = first + v < a.experts ? load(a, row, first + v) : -INFINITY;
+}
+
+template <int V>
+__device__ __forceinline__ void store_row(const Args& a, long long row, int first, const float (&x)[V]) {
+  const long long at = row * a.ld_d + first;
+  if (V >= 2 && a.vec_d && first + V <= a.experts) {
+    if (a.bf16) {
+      uint16_t* const p = static_cast<uint16_t*>(a.dlogits) + at;
+      uint32_t w[V / 2 > 0 ? V / 2 : 1];
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      if constexpr (V >= 8) {
+#pragma unroll
+        for (int q = 0; q < V / 8; ++q) reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      } else if constexpr (V == 2) {
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+      }
+    } else {
+      float* const p = static_cast<float*>(a.dlogits) + at;
+      if constexpr (V >= 4) {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) reinterpret_cast<float4*>(p)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+      } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (first + v >= a.experts) continue;
+    if (a.bf16) {
+      static_cast<__nv_bfloat16*>(a.dlogits)[at + v] = __float2bfloat16_rn(x[v]);
+    } else {
+      static_cast<float*>(a.dlogits)[at + v] = x[v];
+    }
+  }
 }
 
 // Unsigned integers in the order of the numbers, NaN above them all; 0, below them all, is no number's.
@@ -68,16 +155,14 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 __device__ __forceinline__ double of_key(uint64_t k) {
   return __longlong_as_double(static_cast<long long>(k ^ (static_cast<uint64_t>(static_cast<int64_t>(~k) >> 63) | 0x8000000000000000ull)));
 }
-__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kAll, k); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
   const uint32_t hi = static_cast<uint32_t>(k >> 32), top = __reduce_max_sync(kAll, hi);
   const uint32_t lo = __reduce_max_sync(kAll, hi == top ? static_cast<uint32_t>(k) : 0u);
   return (static_cast<uint64_t>(top) << 32) | lo;
 }
+// (NaN: the others' largest)
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
-  return x;
+  return of_key(__reduce_max_sync(kAll, x != x ? 0x007FFFFFu : key_of(x)));  // 0x007FFFFF: -inf's
 }
 template <typename T>
 __device__ __forceinline__ T warp_sum(T x) {
@@ -86,179 +171,275 @@ __device__ __forceinline__ T warp_sum(T x) {
   return x;
 }
 
-// The first register (lowest index) that holds the lane's largest key.
-template <int V, typename K>
-__device__ __forceinline__ K lane_max(const K (&key)[V], int& at) {
-  K best = key[0];
-  at = 0;
-#pragma unroll
-  for (int v = 1; v < V; ++v)
-    if (key[v] > best) best = key[v], at = v;
-  return best;
+// ---------------------------------------------------------------------- in fp64
+
+// What an expert is ranked by: the score and the bias, or without a bias the logit.
+template <bool kSoftmax>
+__device__ __forceinline__ double rank64(const Args& a, float l, int i, double top, double z) {
+  if (a.bias == nullptr) return static_cast<double>(l);
+  const double s = kSoftmax ? exp(static_cast<double>(l) - top) / z : 1.0 / (1.0 + exp(-static_cast<double>(l)));
+  return s + static_cast<double>(a.bias[i]);
 }
-template <int V, typename K>
-__device__ __forceinline__ void clear(K (&key)[V], int v) {
-#pragma unroll
-  for (int q = 0; q < V; ++q)
-    if (q == v) key[q] = 0;
+__device__ __forceinline__ void softmax64(const Args& a, long long row, int lane, double& top, double& z) {
+  float m = -INFINITY;
+  for (int i = lane; i < a.experts; i += 32) m = fmaxf(m, load(a, row, i));
+  top = static_cast<double>(warp_max(m));
+  double part = 0.0;
+  for (int i = lane; i < a.experts; i += 32) part += exp(static_cast<double>(load(a, row, i)) - top);
+  z = warp_sum(part);
 }
 
-// The `most` best, one after another: lane j gets the j-th one's index (-1: there is none), and the
-// keys of those taken become 0.
-template <int V, typename K>
-__device__ __forceinline__ int take_best(K (&key)[V], int most, int lane) {
+// The best `most` of the candidates, one a lane (key 0: none), the lowest index first among equal ones.
+__device__ __forceinline__ int best64(uint64_t key, int i, int most, int lane) {
   int mine = -1;
   for (int j = 0; j < most; ++j) {
-    int at;
-    const K best = lane_max<V>(key, at);
-    const K top = warp_max(best);
+    const uint64_t top = warp_max(key);
     if (top == 0) break;
-    const uint32_t i = __reduce_min_sync(kAll, best == top ? static_cast<uint32_t>(lane + 32 * at) : kAll);
-    if (lane == j) mine = static_cast<int>(i);
-    if ((i & 31u) == static_cast<uint32_t>(lane)) clear<V>(key, static_cast<int>(i >> 5));
+    const int at = static_cast<int>(__reduce_min_sync(kAll, key == top ? static_cast<uint32_t>(i) : kAll));
+    if (lane == j) mine = at;
+    if (key == top && i == at) key = 0;
   }
   return mine;
 }
 
-// Lane g's key of the sum of group g's two largest (the largest alone where there is one; 0: none).
-template <int V, typename K>
-__device__ __forceinline__ K group_keys(const K (&key)[V], const Args& a, int lane) {
-  K mine = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    K in[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) in[v] = static_cast<int>(a.per_group(static_cast<uint32_t>(lane + 32 * v))) == g ? key[v] : 0;
-    int at;
-    K best = lane_max<V>(in, at);
-    const K first = warp_max(best);
-    const uint32_t i = __reduce_min_sync(kAll, best == first ? static_cast<uint32_t>(lane + 32 * at) : kAll);
-    if ((i & 31u) == static_cast<uint32_t>(lane)) clear<V>(in, static_cast<int>(i >> 5));
-    best = lane_max<V>(in, at);
-    const K second = warp_max(best);
-    if (lane == g) mine = first == 0 ? 0 : second == 0 ? first : key_of(of_key(first) + of_key(second));
-  }
-  return mine;
+// The row's choice among `i` of every lane (-1: none).
+template <bool kSoftmax>
+__device__ __noinline__ int among(const Args& a, long long row, int i, int lane) {
+  double top = 0.0, z = 1.0;
+  if (kSoftmax && a.bias != nullptr) softmax64(a, row, lane, top, z);
+  return best64(i >= 0 ? key_of(rank64<kSoftmax>(a, load(a, row, i), i, top, z)) : 0ull, i, a.top_k, lane);
 }
 
-// The mask of the groups that take part, from lane g's key of group g.
-template <typename K>
-__device__ __forceinline__ uint32_t best_groups(K key, const Args& a, int lane) {
-  K k[1] = {key};
-  const int g = take_best<1>(k, a.top_groups, lane);
-  return __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
-}
-
-template <int V, typename K>
-__device__ __forceinline__ void drop_groups(K (&key)[V], uint32_t mask, const Args& a, int lane) {
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (lane + 32 * v < a.experts && ((mask >> a.per_group(static_cast<uint32_t>(lane + 32 * v))) & 1u) == 0) key[v] = 0;
-}
-
-// A row's choice with everything in fp64.
-template <int V, bool kSoftmax>
-__device__ __noinline__ int choose64(const Args& a, long long row, int lane) {
-  uint64_t key[V];
-  double top = 0.0, rz = 1.0;
-  if (kSoftmax) {
-    float m = -INFINITY;
-    for (int i = lane; i < a.experts; i += 32) m = fmaxf(m, load(a, row, i));
-    top = static_cast<double>(warp_max(m));
-    double z = 0.0;
-    for (int i = lane; i < a.experts; i += 32) z += exp(static_cast<double>(load(a, row, i)) - top);
-    rz = warp_sum(z);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int i = lane + 32 * v;
-    key[v] = 0;
-    if (i >= a.experts) continue;
-    const double l = static_cast<double>(load(a, row, i));
-    const double s = kSoftmax ? exp(l - top) / rz : 1.0 / (1.0 + exp(-l));
-    if (l != -INFINITY) key[v] = key_of(a.bias != nullptr ? s + static_cast<double>(a.bias[i]) : s);
-  }
+// The row's choice among all experts, its groups' scores in fp64 as well. Experts a lane at a time: lane l
+// looks at l, l + 32, ...; those taken are marked in `gone`.
+template <bool kSoftmax>
+__device__ __noinline__ int among_all(const Args& a, long long row, int lane) {
+  double top = 0.0, z = 1.0;
+  if (kSoftmax) softmax64(a, row, lane, top, z);
+  uint32_t gone = 0, groups = kAll;
   if (a.groups > 1) {
-    drop_groups<V>(key, best_groups(group_keys<V>(key, a, lane), a, lane), a, lane);
-    if (a.bias == nullptr) {  // within the groups the logits' own order, as everywhere without a bias
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (key[v] != 0) key[v] = key_of(static_cast<double>(load(a, row, lane + 32 * v)));
+    uint64_t mine = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      uint64_t first = 0, second = 0;
+      for (int i = g * static_cast<int>(a.per_group.d) + lane; i < (g + 1) * static_cast<int>(a.per_group.d); i += 32) {
+        const float l = load(a, row, i);
+        if (l == -INFINITY) continue;
+        double c = kSoftmax ? exp(static_cast<double>(l) - top) / z : 1.0 / (1.0 + exp(-static_cast<double>(l)));
+        if (a.bias != nullptr) c += static_cast<double>(a.bias[i]);
+        const uint64_t k = key_of(c);
+        second = k > first ? first : k > second ? k : second;
+        first = k > first ? k : first;
+      }
+      const uint64_t one = warp_max(first);
+      const int owner = __ffs(__ballot_sync(kAll, first == one)) - 1;
+      const uint64_t two = warp_max(lane == owner ? second : first);
+      if (lane == g) mine = one == 0 ? 0 : two == 0 ? one : key_of(of_key(one) + of_key(two));
     }
+    const int g = best64(mine, lane, a.top_groups, lane);
+    groups = __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
   }
-  return take_best<V>(key, a.top_k, lane);
+  int mine = -1;
+  for (int j = 0; j < a.top_k; ++j) {
+    uint64_t best = 0;
+    int at = -1;
+    for (int i = lane, v = 0; i < a.experts; i += 32, ++v) {
+      const float l = load(a, row, i);
+      if (l == -INFINITY || ((gone >> v) & 1u) != 0) continue;
+      if (a.groups > 1 && ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) == 0) continue;
+      const uint64_t k = key_of(rank64<kSoftmax>(a, l, i, top, z));
+      if (k > best) best = k, at = i;
+    }
+    const uint64_t win = warp_max(best);
+    if (win == 0) break;
+    const int i = static_cast<int>(__reduce_min_sync(kAll, best == win ? static_cast<uint32_t>(at) : kAll));
+    if (lane == j) mine = i;
+    if (best == win && at == i) gone |= 1u << (i >> 5);
+  }
+  return mine;
+}
+
+// ---------------------------------------------------------------------- by words
+
+constexpr int kIndexBits = 10;
+constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1u, kTopRank = (1u << (32 - kIndexBits)) - 1u;
+
+// Largest first: Batcher's odd-even merges.
+template <int V>
+__device__ __forceinline__ void sort_words(uint32_t (&w)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t x = w[i + j], y = w[i + j + k];
+            w[i + j] = max(x, y), w[i + j + k] = min(x, y);
+          }
+}
+template <int V>
+__device__ __forceinline__ void drop_first(uint32_t (&w)[V], bool mine) {
+#pragma unroll
+  for (int v = 0; v + 1 < V; ++v) w[v] = mine ? w[v + 1] : w[v];
+  w[V - 1] = mine ? 0u : w[V - 1];
 }
 
 // What is reckoned with, in units of 2^-24: for a score in fp32, of the row's largest, an exponential
-// and divisions (8), and for the softmax a sum of V terms a lane over the warp as well; for sums with a
-// bias or of two scores, of their terms, 4.
-constexpr float kUnit = 1.0f / (1 << 24), kSumError = 4.0f * kUnit;
+// and divisions (8), and for the softmax a sum of V terms a lane over the warp as well; for the sum
+// with a bias, and what is taken from it, 2 of their terms.
+constexpr float kUnit = 1.0f / (1 << 24);
+
+// What the biases of a warp's lanes have in common for every row.
+template <int V>
+struct Bias {
+  float b[V], lo, hi;
+  __device__ __forceinline__ Bias(const Args& a, int first) {
+    lo = 0.0f, hi = 0.0f;
+    if (a.bias == nullptr) return;
+    lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      b[v] = first + v < a.experts ? __ldg(a.bias + first + v) : 0.0f;
+      if (first + v < a.experts) lo = fminf(lo, b[v]), hi = fmaxf(hi, b[v]);
+    }
+    lo = -warp_max(-lo), hi = warp_max(hi);
+  }
+};
 
 template <int V, bool kSoftmax>
-__device__ __forceinline__ int choose(const Args& a, long long row, const float (&l)[V], int lane) {
-  uint32_t key[V];
+__device__ __forceinline__ int choose(const Args& a, long long row, const float (&l)[V], const Bias<V>& bias, int lane) {
+  const int first = lane * V;
+  uint32_t w[V];
+  int near = 0;  // ranks this close or closer need a second look
   if (a.bias == nullptr && a.groups == 1) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = l[v] == -INFINITY ? 0u : key_of(l[v]);
-    return take_best<V>(key, a.top_k, lane);
-  }
-  float m = 0.0f, rz = 1.0f;
-  if (kSoftmax) {
-    m = l[0];
+    for (int v = 0; v < V; ++v) {
+      const uint32_t name = kIndexMask - static_cast<uint32_t>(first + v);
+      w[v] = l[v] == -INFINITY ? 0u : (key_of(l[v]) & ~kIndexMask) | name;
+    }
+    if (a.bf16) near = -1;  // (16 bits are all there is)
+    sort_words<V>(w);
+  } else {
+    float m = 0.0f, rz = 1.0f, c[V];
+    if (kSoftmax) {
+      m = l[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-    m = warp_max(m);
-    float z = 0.0f;
+      for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+      m = warp_max(m);
+      float z = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) z += expf(l[v] - m);
-    rz = 1.0f / warp_sum(z);
-  }
-  float c[V], b[V];
+      for (int v = 0; v < V; ++v) c[v] = expf(l[v] - m), z += c[v];
+      rz = 1.0f / warp_sum(z);
+    }
+    const float range = (kSoftmax ? rz : 1.0f) + (bias.hi - bias.lo), scale = (kTopRank - 3) / range;
+    bool bad = !(range < INFINITY);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int i = lane + 32 * v;
-    b[v] = a.bias != nullptr && i < a.experts ? a.bias[i] : 0.0f;
-    c[v] = (kSoftmax ? expf(l[v] - m) * rz : 1.0f / (1.0f + expf(-l[v]))) + b[v];
-    key[v] = l[v] == -INFINITY ? 0u : key_of(c[v]);
-  }
-  // what two of them may be off together
-  const float off = 2.0f * kUnit * (kSoftmax ? (V + 16) * rz : 8.0f);
-  auto near = [&](float x, float y) { return !(x - y > off + kSumError * (fabsf(x) + fabsf(y))); };
-  bool again = false;
-  if (a.groups > 1) {
-    const uint32_t mine = group_keys<V>(key, a, lane);
-    const uint32_t mask = best_groups(mine, a, lane);
-    const bool in = (mask >> lane) & 1u;
-    // the worst group in and the best one out
-    const uint32_t worst = ~warp_max(in ? ~mine : 0u), best = warp_max(in || lane >= a.groups ? 0u : mine);
-    again = best != 0 && (near(of_key(worst), of_key(best) + off));
-    drop_groups<V>(key, mask, a, lane);
-    if (a.bias == nullptr) {
+    for (int v = 0; v < V; ++v) {
+      c[v] = kSoftmax ? c[v] * rz : 1.0f / (1.0f + expf(-l[v]));
+      if (a.bias != nullptr) c[v] += bias.b[v];
+      bad = bad || c[v] != c[v];
+      const uint32_t q = min(1u + static_cast<uint32_t>(fmaxf((c[v] - bias.lo) * scale, 0.0f)), kTopRank - 1u);
+      w[v] = l[v] == -INFINITY ? 0u : (q << kIndexBits) | (kIndexMask - static_cast<uint32_t>(first + v));
+    }
+    if (__any_sync(kAll, bad)) return among_all<kSoftmax>(a, row, lane);
+    const float off = kUnit * (2.0f * (kSoftmax ? (V + 16) * rz : 8.0f) + 4.0f * (fabsf(bias.lo) + fabsf(bias.hi) + range));
+    near = static_cast<int>(off * scale) + 3;  // (and a unit of each of the two, and of the product)
+    if (a.groups > 1) {
+      const float unit = range / (kTopRank - 3);
+      auto value = [&](uint32_t word) { return bias.lo + unit * static_cast<float>(word >> kIndexBits); };
+      uint32_t one, two;
+      int group;  // whose two best words the lane has
+      bool in_lane = a.lanes_per_group > 0;
+      if (in_lane) {  // a group is a power of two of lanes: their first two words are merged
+        sort_words<V>(w);
+        one = w[0], two = V > 1 ? w[V > 1 ? 1 : 0] : 0u;
+        for (int d = 1; d < a.lanes_per_group; d <<= 1) {
+          const uint32_t x = __shfl_xor_sync(kAll, one, d), y = __shfl_xor_sync(kAll, two, d);
+          two = max(min(one, x), max(two, y));
+          one = max(one, x);
+        }
+        group = lane / a.lanes_per_group;
+      } else {
+        one = two = 0;
+        for (int g = 0; g < a.groups; ++g) {
+          uint32_t x = 0, y = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (key[v] != 0) key[v] = key_of(l[v]);
+          for (int v = 0; v < V; ++v) {
+            const uint32_t k = static_cast<int>(a.per_group(static_cast<uint32_t>(first + v))) == g ? w[v] : 0u;
+            y = max(y, min(x, k));
+            x = max(x, k);
+          }
+          const uint32_t best = __reduce_max_sync(kAll, x), next = __reduce_max_sync(kAll, x == best ? y : x);
+          if (lane == g) one = best, two = next;
+        }
+        group = lane;
+      }
+      const bool speaks = in_lane ? lane % a.lanes_per_group == 0 && group < a.groups : group < a.groups;
+      uint32_t sum = !speaks || one == 0 ? 0u : key_of(two == 0 ? value(one) : value(one) + value(two));
+      uint32_t mask = 0, worst = 0;
+      for (int j = 0; j < a.top_groups; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, sum);
+        if (top == 0) break;
+        const int owner = __ffs(__ballot_sync(kAll, sum == top)) - 1;
+        worst = top;
+        mask |= 1u << __shfl_sync(kAll, group, owner);
+        if (lane == owner) sum = 0;
+      }
+      const uint32_t left = __reduce_max_sync(kAll, sum);
+      if (left != 0 && !(of_key(worst) - of_key(left) > 2.0f * (near + 1) * unit + 8.0f * kUnit * (fabsf(of_key(worst)) + fabsf(of_key(left)))))
+        return among_all<kSoftmax>(a, row, lane);
+      if (in_lane) {
+        if (((mask >> group) & 1u) == 0 || group >= a.groups) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) w[v] = 0;
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (first + v < a.experts && ((mask >> a.per_group(static_cast<uint32_t>(first + v))) & 1u) == 0) w[v] = 0;
+        sort_words<V>(w);
+      }
+    } else {
+      sort_words<V>(w);
     }
   }
-  int mine = -1;
-  if (!again) {
-    mine = take_best<V>(key, a.top_k, lane);
-    if (a.bias != nullptr) {
-      // neighbours in the order, and the last one against the best that was left
-      const int n = __popc(__ballot_sync(kAll, mine >= 0));
-      const float ml = mine >= 0 ? load(a, row, mine) : 0.0f, mb = mine >= 0 ? a.bias[mine] : 0.0f;
-      const float mc = (kSoftmax ? expf(ml - m) * rz : 1.0f / (1.0f + expf(-ml))) + mb;
-      const float nl = __shfl_down_sync(kAll, ml, 1), nb = __shfl_down_sync(kAll, mb, 1), nc = __shfl_down_sync(kAll, mc, 1);
-      again = lane + 1 < n && near(mc, nc) && !(ml == nl && mb == nb);
-      const int last = n > 0 ? n - 1 : 0;
-      const float ll = __shfl_sync(kAll, ml, last), lb = __shfl_sync(kAll, mb, last), lc = __shfl_sync(kAll, mc, last);
-      float left = -INFINITY;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (key[v] != 0 && !(l[v] == ll && b[v] == lb)) left = fmaxf(left, c[v]);
-      again = again || (n == a.top_k && left != -INFINITY && near(lc, left));
-    }
+  uint32_t mine = 0, top = 0;
+  int n = 0;
+  for (; n < a.top_k; ++n) {
+    top = __reduce_max_sync(kAll, w[0]);
+    if (top == 0) break;
+    if (lane == n) mine = top;
+    drop_first<V>(w, w[0] == top);
   }
-  if (__any_sync(kAll, again)) mine = choose64<V, kSoftmax>(a, row, lane);
-  return mine;
+  const int chosen = mine == 0 ? -1 : static_cast<int>(kIndexMask - (mine & kIndexMask));
+  if (near < 0) return chosen;
+  // neighbours in the order
+  const int rank = static_cast<int>(mine >> kIndexBits), next = __shfl_down_sync(kAll, rank, 1);
+  const bool close = lane + 1 < n && rank - next <= near;
+  uint32_t left = n == a.top_k ? __reduce_max_sync(kAll, w[0]) : 0u;
+  const int last = __shfl_sync(kAll, rank, n > 0 ? n - 1 : 0);
+  const bool border = left != 0 && last - static_cast<int>(left >> kIndexBits) <= near;
+  if (!__any_sync(kAll, close) && !border) return chosen;
+  // the same numbers (their order is the index's), or others
+  float ml = 0.0f, mb = 0.0f;
+  if (chosen >= 0) ml = load(a, row, chosen), mb = a.bias != nullptr ? a.bias[chosen] : 0.0f;
+  const float nl = __shfl_down_sync(kAll, ml, 1), nb = __shfl_down_sync(kAll, mb, 1);
+  bool again = __any_sync(kAll, close && !(ml == nl && mb == nb));
+  const float ll = __shfl_sync(kAll, ml, n > 0 ? n - 1 : 0), lb = __shfl_sync(kAll, mb, n > 0 ? n - 1 : 0);
+  int candidate = chosen, found = n;
+  while (left != 0 && last - static_cast<int>(left >> kIndexBits) <= near) {
+    const int i = static_cast<int>(kIndexMask - (left & kIndexMask));
+    if (!(load(a, row, i) == ll && (a.bias == nullptr || a.bias[i] == lb))) again = true;
+    if (lane == found) candidate = i;
+    ++found;
+    drop_first<V>(w, w[0] == left);
+    left = __reduce_max_sync(kAll, w[0]);
+  }
+  if (!again) return chosen;
+  if (found > 32) return among_all<kSoftmax>(a, row, lane);
+  return among<kSoftmax>(a, row, candidate, lane);
 }
 
 template <int V, bool kSoftmax>
@@ -271,15 +452,15 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args a) {
     __syncthreads();
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Bias<V> bias(a, lane * V);
   for (long long row = static_cast<long long>(blockIdx.x) * kWarps + warp; row < a.tokens;
        row += static_cast<long long>(gridDim.x) * kWarps) {
     int mine = -1;
     float w = 0.0f;
     if (a.live == nullptr || a.live[row] != 0) {
       float l[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) l[v] = lane + 32 * v < a.experts ? load(a, row, lane + 32 * v) : -INFINITY;
-      mine = choose<V, kSoftmax>(a, row, l, lane);
+      load_row<V>(a, row, lane * V, l);
+      mine = choose<V, kSoftmax>(a, row, l, bias, lane);
       const bool on = mine >= 0;
       const float ml = on ? load(a, row, mine) : -INFINITY;
       if (kSoftmax) {
@@ -337,71 +518,74 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args a) {
 //   softmax, renormalised:  dl_j = w_j (dw_j - sum_k dw_k q_k)            for chosen j, 0 elsewhere
 //   softmax:                dl_i = scale p_i ([i chosen] dw_i - sum_k dw_k p_k)
 //   logistic:               as the first with a factor 1 - s_j; without the sum where not renormalised.
+//
+// A warp writes its row whole, with what the chosen experts' entries would be if they had not been
+// chosen, and then the chosen ones' again, a lane each. Bound by what it writes.
 template <int V, bool kSoftmax>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const Args a) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = lane * V;
+  const float nan = __uint_as_float(0x7FC00000u);
   for (long long row = static_cast<long long>(blockIdx.x) * kWarps + warp; row < a.tokens;
        row += static_cast<long long>(gridDim.x) * kWarps) {
     int mine = -1;
     float w = 0.0f, g = 0.0f;
-    if (lane < a.top_k) {
-      mine = a.index[row * a.top_k + lane];
-      if (mine >= 0 && mine < a.experts) {
-        w = a.weight[row * a.top_k + lane];
-        g = a.dweight[row * a.top_k + lane];
-      } else {
-        mine = mine == -1 ? -1 : a.experts;
-      }
+    if (lane < a.top_k) mine = a.index[row * a.top_k + lane];
+    const bool on = mine >= 0 && mine < a.experts, bad = __any_sync(kAll, mine != -1 && !on);
+    float ml = 0.0f;
+    if (on) {
+      w = a.weight[row * a.top_k + lane];
+      g = a.dweight[row * a.top_k + lane];
+      if (!kSoftmax) ml = load(a, row, mine);
     }
-    const bool on = mine >= 0 && mine < a.experts;
-    const bool bad = __any_sync(kAll, mine >= a.experts), any = __any_sync(kAll, on);
     const float mean = warp_sum(g * w) / a.scale;
     float d = (a.renormalise ? g - mean : g) * w;
-    if (!kSoftmax && on) {
-      const float ml = load(a, row, mine);
-      d *= 1.0f / (1.0f + expf(ml));  // 1 - s
-    }
+    if (!kSoftmax) d *= 1.0f / (1.0f + expf(ml));  // 1 - s
     float out[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = 0.0f;
-    if (kSoftmax && !a.renormalise && any) {
-      float l[V], m = -INFINITY, z = 0.0f;
+    float rest = 0.0f;  // what the lane's expert would have if it were not chosen
+    if (kSoftmax && !a.renormalise && __any_sync(kAll, on)) {
+      float m, z = 0.0f;
+      load_row<V>(a, row, first, out);
+      m = out[0];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        l[v] = lane + 32 * v < a.experts ? load(a, row, lane + 32 * v) : -INFINITY;
-        m = fmaxf(m, l[v]);
-      }
+      for (int v = 1; v < V; ++v) m = fmaxf(m, out[v]);
       m = warp_max(m);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        out[v] = l[v] == -INFINITY ? 0.0f : expf(l[v] - m);
+        out[v] = out[v] == -INFINITY ? 0.0f : expf(out[v] - m);
         z += out[v];
       }
       const float f = -mean * a.scale / warp_sum(z);
 #pragma unroll
       for (int v = 0; v < V; ++v) out[v] *= f;
+      if (on) rest = expf(load(a, row, mine) - m) * f;
     }
-    for (int j = 0; j < a.top_k; ++j) {
-      const int i = __shfl_sync(kAll, mine, j);
-      const float x = __shfl_sync(kAll, d, j);
-      if (i >= 0 && (i & 31) == lane) {
+    if (bad) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (v == i >> 5) out[v] += x;
+      for (int v = 0; v < V; ++v) out[v] = nan;
+    }
+    store_row<V>(a, row, first, out);
+    if (bad) continue;
+    // an expert that the row names more than once takes all its slots' parts, in their order
+    const unsigned same = __match_any_sync(kAll, on ? mine : -1 - lane);
+    float sum = d;
+    if (__any_sync(kAll, __popc(same) > 1)) {
+      sum = 0.0f;
+      for (int j = 0; j < a.top_k; ++j) {
+        const float x = __shfl_sync(kAll, d, j);
+        if ((same >> j) & 1u) sum += x;
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int i = lane + 32 * v;
-      if (i >= a.experts) continue;
-      if (bad) out[v] = __uint_as_float(0x7FC00000u);
-      const long long at = row * a.ld_d + i;
+    __syncwarp();  // (orders the two stores to one address)
+    if (on && (same & ((1u << lane) - 1u)) == 0) {
+      const long long at = row * a.ld_d + mine;
       if (a.bf16) {
-        static_cast<__nv_bfloat16*>(a.dlogits)[at] = __float2bfloat16_rn(out[v]);
+        static_cast<__nv_bfloat16*>(a.dlogits)[at] = __float2bfloat16_rn(rest + sum);
       } else {
-        static_cast<float*>(a.dlogits)[at] = out[v];
+        static_cast<float*>(a.dlogits)[at] = rest + sum;
       }
     }
   }
@@ -453,7 +637,12 @@ Args args_of(const zopt_route_job& c) {
 }
 
 template <int V>
-zopt_status launch(const Args& a, bool softmax, bool backward, unsigned blocks, cudaStream_t s) {
+zopt_status launch(Args& a, bool softmax, bool backward, unsigned blocks, cudaStream_t s) {
+  const uintptr_t size = a.bf16 ? 2 : 4, piece = std::min<uintptr_t>(16, V * size);
+  a.vec = reinterpret_cast<uintptr_t>(a.logits) % piece == 0 && a.ld * size % piece == 0;
+  a.vec_d = reinterpret_cast<uintptr_t>(a.dlogits) % piece == 0 && a.ld_d * size % piece == 0;
+  const int per = static_cast<int>(a.per_group.d), lanes = per / V;
+  a.lanes_per_group = per % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
   const auto kernel = backward ? (softmax ? backward_kernel<V, true> : backward_kernel<V, false>)
                                : (softmax ? forward_kernel<V, true> : forward_kernel<V, false>);
   return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, s, a);
