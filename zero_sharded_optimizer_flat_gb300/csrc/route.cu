@@ -1,17 +1,17 @@
 // Routing tokens to experts, forward and backward.
 //
-// A warp takes a token's row, a lane V experts that follow one another. Ranking is in exact order (of the
-// score plus the bias as real numbers, the lowest index first among equal ones), so that a choice never
-// depends on how an exponential rounds. An expert is one word: 22 bits that do not decrease with its
-// rank's number, above 10 that fall with its index. A lane sorts its words once (a fixed network); the
-// warp's largest word, an integer maximum, is the next choice, and its lane moves its words up. Without a
-// bias the 22 bits are the logit's own leading ones (a bf16 logit's are all of it), with one, or with
-// groups, the score's and the bias's sum in fixed point over the row's range. Neighbours in the
-// order that come closer than those bits and the score's error tell apart, if they are not the same
-// numbers, are told apart in fp64, together with what the border of the choice may have left out (one
-// row in some hundreds).
+// A warp takes a few tokens' rows one after another, a lane V experts that follow one another. Ranking is
+// in exact order (of the score plus the bias as real numbers, the lowest index first among equal ones), so
+// that a choice never depends on how an exponential rounds. An expert is one word: 22 bits that do not
+// decrease with its rank's number, above 10 that fall with its index. A lane sorts its words once (a
+// fixed network); the warp's largest word, an integer maximum, is the next choice, and its lane moves its
+// words up. Without a bias the 22 bits are the logit's own leading ones (a bf16 logit's are all of
+// it), with one, or with groups, the score's and the bias's sum in fixed point over the row's range.
+// Neighbours in the order that come closer than those bits and the score's error tell apart have the
+// warp rank their row again in fp64 (one row in some hundreds where there is a bias).
 //
-// Bound by the instructions of a row, some 200 for eight of 256 experts.
+// The choices of the rows lie side by side in the warp's lanes, so that weights, checks and stores are
+// done once for all of them. Bound by the instructions of a row.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,7 +45,8 @@ struct Args {
   long long tokens;
   int experts, top_k, groups, top_groups;
   Divisor per_group;
-  int bf16, renormalise, alone;  // alone: one block has all rows, counts need no sum over blocks
+  int softmax, bf16, renormalise, alone;  // alone: one block has all rows, counts need no sum over blocks
+  int width, rows;               // lanes for a row's choices (a power of two), rows of a warp at a time
   int vec, vec_d;                // a lane's experts can be loaded (stored) at once
   int lanes_per_group;           // where a group is a power of two of whole lanes' experts, else 0
   float scale;
@@ -160,9 +161,10 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
   const uint32_t lo = __reduce_max_sync(kAll, hi == top ? static_cast<uint32_t>(k) : 0u);
   return (static_cast<uint64_t>(top) << 32) | lo;
 }
-// (NaN: the others' largest)
-__device__ __forceinline__ float warp_max(float x) {
-  return of_key(__reduce_max_sync(kAll, x != x ? 0x007FFFFFu : key_of(x)));  // 0x007FFFFF: -inf's
+__device__ __forceinline__ float warp_max(float x) {  // (NaN: the others' largest)
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+  return x;
 }
 template <typename T>
 __device__ __forceinline__ T warp_sum(T x) {
@@ -170,23 +172,44 @@ __device__ __forceinline__ T warp_sum(T x) {
   for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
   return x;
 }
+// Over `width` (a power of two) lanes side by side.
+__device__ __forceinline__ float lanes_max(float x, int width) {
+  for (int d = width >> 1; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+  return x;
+}
+__device__ __forceinline__ float lanes_sum(float x, int width) {
+  for (int d = width >> 1; d >= 1; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+  return x;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------- in fp64
 
-// What an expert is ranked by: the score and the bias, or without a bias the logit.
-template <bool kSoftmax>
-__device__ __forceinline__ double rank64(const Args& a, float l, int i, double top, double z) {
-  if (a.bias == nullptr) return static_cast<double>(l);
-  const double s = kSoftmax ? exp(static_cast<double>(l) - top) / z : 1.0 / (1.0 + exp(-static_cast<double>(l)));
-  return s + static_cast<double>(a.bias[i]);
-}
-__device__ __forceinline__ void softmax64(const Args& a, long long row, int lane, double& top, double& z) {
-  float m = -INFINITY;
-  for (int i = lane; i < a.experts; i += 32) m = fmaxf(m, load(a, row, i));
-  top = static_cast<double>(warp_max(m));
-  double part = 0.0;
-  for (int i = lane; i < a.experts; i += 32) part += exp(static_cast<double>(load(a, row, i)) - top);
-  z = warp_sum(part);
+// e^x, x at most 700, to some 2^-50: x = k ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, as Cody and Waite take
+// it) and r's Taylor series. (The fp64 pipe is narrow, and this need not be exact to the last bit.)
+__device__ __forceinline__ double exp64(double x) {
+  x = x < -700.0 ? -700.0 : x > 700.0 ? 700.0 : x;  // (NaN stays)
+  const double k = rint(x * 1.4426950408889634);
+  const double r = fma(-k, 1.9082149292705877e-10, fma(-k, 0.693147180369123816490, x));
+  double p = 1.0 / 479001600.0;
+#pragma unroll
+  for (int n = 11; n >= 0; --n) {
+    constexpr double c[12] = {1.0,         1.0,          1.0 / 2.0,     1.0 / 6.0,      1.0 / 24.0,      1.0 / 120.0,
+                              1.0 / 720.0, 1.0 / 5040.0, 1.0 / 40320.0, 1.0 / 362880.0, 1.0 / 3628800.0, 1.0 / 39916800.0};
+    p = fma(p, r, c[n]);
+  }
+  return p * __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(1023 + static_cast<int>(k)) << 52));
 }
 
 // The best `most` of the candidates, one a lane (key 0: none), the lowest index first among equal ones.
@@ -202,31 +225,88 @@ __device__ __forceinline__ int best64(uint64_t key, int i, int most, int lane) {
   return mine;
 }
 
-// The row's choice among `i` of every lane (-1: none).
-template <bool kSoftmax>
-__device__ __noinline__ int among(const Args& a, long long row, int i, int lane) {
-  double top = 0.0, z = 1.0;
-  if (kSoftmax && a.bias != nullptr) softmax64(a, row, lane, top, z);
-  return best64(i >= 0 ? key_of(rank64<kSoftmax>(a, load(a, row, i), i, top, z)) : 0ull, i, a.top_k, lane);
+// An expert's rank: its score and the bias, without a bias (but for groups' sums) its logit.
+struct Rank64 {
+  double m = 0.0, z = 1.0;
+  __device__ __forceinline__ double score(const Args& a, float l, int i) const {
+    const double x = static_cast<double>(l), e = exp64(a.softmax ? x - m : -x);
+    const double s = a.softmax ? e / z : l == INFINITY ? 1.0 : 1.0 / (1.0 + e);
+    return a.bias != nullptr ? s + static_cast<double>(a.bias[i]) : s;
+  }
+  __device__ __forceinline__ uint64_t key(const Args& a, float l, int i) const {
+    return key_of(a.bias == nullptr ? static_cast<double>(l) : score(a, l, i));
+  }
+};
+
+// A row's choice once more, from those alone whose word is `least` or more, in the groups given: lane j gets
+// the j-th. They are few as a rule; they are listed, a lane takes each (the fp64 pipe being narrow), and more
+// than 32 are left to choose_all.
+template <int V>
+__device__ __noinline__ int choose_near(const Args& a, long long row, float lo, float scale, uint32_t least, uint32_t groups,
+                                        uint16_t* list) {
+  const int lane = threadIdx.x & 31, first = lane * V;
+  float l[V];
+  load_row<V>(a, row, first, l);
+  Rank64 r;
+  float m = 0.0f, rz = 1.0f;
+  if (a.softmax && scale > 0.0f) {
+    m = l[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+    m = warp_max(m);
+    double z = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) z += l[v] == -INFINITY ? 0.0 : exp64(static_cast<double>(l[v]) - static_cast<double>(m));
+    r.m = static_cast<double>(m), r.z = warp_sum(z);
+    rz = 1.0f / static_cast<float>(r.z);
+  }
+  int n = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int i = first + v;
+    bool in = l[v] != -INFINITY && (a.groups == 1 || ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) != 0);
+    if (scale > 0.0f) {  // (as Chooser::row has it, but for the last bits)
+      const float s = (a.softmax ? __expf(l[v] - m) * rz : 1.0f / (1.0f + __expf(-l[v]))) + (a.bias != nullptr && i < a.experts ? a.bias[i] : 0.0f);
+      in = in && (s - lo) * scale + 16.0f >= static_cast<float>(least);
+    } else {
+      in = in && (key_of(l[v]) >> 10) >= least;
+    }
+    const unsigned who = __ballot_sync(kAll, in);
+    const int at = n + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) list[at] = static_cast<uint16_t>(i);
+    n += __popc(who);
+  }
+  __syncwarp();
+  if (n > 32) return -2;
+  const int i = lane < n ? list[lane] : -1;
+  __syncwarp();
+  return best64(i >= 0 ? r.key(a, load(a, row, i), i) : 0ull, i, a.top_k, lane);
 }
 
-// The row's choice among all experts, its groups' scores in fp64 as well. Experts a lane at a time: lane l
-// looks at l, l + 32, ...; those taken are marked in `gone`.
-template <bool kSoftmax>
-__device__ __noinline__ int among_all(const Args& a, long long row, int lane) {
-  double top = 0.0, z = 1.0;
-  if (kSoftmax) softmax64(a, row, lane, top, z);
-  uint32_t gone = 0, groups = kAll;
+// A row's choice once more, from all its experts, the groups ranked again as well. Lane l looks at experts l,
+// l + 32, ....
+__device__ __noinline__ int choose_all(const Args& a, long long row) {
+  const int lane = threadIdx.x & 31;
+  Rank64 r;
+  if (a.softmax && (a.bias != nullptr || a.groups > 1)) {
+    float m = -INFINITY;
+    for (int i = lane; i < a.experts; i += 32) m = fmaxf(m, load(a, row, i));
+    m = warp_max(m);
+    double part = 0.0;
+    for (int i = lane; i < a.experts; i += 32) part += exp64(static_cast<double>(load(a, row, i)) - static_cast<double>(m));
+    r.m = static_cast<double>(m), r.z = warp_sum(part);
+    if (!(m < INFINITY)) r.z = __longlong_as_double(0x7FF8000000000000ll);
+  }
+  uint32_t groups = kAll, gone = 0;
   if (a.groups > 1) {
     uint64_t mine = 0;
+    const int per = static_cast<int>(a.per_group.d);
     for (int g = 0; g < a.groups; ++g) {
       uint64_t first = 0, second = 0;
-      for (int i = g * static_cast<int>(a.per_group.d) + lane; i < (g + 1) * static_cast<int>(a.per_group.d); i += 32) {
+      for (int i = g * per + lane; i < (g + 1) * per; i += 32) {
         const float l = load(a, row, i);
         if (l == -INFINITY) continue;
-        double c = kSoftmax ? exp(static_cast<double>(l) - top) / z : 1.0 / (1.0 + exp(-static_cast<double>(l)));
-        if (a.bias != nullptr) c += static_cast<double>(a.bias[i]);
-        const uint64_t k = key_of(c);
+        const uint64_t k = key_of(r.score(a, l, i));
         second = k > first ? first : k > second ? k : second;
         first = k > first ? k : first;
       }
@@ -244,9 +324,9 @@ __device__ __noinline__ int among_all(const Args& a, long long row, int lane) {
     int at = -1;
     for (int i = lane, v = 0; i < a.experts; i += 32, ++v) {
       const float l = load(a, row, i);
-      if (l == -INFINITY || ((gone >> v) & 1u) != 0) continue;
+      if (((gone >> v) & 1u) != 0 || l == -INFINITY) continue;
       if (a.groups > 1 && ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) == 0) continue;
-      const uint64_t k = key_of(rank64<kSoftmax>(a, l, i, top, z));
+      const uint64_t k = r.key(a, l, i);
       if (k > best) best = k, at = i;
     }
     const uint64_t win = warp_max(best);
@@ -256,6 +336,17 @@ __device__ __noinline__ int among_all(const Args& a, long long row, int lane) {
     if (best == win && at == i) gone |= 1u << (i >> 5);
   }
   return mine;
+}
+
+// The groups that take part, from the two best experts of each (lane g: group g's; -1: there is none), in fp64.
+__device__ __noinline__ uint32_t groups64(const Args& a, long long row, int one, int two) {
+  const Rank64 r;
+  const int lane = threadIdx.x & 31;
+  double sum = 0.0;
+  if (one >= 0) sum = r.score(a, load(a, row, one), one);
+  if (two >= 0) sum += r.score(a, load(a, row, two), two);
+  const int g = best64(one >= 0 ? key_of(sum) : 0ull, lane, a.top_groups, lane);
+  return __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
 }
 
 // ---------------------------------------------------------------------- by words
@@ -286,220 +377,273 @@ __device__ __forceinline__ void drop_first(uint32_t (&w)[V], bool mine) {
   w[V - 1] = mine ? 0u : w[V - 1];
 }
 
-// What is reckoned with, in units of 2^-24: for a score in fp32, of the row's largest, an exponential
-// and divisions (8), and for the softmax a sum of V terms a lane over the warp as well; for the sum
-// with a bias, and what is taken from it, 2 of their terms.
+// What a rank in fp32 may be off, in units of 2^-24. A logistic score: its exponential's 2^-22 and its
+// argument's rounding weigh at most a quarter, the sum and the reciprocal are 2^-24 and 2^-23: 5. A
+// softmax score, of the row's largest: an exponential (5), the sum of V terms a lane over the warp's
+// lanes (V + 5) and the reciprocal and products (5). What is made of it and the bias: 2 of their terms.
 constexpr float kUnit = 1.0f / (1 << 24);
+// 2^23, what brings a number below 2^22 into the low bits of its fp32 pattern.
+constexpr float kMagic = 8388608.0f;
 
-// What the biases of a warp's lanes have in common for every row.
-template <int V>
-struct Bias {
-  float b[V], lo, hi;
-  __device__ __forceinline__ Bias(const Args& a, int first) {
-    lo = 0.0f, hi = 0.0f;
-    if (a.bias == nullptr) return;
+// What a batch of rows has in its lanes: lane r W + j row r's j-th choice, and in all of a row's W lanes
+// what else is known of the row.
+struct Batch {
+  uint32_t mine = 0;       // the choice's word
+  uint32_t left = 0;       // the best word that was left out
+  int near = -1;           // ranks this close or closer need a second look
+  float scale = 0.0f;      // of fixed point (0: the words are of logits)
+  uint32_t groups = kAll;  // those that take part
+  bool all = false;        // its groups may be others, or a number was none: choose_all
+  bool bad = false;        // softmax: a NaN or +inf
+  float m = 0.0f, z = 1.0f;  // softmax: the largest logit and the sum relative to it
+};
+
+template <int V, bool kPlain>
+struct Chooser {
+  const Args& a;
+  int lane, first;
+  float b[V], lo = 0.0f, hi = 0.0f;
+
+  __device__ __forceinline__ explicit Chooser(const Args& args) : a(args), lane(threadIdx.x & 31), first(lane * V) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) b[v] = 0.0f;
+    if (kPlain || a.bias == nullptr) return;
     lo = INFINITY, hi = -INFINITY;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      b[v] = first + v < a.experts ? __ldg(a.bias + first + v) : 0.0f;
-      if (first + v < a.experts) lo = fminf(lo, b[v]), hi = fmaxf(hi, b[v]);
+      if (first + v >= a.experts) continue;
+      b[v] = __ldg(a.bias + first + v);
+      lo = fminf(lo, b[v]), hi = fmaxf(hi, b[v]);
     }
     lo = -warp_max(-lo), hi = warp_max(hi);
   }
-};
+  __device__ __forceinline__ uint32_t name(int v) const { return kIndexMask - static_cast<uint32_t>(first + v); }
 
-template <int V, bool kSoftmax>
-__device__ __forceinline__ int choose(const Args& a, long long row, const float (&l)[V], const Bias<V>& bias, int lane) {
-  const int first = lane * V;
-  uint32_t w[V];
-  int near = 0;  // ranks this close or closer need a second look
-  if (a.bias == nullptr && a.groups == 1) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const uint32_t name = kIndexMask - static_cast<uint32_t>(first + v);
-      w[v] = l[v] == -INFINITY ? 0u : (key_of(l[v]) & ~kIndexMask) | name;
-    }
-    if (a.bf16) near = -1;  // (16 bits are all there is)
-    sort_words<V>(w);
-  } else {
-    float m = 0.0f, rz = 1.0f, c[V];
-    if (kSoftmax) {
-      m = l[0];
-#pragma unroll
-      for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-      m = warp_max(m);
-      float z = 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) c[v] = expf(l[v] - m), z += c[v];
-      rz = 1.0f / warp_sum(z);
-    }
-    const float range = (kSoftmax ? rz : 1.0f) + (bias.hi - bias.lo), scale = (kTopRank - 3) / range;
-    bool bad = !(range < INFINITY);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      c[v] = kSoftmax ? c[v] * rz : 1.0f / (1.0f + expf(-l[v]));
-      if (a.bias != nullptr) c[v] += bias.b[v];
-      bad = bad || c[v] != c[v];
-      const uint32_t q = min(1u + static_cast<uint32_t>(fmaxf((c[v] - bias.lo) * scale, 0.0f)), kTopRank - 1u);
-      w[v] = l[v] == -INFINITY ? 0u : (q << kIndexBits) | (kIndexMask - static_cast<uint32_t>(first + v));
-    }
-    if (__any_sync(kAll, bad)) return among_all<kSoftmax>(a, row, lane);
-    const float off = kUnit * (2.0f * (kSoftmax ? (V + 16) * rz : 8.0f) + 4.0f * (fabsf(bias.lo) + fabsf(bias.hi) + range));
-    near = static_cast<int>(off * scale) + 3;  // (and a unit of each of the two, and of the product)
-    if (a.groups > 1) {
-      const float unit = range / (kTopRank - 3);
-      auto value = [&](uint32_t word) { return bias.lo + unit * static_cast<float>(word >> kIndexBits); };
-      uint32_t one, two;
-      int group;  // whose two best words the lane has
-      bool in_lane = a.lanes_per_group > 0;
-      if (in_lane) {  // a group is a power of two of lanes: their first two words are merged
-        sort_words<V>(w);
-        one = w[0], two = V > 1 ? w[V > 1 ? 1 : 0] : 0u;
-        for (int d = 1; d < a.lanes_per_group; d <<= 1) {
-          const uint32_t x = __shfl_xor_sync(kAll, one, d), y = __shfl_xor_sync(kAll, two, d);
-          two = max(min(one, x), max(two, y));
-          one = max(one, x);
-        }
-        group = lane / a.lanes_per_group;
-      } else {
-        one = two = 0;
-        for (int g = 0; g < a.groups; ++g) {
-          uint32_t x = 0, y = 0;
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const uint32_t k = static_cast<int>(a.per_group(static_cast<uint32_t>(first + v))) == g ? w[v] : 0u;
-            y = max(y, min(x, k));
-            x = max(x, k);
-          }
-          const uint32_t best = __reduce_max_sync(kAll, x), next = __reduce_max_sync(kAll, x == best ? y : x);
-          if (lane == g) one = best, two = next;
-        }
-        group = lane;
+  // The words of the groups that take part, sorted; what the row's lanes have to know goes to r.
+  __device__ __forceinline__ void choose_groups(uint32_t (&w)[V], long long row, float unit, int near, Batch& r) const {
+    auto value = [&](uint32_t word) { return lo + unit * static_cast<float>(word >> kIndexBits); };
+    // a group's sum, its name (the lowest first among equal sums) in the low bits
+    auto sum_of = [&](uint32_t one, uint32_t two, int g) {
+      return one == 0 ? 0u : (key_of(two == 0 ? value(one) : value(one) + value(two)) & ~31u) | (31u - static_cast<uint32_t>(g));
+    };
+    uint32_t sum = 0, one = 0, two = 0;  // (in_lane: of the lane's group; else of group `lane`)
+    const bool in_lane = a.lanes_per_group > 0;
+    if (in_lane) {  // a group is a power of two of lanes: their first two words are merged
+      sort_words<V>(w);
+      one = w[0], two = V > 1 ? w[V > 1 ? 1 : 0] : 0u;
+      for (int d = 1; d < a.lanes_per_group; d <<= 1) {
+        const uint32_t x = __shfl_xor_sync(kAll, one, d), y = __shfl_xor_sync(kAll, two, d);
+        two = max(min(one, x), max(two, y));
+        one = max(one, x);
       }
-      const bool speaks = in_lane ? lane % a.lanes_per_group == 0 && group < a.groups : group < a.groups;
-      uint32_t sum = !speaks || one == 0 ? 0u : key_of(two == 0 ? value(one) : value(one) + value(two));
-      uint32_t mask = 0, worst = 0;
-      for (int j = 0; j < a.top_groups; ++j) {
-        const uint32_t top = __reduce_max_sync(kAll, sum);
-        if (top == 0) break;
-        const int owner = __ffs(__ballot_sync(kAll, sum == top)) - 1;
-        worst = top;
-        mask |= 1u << __shfl_sync(kAll, group, owner);
-        if (lane == owner) sum = 0;
+      const int g = lane / a.lanes_per_group;
+      if (lane % a.lanes_per_group == 0 && g < a.groups) sum = sum_of(one, two, g);
+    } else {  // one group after another
+      for (int g = 0; g < a.groups; ++g) {
+        uint32_t x = 0, y = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const uint32_t k = static_cast<int>(a.per_group(static_cast<uint32_t>(first + v))) == g ? w[v] : 0u;
+          y = max(y, min(x, k));
+          x = max(x, k);
+        }
+        const uint32_t top = __reduce_max_sync(kAll, x), next = __reduce_max_sync(kAll, x == top ? y : x);
+        if (lane == g) one = top, two = next, sum = sum_of(top, next, g);
       }
-      const uint32_t left = __reduce_max_sync(kAll, sum);
-      if (left != 0 && !(of_key(worst) - of_key(left) > 2.0f * (near + 1) * unit + 8.0f * kUnit * (fabsf(of_key(worst)) + fabsf(of_key(left)))))
-        return among_all<kSoftmax>(a, row, lane);
+    }
+    uint32_t mask = 0, worst = 0;
+    for (int j = 0; j < a.top_groups; ++j) {
+      const uint32_t top = __reduce_max_sync(kAll, sum);
+      if (top == 0) break;  // (the whole warp's)
+      worst = top;
+      mask |= 1u << (31u - (top & 31u));
+      if (sum == top) sum = 0;
+    }
+    const uint32_t left = __reduce_max_sync(kAll, sum);
+    const float in = of_key(worst & ~31u), out = of_key(left & ~31u);
+    // (32 ulp of each go with their names)
+    if (left != 0 && !(in - out > 2.0f * (near + 1) * unit + 80.0f * kUnit * (fabsf(in) + fabsf(out)))) {
+      // The sums again in fp64, if it is clear which two experts they are of and (softmax) no sum is needed.
+      bool third = false;
       if (in_lane) {
-        if (((mask >> group) & 1u) == 0 || group >= a.groups) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) w[v] = 0;
-        }
-      } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          if (first + v < a.experts && ((mask >> a.per_group(static_cast<uint32_t>(first + v))) & 1u) == 0) w[v] = 0;
-        sort_words<V>(w);
+          third = third || (w[v] != 0 && w[v] < two && static_cast<int>((two >> kIndexBits) - (w[v] >> kIndexBits)) <= near);
+      }
+      if (!in_lane || a.softmax || __any_sync(kAll, third)) {
+        r.all = true;
+      } else {
+        const int from = min(lane * a.lanes_per_group, 31);
+        const uint32_t x = __shfl_sync(kAll, one, from), y = __shfl_sync(kAll, two, from);
+        auto expert = [&](uint32_t word) { return lane < a.groups && word != 0 ? static_cast<int>(kIndexMask - (word & kIndexMask)) : -1; };
+        mask = groups64(a, row, expert(x), expert(y));
+      }
+    }
+    r.groups = mask;
+    if (in_lane) {
+      const int g = lane / a.lanes_per_group;
+      if (g >= a.groups || ((mask >> g) & 1u) == 0) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) w[v] = 0;
       }
     } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (first + v < a.experts && ((mask >> a.per_group(static_cast<uint32_t>(first + v))) & 1u) == 0) w[v] = 0;
       sort_words<V>(w);
     }
   }
-  uint32_t mine = 0, top = 0;
-  int n = 0;
-  for (; n < a.top_k; ++n) {
-    top = __reduce_max_sync(kAll, w[0]);
-    if (top == 0) break;
-    if (lane == n) mine = top;
-    drop_first<V>(w, w[0] == top);
-  }
-  const int chosen = mine == 0 ? -1 : static_cast<int>(kIndexMask - (mine & kIndexMask));
-  if (near < 0) return chosen;
-  // neighbours in the order
-  const int rank = static_cast<int>(mine >> kIndexBits), next = __shfl_down_sync(kAll, rank, 1);
-  const bool close = lane + 1 < n && rank - next <= near;
-  uint32_t left = n == a.top_k ? __reduce_max_sync(kAll, w[0]) : 0u;
-  const int last = __shfl_sync(kAll, rank, n > 0 ? n - 1 : 0);
-  const bool border = left != 0 && last - static_cast<int>(left >> kIndexBits) <= near;
-  if (!__any_sync(kAll, close) && !border) return chosen;
-  // the same numbers (their order is the index's), or others
-  float ml = 0.0f, mb = 0.0f;
-  if (chosen >= 0) ml = load(a, row, chosen), mb = a.bias != nullptr ? a.bias[chosen] : 0.0f;
-  const float nl = __shfl_down_sync(kAll, ml, 1), nb = __shfl_down_sync(kAll, mb, 1);
-  bool again = __any_sync(kAll, close && !(ml == nl && mb == nb));
-  const float ll = __shfl_sync(kAll, ml, n > 0 ? n - 1 : 0), lb = __shfl_sync(kAll, mb, n > 0 ? n - 1 : 0);
-  int candidate = chosen, found = n;
-  while (left != 0 && last - static_cast<int>(left >> kIndexBits) <= near) {
-    const int i = static_cast<int>(kIndexMask - (left & kIndexMask));
-    if (!(load(a, row, i) == ll && (a.bias == nullptr || a.bias[i] == lb))) again = true;
-    if (lane == found) candidate = i;
-    ++found;
-    drop_first<V>(w, w[0] == left);
-    left = __reduce_max_sync(kAll, w[0]);
-  }
-  if (!again) return chosen;
-  if (found > 32) return among_all<kSoftmax>(a, row, lane);
-  return among<kSoftmax>(a, row, candidate, lane);
-}
 
-template <int V, bool kSoftmax>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const Args a) {
+  // A row's choice, into the lanes from lane0 on.
+  __device__ __forceinline__ void row(const float (&l)[V], long long at, int lane0, bool here, Batch& batch) const {
+    uint32_t w[V];
+    Batch r;
+    // (of a 1024th of each: no sum of finite ones overflows)
+    float size = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) size = fmaf(l[v], 1.0f / 1024.0f, size);
+    r.bad = __any_sync(kAll, !(size < INFINITY));
+    if (a.softmax && !(kPlain && a.renormalise)) {
+      r.m = l[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) r.m = fmaxf(r.m, l[v]);
+      r.m = warp_max(r.m);
+    }
+    if constexpr (kPlain) {
+      if (a.softmax && !a.renormalise) {
+        float z = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) z += l[v] == -INFINITY ? 0.0f : ex2((l[v] - r.m) * kLog2e);
+        r.z = warp_sum(z);
+      }
+      r.near = a.bf16 ? -1 : 0;  // (of a bf16 logit 16 bits are all there is)
+      r.all = r.bad;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t u = __float_as_uint(l[v] + 0.0f);  // -0 is 0
+        const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+        w[v] = l[v] == -INFINITY ? 0u : (key & ~kIndexMask) | name(v);
+      }
+      sort_words<V>(w);
+    } else {
+      float s[V], rz = 1.0f;
+      if (a.softmax) {
+        float z = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = ex2((l[v] - r.m) * kLog2e), z += s[v];
+        r.z = warp_sum(z);
+        rz = rcp(r.z);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = rcp(1.0f + ex2(l[v] * -kLog2e));
+      }
+      const float range = rz + (hi - lo), scale = (kTopRank - 3) * rcp(range), from = rz * scale;
+      uint32_t seen = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {  // rank = 1 + (s + b - lo) scale, rounded into the low bits
+        const uint32_t u = __float_as_uint(fmaf(s[v], from, fmaf(b[v] - lo, scale, kMagic + 1.0f)));
+        seen |= u;
+        w[v] = l[v] == -INFINITY ? 0u : (u << kIndexBits) | name(v);
+      }
+      // (a number that is none has other leading bits than 2^23's)
+      r.all = __any_sync(kAll, (seen >> 23) != (__float_as_uint(kMagic) >> 23)) || !(range < INFINITY);
+      const float off = kUnit * (2.0f * (a.softmax ? (V + 15) * rz : 5.0f) + 4.0f * (fabsf(lo) + fabsf(hi) + range));
+      r.near = static_cast<int>(off * scale) + 4;  // (and two units of each of the two)
+      r.scale = scale;
+      if (a.groups > 1) {
+        choose_groups(w, at, range * (1.0f / (kTopRank - 3)), r.near, r);
+      } else {
+        sort_words<V>(w);
+      }
+    }
+    for (int n = 0; n < a.top_k; ++n) {
+      const uint32_t top = __reduce_max_sync(kAll, w[0]);
+      if (top == 0) break;  // (the whole warp's)
+      if (lane == lane0 + n) batch.mine = top;
+      drop_first<V>(w, w[0] == top);
+    }
+    r.left = __reduce_max_sync(kAll, w[0]);
+    if (here) {
+      r.mine = batch.mine;
+      batch = r;
+    }
+  }
+};
+
+template <int V, bool kPlain>
+__global__ void __launch_bounds__(kThreads, V >= 16 ? 2 : V >= 8 ? 3 : 4) forward_kernel(const Args a) {
   __shared__ int count[kMaxExperts];
+  __shared__ uint16_t list[kWarps][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   if (a.counts != nullptr) {
     for (int i = threadIdx.x; i < a.experts; i += kThreads) count[i] = 0;
     __syncthreads();
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Bias<V> bias(a, lane * V);
-  for (long long row = static_cast<long long>(blockIdx.x) * kWarps + warp; row < a.tokens;
-       row += static_cast<long long>(gridDim.x) * kWarps) {
-    int mine = -1;
-    float w = 0.0f;
-    if (a.live == nullptr || a.live[row] != 0) {
+  const Chooser<V, kPlain> chooser(a);
+  const int lane = threadIdx.x & 31, W = a.width, j = lane & (W - 1), which = lane / W;
+  const long long step = static_cast<long long>(gridDim.x) * kWarps * a.rows;
+  for (long long row0 = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * a.rows; row0 < a.tokens; row0 += step) {
+    const int n = static_cast<int>(min(static_cast<long long>(a.rows), a.tokens - row0));
+    // bit r: row row0 + r is no padding
+    const uint32_t live = __ballot_sync(kAll, lane < n && (a.live == nullptr || a.live[row0 + lane] != 0));
+    Batch r;
+    float next[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) next[v] = -INFINITY;
+    if (live & 1u) load_row<V>(a, row0, chooser.first, next);
+    for (int k = 0; k < n; ++k) {  // (the next row is on its way while one is worked on)
       float l[V];
-      load_row<V>(a, row, lane * V, l);
-      mine = choose<V, kSoftmax>(a, row, l, bias, lane);
-      const bool on = mine >= 0;
-      const float ml = on ? load(a, row, mine) : -INFINITY;
-      if (kSoftmax) {
-        // relative to the largest logit: of the chosen ones where the weights are renormalised (the other
-        // terms cancel), else of all. A row with a NaN or +inf has no softmax.
-        bool bad = false;
 #pragma unroll
-        for (int v = 0; v < V; ++v) bad = bad || !(l[v] < INFINITY);
-        float m, z;
-        if (a.renormalise) {
-          m = warp_max(ml);
-          w = on ? expf(ml - m) : 0.0f;
-          z = warp_sum(w);
-        } else {
-          m = l[0];
-#pragma unroll
-          for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-          m = warp_max(m);
-          w = on ? expf(ml - m) : 0.0f;
-          float part = 0.0f;
-#pragma unroll
-          for (int v = 0; v < V; ++v) part += l[v] == -INFINITY ? 0.0f : expf(l[v] - m);
-          z = warp_sum(part);
-        }
-        w = on ? w / z * a.scale : 0.0f;
-        if (__any_sync(kAll, bad) && on) w = __uint_as_float(0x7FC00000u);
-      } else {
-        // s = e^l / (1 + e^l); where all chosen logits are negative, e^(l - max) in its place where the
-        // weights are renormalised: the quotients stay what they are and nothing underflows.
-        const float top = a.renormalise ? fminf(0.0f, warp_max(ml)) : 0.0f;
-        w = !on ? 0.0f : ml >= 0.0f ? 1.0f / (1.0f + expf(-ml)) : expf(ml - top) / (1.0f + expf(ml));
-        if (a.renormalise) w = w / warp_sum(w);
-        w = on ? w * a.scale : 0.0f;
-      }
+      for (int v = 0; v < V; ++v) l[v] = next[v];
+      if ((live >> k) & 2u) load_row<V>(a, row0 + k + 1, chooser.first, next);
+      if ((live >> k) & 1u) chooser.row(l, row0 + k, k * W, which == k, r);
     }
-    if (lane < a.top_k) {
-      a.index[row * a.top_k + lane] = mine;
-      a.weight[row * a.top_k + lane] = w;
-      if (a.counts != nullptr && mine >= 0) atomicAdd(count + mine, 1);
+    const long long row = row0 + which;
+    const bool there = which < n && ((live >> which) & 1u) != 0;
+    int mine = r.mine == 0 ? -1 : static_cast<int>(kIndexMask - (r.mine & kIndexMask));
+    // neighbours in the order, and the last one against the best that was left out
+    const int rank = static_cast<int>(r.mine >> kIndexBits), below = static_cast<int>(r.left >> kIndexBits);
+    const int after = __shfl_down_sync(kAll, rank, 1);
+    const bool close = j + 1 < a.top_k ? after > 0 && rank - after <= r.near : j + 1 == a.top_k && rank > 0 && below > 0 && rank - below <= r.near;
+    unsigned todo = __ballot_sync(kAll, there && (close || r.all));
+    while (todo != 0) {
+      const int from = (__ffs(todo) - 1) / W * W;  // the row's first lane
+      const int least = __shfl_sync(kAll, rank, from + a.top_k - 1) - __shfl_sync(kAll, r.near, from);
+      const bool all = __shfl_sync(kAll, r.all ? 1 : 0, from) != 0;
+      int got = -2;
+      if (!all)
+        got = choose_near<V>(a, row0 + from / W, chooser.lo, __shfl_sync(kAll, r.scale, from), static_cast<uint32_t>(max(least, 1)),
+                             __shfl_sync(kAll, r.groups, from), list[threadIdx.x >> 5]);
+      if (got == -2) got = choose_all(a, row0 + from / W);  // (-2 in every lane)
+      const int here = __shfl_sync(kAll, got, j);
+      if (lane - j == from) mine = j < a.top_k ? here : -1;
+      todo &= ~((W == 32 ? kAll : (1u << W) - 1u) << from);
+    }
+    const bool on = there && mine >= 0;
+    const float ml = on ? load(a, row, mine) : -INFINITY;
+    float w;
+    if (a.softmax) {
+      // relative to the largest logit: of the chosen ones where the weights are renormalised (the other
+      // terms cancel), else of all. A row with a NaN or +inf has no softmax.
+      const float top = a.renormalise ? lanes_max(ml, W) : r.m;
+      w = on ? ex2((ml - top) * kLog2e) : 0.0f;
+      const float z = a.renormalise ? lanes_sum(w, W) : r.z;
+      w = on ? __fdividef(w, z) * a.scale : 0.0f;
+      if (r.bad && on) w = __uint_as_float(0x7FC00000u);
+    } else {
+      // s = e^l / (1 + e^l); where all chosen logits are negative, e^(l - max) in its place where the
+      // weights are renormalised: the quotients stay what they are and nothing underflows.
+      const float top = a.renormalise ? fminf(0.0f, lanes_max(ml, W)) : 0.0f;
+      const float e = ex2(-fabsf(ml) * kLog2e);
+      w = !on ? 0.0f : __fdividef(ml >= 0.0f ? 1.0f : top < 0.0f ? ex2((ml - top) * kLog2e) : e, 1.0f + e);
+      if (a.renormalise) w = __fdividef(w, lanes_sum(w, W));
+      w = on ? w * a.scale : 0.0f;
+    }
+    if (j < a.top_k && which < n) {
+      a.index[row * a.top_k + j] = on ? mine : -1;
+      a.weight[row * a.top_k + j] = w;
+      if (a.counts != nullptr && on) atomicAdd(count + mine, 1);
     }
   }
   if (a.counts == nullptr) return;
@@ -521,7 +665,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const Args a) {
 //
 // A warp writes its row whole, with what the chosen experts' entries would be if they had not been
 // chosen, and then the chosen ones' again, a lane each. Bound by what it writes.
-template <int V, bool kSoftmax>
+template <int V>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const Args a) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
@@ -537,16 +681,16 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const Args a) {
     if (on) {
       w = a.weight[row * a.top_k + lane];
       g = a.dweight[row * a.top_k + lane];
-      if (!kSoftmax) ml = load(a, row, mine);
+      if (!a.softmax) ml = load(a, row, mine);
     }
     const float mean = warp_sum(g * w) / a.scale;
     float d = (a.renormalise ? g - mean : g) * w;
-    if (!kSoftmax) d *= 1.0f / (1.0f + expf(ml));  // 1 - s
+    if (!a.softmax) d *= 1.0f / (1.0f + expf(ml));  // 1 - s
     float out[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = 0.0f;
     float rest = 0.0f;  // what the lane's expert would have if it were not chosen
-    if (kSoftmax && !a.renormalise && __any_sync(kAll, on)) {
+    if (a.softmax && !a.renormalise && __any_sync(kAll, on)) {
       float m, z = 0.0f;
       load_row<V>(a, row, first, out);
       m = out[0];
@@ -631,21 +775,36 @@ Args args_of(const zopt_route_job& c) {
   a.tokens = c.tokens;
   a.experts = c.experts, a.top_k = c.top_k, a.groups = c.groups, a.top_groups = c.top_groups;
   a.per_group = Divisor(static_cast<uint32_t>(c.experts / c.groups));
+  a.softmax = c.score == ZOPT_SCORE_SOFTMAX;
   a.bf16 = c.dtype == ZOPT_BF16, a.renormalise = c.renormalise;
   a.scale = c.scale;
   return a;
 }
 
+// Rows of a warp at a time: as many as its lanes hold the choices of, but not so many that fewer than 16
+// warps an SM have some.
 template <int V>
-zopt_status launch(Args& a, bool softmax, bool backward, unsigned blocks, cudaStream_t s) {
+zopt_status launch_forward(Args a, int sms, cudaStream_t s) {
+  const uintptr_t size = a.bf16 ? 2 : 4, piece = std::min<uintptr_t>(16, V * size);
+  a.vec = reinterpret_cast<uintptr_t>(a.logits) % piece == 0 && a.ld * size % piece == 0;
+  const int per = static_cast<int>(a.per_group.d), lanes = per / V;
+  a.lanes_per_group = per % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  for (a.width = 1; a.width < a.top_k;) a.width *= 2;
+  a.rows = static_cast<int>(std::max<long long>(1, std::min<long long>(32 / a.width, a.tokens / (16LL * sms))));
+  const auto kernel = a.bias == nullptr && a.groups == 1 ? forward_kernel<V, true> : forward_kernel<V, false>;
+  const long long rows = static_cast<long long>(kWarps) * a.rows;
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((a.tokens + rows - 1) / rows, 8LL * sms));
+  a.alone = blocks == 1;
+  if (a.counts != nullptr && !a.alone) ZOPT_CUDA_TRY(cudaMemsetAsync(a.counts, 0, sizeof(int32_t) * a.experts, s));
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, s, a);
+}
+template <int V>
+zopt_status launch_backward(Args a, int sms, cudaStream_t s) {
   const uintptr_t size = a.bf16 ? 2 : 4, piece = std::min<uintptr_t>(16, V * size);
   a.vec = reinterpret_cast<uintptr_t>(a.logits) % piece == 0 && a.ld * size % piece == 0;
   a.vec_d = reinterpret_cast<uintptr_t>(a.dlogits) % piece == 0 && a.ld_d * size % piece == 0;
-  const int per = static_cast<int>(a.per_group.d), lanes = per / V;
-  a.lanes_per_group = per % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-  const auto kernel = backward ? (softmax ? backward_kernel<V, true> : backward_kernel<V, false>)
-                               : (softmax ? forward_kernel<V, true> : forward_kernel<V, false>);
-  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), 0, s, a);
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((a.tokens + kWarps - 1) / kWarps, 8LL * sms));
+  return launch_pdl(backward_kernel<V>, dim3(blocks), dim3(kThreads), 0, s, a);
 }
 
 zopt_status run(const char* fn, const zopt_route_job* cp, bool backward, cudaStream_t s) {
@@ -659,17 +818,20 @@ zopt_status run(const char* fn, const zopt_route_job* cp, bool backward, cudaStr
   }
   const int sms = sm_count();
   if (sms < 1) return fail(ZOPT_ECUDA, std::string(fn) + ": no CUDA device");
-  const unsigned blocks = static_cast<unsigned>(std::min<long long>((c.tokens + kWarps - 1) / kWarps, 8LL * sms));
-  a.alone = blocks == 1;
-  if (!backward && c.counts != nullptr && !a.alone) ZOPT_CUDA_TRY(cudaMemsetAsync(c.counts, 0, sizeof(int32_t) * c.experts, s));
-  const bool softmax = c.score == ZOPT_SCORE_SOFTMAX;
-  const int v = (c.experts + 31) / 32;
-  return v <= 1   ? launch<1>(a, softmax, backward, blocks, s)
-         : v <= 2 ? launch<2>(a, softmax, backward, blocks, s)
-         : v <= 4 ? launch<4>(a, softmax, backward, blocks, s)
-         : v <= 8 ? launch<8>(a, softmax, backward, blocks, s)
-         : v <= 16 ? launch<16>(a, softmax, backward, blocks, s)
-                   : launch<32>(a, softmax, backward, blocks, s);
+  const int e = c.experts;
+  if (backward) {
+    return e <= 32    ? launch_backward<1>(a, sms, s)
+           : e <= 64  ? launch_backward<2>(a, sms, s)
+           : e <= 128 ? launch_backward<4>(a, sms, s)
+           : e <= 256 ? launch_backward<8>(a, sms, s)
+                      : launch_backward<32>(a, sms, s);
+  }
+  return e <= 32    ? launch_forward<1>(a, sms, s)
+         : e <= 64  ? launch_forward<2>(a, sms, s)
+         : e <= 128 ? launch_forward<4>(a, sms, s)
+         : e <= 256 ? launch_forward<8>(a, sms, s)
+         : e <= 512 ? launch_forward<16>(a, sms, s)
+                    : launch_forward<32>(a, sms, s);
 }
 
 }  // namespace
