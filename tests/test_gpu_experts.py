@@ -429,3 +429,17 @@ def test_refusals(zopt):
         zopt.experts_forward(**args(ws=ws[:1024]))
     with pytest.raises(zopt.ZoptError, match="kept"):
         zopt.experts_backward(b.dy, b.x, b.index, b.weight, None, b.wgu, b.wd, b.x.clone(), b.weight.clone(), b.wgu.clone(), b.wd.clone(), ws)
+
+
+@pytest.mark.parametrize("case", [(1, 264, 300, 6, 6, "silu", "e4m3", 0), (2, 2056, 40, 5, 3, "gelu", "bf16", 0), (5, 33, 129, 7, 3, "silu", "e4m3", 1),
+                                  (8, 100, 47, 3, 2, "gelu", "bf16", 2), (16, 72, 264, 4, 1, "silu", "bf16", 3), (4, 520, 128, 9, 4, "silu", "e4m3", 0)])
+@pytest.mark.parametrize("extra", [0, 3])
+def test_a_few_slots(zopt, case, extra):
+    """At most 16 slots: sums of weight rows, one slot's after another's."""
+    b = Block(*case, extra=extra, seed=13)
+    b.forward(zopt)
+    b.backward(zopt)
+    b.check(zopt)
+    y = b.y.clone()
+    b.forward(zopt)
+    assert torch.equal(y, b.y)

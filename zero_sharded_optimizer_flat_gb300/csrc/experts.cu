@@ -8,6 +8,7 @@
 //   backward:  x's and dy's rows copied; dh, whose epilogue reads the kept gate and up and writes dgate,
 //              dup, h and the parts of dweight; dx's parts, dgate_up and ddown in one launch; every
 //              token's parts added up.
+// (A forward of a few slots takes experts_few.cu.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -17,6 +18,7 @@
 
 #include "act8.cuh"
 #include "act8_host.h"
+#include "experts_few.h"
 #include "experts_gemm.h"
 #include "guarded.h"
 #include "launch.cuh"
@@ -309,8 +311,9 @@ struct Layout {
   long long dp, fp, gp;  // dim, hidden and 2 hidden rounded up to 8
   long long slots, rows, tiles;
   bool stage_gate, stage_up, stage_down;
-  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, total;
+  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, few_gate_up, few_y, total;
   int dot_parts;
+  bool few;
 };
 
 size_t take(size_t& at, long long bytes) {
@@ -371,6 +374,15 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   p.total = at;
   if (p.stage_up) p.up = take(p.total, E * D * p.fp * 2);
   p.parts = p.xs;  // the forward's y parts, when x has been read
+  p.few = few::takes(c);
+  if (p.few) {
+    long long gate_up, y;
+    few::partial_elems(c, &gate_up, &y);
+    size_t end = 0;
+    p.few_gate_up = take(end, gate_up * 4);
+    p.few_y = take(end, y * 4);
+    p.total = end;
+  }
   if (!backward) return p;
   p.dys = take(at, p.rows * p.dp * 2);
   p.dgu = take(at, p.rows * p.gp * 2);
@@ -541,6 +553,7 @@ struct Call {
   }
 
   zopt_status forward() const {
+    if (p.few) return few::experts_forward(c, at<float>(p.few_gate_up), at<float>(p.few_y), s);
     Weights w;
     TRY(plan());
     TRY(gather(false));
