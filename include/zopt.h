@@ -713,10 +713,10 @@ ZOPT_API zopt_status zopt_route_backward(const zopt_route_job* job, zopt_stream 
  * share), and the parts are added in fp32 in the order of the slots. kept and kept8 have a row for every slot, row t top_k + j. Experts' matrices lie stride_*
  * elements apart (any distance that keeps them apart). Rows that the TMA cannot read in place (ld or
  * stride not a multiple of 8 elements; the forward's up columns where F is not) are copied into the
- * workspace first. A forward of at most 16 slots runs on the CUDA cores instead, which read the weights in
- * place and keep h and the parts in fp32: a token's y may differ there from its y in a larger batch by
- * their roundings. Outputs must not overlap inputs or each other. Repeated on the same inputs a call
- * gives the same bits.
+ * workspace first. A forward of a few slots (at most 64, fewer where the weights are large) runs on the
+ * CUDA cores instead, which read the weights in place and keep h and the parts in fp32: a token's y may
+ * differ there from its y in a larger batch by their roundings. Outputs must not overlap inputs or each
+ * other. Repeated on the same inputs a call gives the same bits.
  * ====================================================================================== */
 typedef struct zopt_experts_job {
   int64_t tokens, dim, hidden;

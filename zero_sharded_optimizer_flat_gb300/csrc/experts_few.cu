@@ -2,10 +2,10 @@
 //
 // As ffn_few.cu has it for a dense block, a slot in a token's place: nothing has to be sorted, each
 // slot's products are sums of its expert's weight rows on the CUDA cores, in fp32 throughout.
-//   1. gate and up:  partial[s][slot] = x[k in s] gate_up[k in s];
-//   2. down: a CTA adds up the parts of its 128 hidden columns (one 8-bit block), forms h with the
-//      slot's weight (and keeps what is to be kept), and writes partial[block][slot] = h[block] down[block];
-//      its weights are on their way to L2 while it waits for the first launch;
+//   1. gate and up:  partial[s][slot] = x[k in s] gate_up[k in s]; its CTAs also bring the slots' down
+//      matrices to L2, so that HBM has all the call's bytes to fetch from the start;
+//   2. down: a CTA adds up the parts of its 256 hidden columns (two 8-bit blocks), forms h with the
+//      slot's weight (and keeps what is to be kept), and writes partial[slot][part] = h[part] down[part];
 //   3. y = the sum of a token's slots' parts.
 // Everything is added in a fixed order. A slot without an expert reads and writes nothing. An expert that
 // several slots name is read for each, from L2 as a rule.
@@ -26,6 +26,9 @@ namespace zopt {
 namespace few {
 namespace {
 
+constexpr long long kFewSlots = 64;
+constexpr int kParts = 2, kHidden = kParts * kBlock;  // of the hidden columns: a CTA's of the second launch
+
 struct Slots {
   const int32_t* index;
   const float* weight;
@@ -38,8 +41,9 @@ __device__ __forceinline__ int expert_of(const Slots& s, int slot) {
   return e >= 0 && e < s.experts ? e : -1;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) expert_gate_up_kernel(Matrix m, long long stride, const Slots slots, const uint16_t* x,
-                                                                     long long ld_x, int share, float* partial) {
+__global__ void __launch_bounds__(kThreads, 2) expert_gate_up_kernel(Matrix m, long long stride, const Matrix down, long long down_stride,
+                                                                     const Slots slots, const uint16_t* x, long long ld_x, int share,
+                                                                     float* partial) {
   extern __shared__ float red[];  // [kWarps][kCols]
   __shared__ float xs[kRows];
   // Whatever wrote the weights, x or the routing has ended before the launch that follows may start.
@@ -52,6 +56,12 @@ __global__ void __launch_bounds__(kThreads, 2) expert_gate_up_kernel(Matrix m, l
   const long long n0 = static_cast<long long>(blockIdx.x) * kCols, col = n0 + 8 * lane;
   const long long k0 = static_cast<long long>(blockIdx.y) * share, k1 = min(m.rows, k0 + share);
   const __nv_bfloat16* const row = reinterpret_cast<const __nv_bfloat16*>(x) + slot / slots.top_k * ld_x;
+  {  // this CTA's share of the down matrix's 128-byte lines
+    const long long lines = (down.cols + 63) / 64, all = down.rows * lines, ctas = static_cast<long long>(gridDim.x) * gridDim.y;
+    const long long cta = static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x;
+    for (long long i = cta * kThreads + threadIdx.x; i < all; i += ctas * kThreads)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(down.w + e * down_stride + i / lines * down.ld + i % lines * 64));
+  }
   F2 acc[1][4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) acc[0][q] = f2(0.0f, 0.0f);
@@ -69,22 +79,20 @@ template <int kAct>
 __global__ void __launch_bounds__(kThreads, 2) expert_down_kernel(Matrix m, long long stride, const Slots slots, const float* parts,
                                                                   int splits, const Keep keep, float* partial) {
   extern __shared__ float red[];  // [kWarps][kCols]
-  __shared__ float hs[kBlock];
-  __shared__ float top[2][4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = blockIdx.z;
-  const int e = expert_of(slots, slot);  // (written before the launch before this one began its work)
-  const long long n0 = static_cast<long long>(blockIdx.x) * kCols, col = n0 + 8 * lane;
-  const long long F = m.rows, k0 = static_cast<long long>(blockIdx.y) * kBlock;
-  const int n = static_cast<int>(min(static_cast<long long>(kBlock), F - k0));
-  const int i = threadIdx.x & 127, group = threadIdx.x >> 7;
-  if (e >= 0) m.w += e * stride;
-  if (e >= 0 && i < n && n0 + 64 * group < m.cols)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(m.w + (k0 + i) * m.ld + n0 + 64 * group));
+  __shared__ float hs[kHidden];
+  __shared__ float top[2][4 * kParts];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = blockIdx.z;
+  const int e = expert_of(slots, slot);
   if (e < 0) return;
-  const long long f = k0 + i, all = static_cast<long long>(gridDim.z) * 2 * F;
-  if (group == 0) {
+  m.w += e * stride;
+  const long long n0 = static_cast<long long>(blockIdx.x) * kCols, col = n0 + 8 * lane;
+  const long long F = m.rows, k0 = static_cast<long long>(blockIdx.y) * kHidden;
+  const int n = static_cast<int>(min(static_cast<long long>(kHidden), F - k0));
+  const int i = threadIdx.x, part = i / kBlock;  // a hidden column each; a block's 128 threads
+  if (part < kParts) {
+    const long long f = k0 + i, all = static_cast<long long>(gridDim.z) * 2 * F;
     const bool in = i < n;
     float g = 0.0f, u = 0.0f;
     if (in) {
@@ -108,18 +116,19 @@ __global__ void __launch_bounds__(kThreads, 2) expert_down_kernel(Matrix m, long
         b = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, d));
       }
       if (lane == 0) top[0][warp] = a, top[1][warp] = b;
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // (this group's four warps)
-      const uint32_t eg = act8::exponent_byte(fmaxf(fmaxf(top[0][0], top[0][1]), fmaxf(top[0][2], top[0][3])));
-      const uint32_t eu = act8::exponent_byte(fmaxf(fmaxf(top[1][0], top[1][1]), fmaxf(top[1][2], top[1][3])));
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");  // (the block's four warps)
+      const float *x = top[0] + 4 * part, *z = top[1] + 4 * part;
+      const uint32_t eg = act8::exponent_byte(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+      const uint32_t eu = act8::exponent_byte(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
       if (in) {
         uint8_t* q = static_cast<uint8_t*>(keep.kept) + slot * keep.ld + f;
         q[0] = static_cast<uint8_t>(act8::encode2(g, 0.0f, act8::inv_scale(eg)) & 255u);
         q[F] = static_cast<uint8_t>(act8::encode2(u, 0.0f, act8::inv_scale(eu)) & 255u);
-      }
-      if (i == 0) {
-        const long long nb = act8::blocks_of(F);
-        keep.scale[slot * 2 * nb + blockIdx.y] = static_cast<uint8_t>(eg);
-        keep.scale[slot * 2 * nb + nb + blockIdx.y] = static_cast<uint8_t>(eu);
+        if (i % kBlock == 0) {
+          const long long nb = act8::blocks_of(F), block = blockIdx.y * kParts + part;
+          keep.scale[slot * 2 * nb + block] = static_cast<uint8_t>(eg);
+          keep.scale[slot * 2 * nb + nb + block] = static_cast<uint8_t>(eu);
+        }
       }
     }
     float phi = g;
@@ -134,27 +143,27 @@ __global__ void __launch_bounds__(kThreads, 2) expert_down_kernel(Matrix m, long
 #pragma unroll
   for (int q = 0; q < 4; ++q) acc[0][q] = f2(0.0f, 0.0f);
   add_rows<1>(m, k0, n, col, hs, warp, acc);
-  join_warps<1>(acc, red, 1, n0, m.cols, partial + (static_cast<long long>(blockIdx.y) * gridDim.z + slot) * m.cols, warp, lane);
+  join_warps<1>(acc, red, 1, n0, m.cols, partial + (static_cast<long long>(slot) * gridDim.y + blockIdx.y) * m.cols, warp, lane);
 }
 
 // y[t][c] = the sum of its slots' parts: 32 columns a CTA, its eight warps taking every eighth part.
-__global__ void __launch_bounds__(256) expert_y_kernel(const float* partial, int blocks, const Slots slots, long long cols, uint16_t* y,
+__global__ void __launch_bounds__(256) expert_y_kernel(const float* partial, int parts, const Slots slots, long long cols, uint16_t* y,
                                                        long long ld_y) {
   __shared__ float red[8][32];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y, first = t * slots.top_k, all = gridDim.y * slots.top_k;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y, first = t * slots.top_k;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
   const int index = lane < slots.top_k ? slots.index[first + lane] : -1;
   const unsigned on = __ballot_sync(0xFFFFFFFFu, index >= 0 && index < slots.experts);
   const bool bad = __any_sync(0xFFFFFFFFu, index != -1 && !(index >= 0 && index < slots.experts));
   float s = 0.0f;
   if (c < cols) {
-    for (int j = 0; j < slots.top_k; ++j) {
-      if (((on >> j) & 1u) == 0) continue;
+    const float* const p = partial + static_cast<long long>(first) * parts * cols + c;
+    const int all = slots.top_k * parts;
 #pragma unroll 8
-      for (int b = warp; b < blocks; b += 8) s += __ldcg(partial + (static_cast<long long>(b) * all + first + j) * cols + c);
-    }
+    for (int q = warp; q < all; q += 8)
+      if ((on >> (q / parts)) & 1u) s += __ldcg(p + q * cols);
   }
   red[warp][lane] = s;
   __syncthreads();
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(256) expert_y_kernel(const float* partial, int
 }
 
 struct ExpertPlan {
-  int slots, groups, splits, share, blocks, y_groups;
+  int slots, groups, splits, share, parts, y_groups;
 };
 ExpertPlan plan_of(const zopt_experts_job& c) {
   ExpertPlan p;
@@ -177,23 +186,39 @@ ExpertPlan plan_of(const zopt_experts_job& c) {
   const long long want = std::min<long long>(std::max<long long>(1, 304LL / (static_cast<long long>(p.groups) * p.slots)), most);
   p.share = static_cast<int>((c.dim + want - 1) / want);
   p.splits = static_cast<int>((c.dim + p.share - 1) / p.share);
-  p.blocks = static_cast<int>((c.hidden + kBlock - 1) / kBlock);
+  p.parts = static_cast<int>((c.hidden + kHidden - 1) / kHidden);
   p.y_groups = static_cast<int>((c.dim + kCols - 1) / kCols);
   return p;
 }
 
 }  // namespace
 
+// By an estimate of both paths' times, in us, the weights of a slot being W MB and `used` the experts that so
+// many slots name where they choose at random: this path 17 + W (0.14 used + 0.08 slots), twice and more
+// of that where the weights' rows do not start on 16 bytes; the tensor cores 40 + 0.18 W used, and 0.36 W
+// for every expert that is copied because the TMA cannot read it in place. (This path against the other,
+// from a cold L2: 2048 x 1408 of 64 experts, 6 slots 34 for 55, 24 82 for 106, 32 115 for 111, 64 200 for 142;
+// 2048 x 5632 of 8, 8 slots 124 for 131, 12 153 for 129; 256 x 768 of 8, 64 slots 24 for 32; 1000 x 683 of 12,
+// 24 slots 42 for 65, 64 108 for 66.)
 bool takes(const zopt_experts_job& c) {
-  if (c.tokens < 1 || c.tokens * c.top_k > 16) return false;
+  const long long slots = c.tokens * c.top_k;
+  if (c.tokens < 1 || slots > kFewSlots) return false;
   const ExpertPlan p = plan_of(c);
-  return p.splits <= 65535 && p.blocks <= 65535;  // (a grid's second dimension)
+  if (p.splits > 65535 || p.parts > 65535) return false;  // (a grid's second dimension)
+  const bool in_place = c.ld_gate_up % 8 == 0 && c.ld_down % 8 == 0 && c.hidden % 8 == 0 &&
+                        (c.experts == 1 || (c.stride_gate_up % 8 == 0 && c.stride_down % 8 == 0));
+  const double mb = 6e-6 * static_cast<double>(c.dim) * static_cast<double>(c.hidden);
+  double missed = 1.0;  // an expert's chance not to be named
+  for (long long i = 0; i < slots; ++i) missed *= 1.0 - 1.0 / c.experts;
+  const double used = std::max<double>(std::min(c.top_k, c.experts), c.experts * (1.0 - missed));
+  return 17.0 + (in_place ? 1.0 : 2.2) * mb * (0.14 * used + 0.08 * static_cast<double>(slots)) <=
+         40.0 + mb * (0.18 * used + (in_place ? 0.0 : 0.36 * c.experts));
 }
 
 void partial_elems(const zopt_experts_job& c, long long* gate_up, long long* y) {
   const ExpertPlan p = plan_of(c);
   *gate_up = static_cast<long long>(p.splits) * p.slots * 2 * c.hidden;
-  *y = static_cast<long long>(p.blocks) * p.slots * c.dim;
+  *y = static_cast<long long>(p.parts) * p.slots * c.dim;
 }
 
 zopt_status experts_forward(const zopt_experts_job& c, float* gate_up, float* y, cudaStream_t s) {
@@ -201,8 +226,9 @@ zopt_status experts_forward(const zopt_experts_job& c, float* gate_up, float* y,
   constexpr size_t smem = static_cast<size_t>(kWarps) * kCols * 4;  // 16 KiB
   const Slots slots{c.index, c.weight, c.experts, c.top_k};
   const Matrix gu{c.w_gate_up, c.ld_gate_up, c.dim, 2 * c.hidden, c.ld_gate_up % 8 == 0 && (c.experts == 1 || c.stride_gate_up % 8 == 0)};
+  const Matrix d{c.w_down, c.ld_down, c.hidden, c.dim, c.ld_down % 8 == 0 && (c.experts == 1 || c.stride_down % 8 == 0)};
   zopt_status st = launch_pdl(expert_gate_up_kernel, dim3(p.groups, p.splits, p.slots), dim3(kThreads), smem, s, gu,
-                              static_cast<long long>(c.stride_gate_up), slots, c.x, static_cast<long long>(c.ld_x), p.share, gate_up);
+                              static_cast<long long>(c.stride_gate_up), d, static_cast<long long>(c.stride_down), slots, c.x, static_cast<long long>(c.ld_x), p.share, gate_up);
   if (st != ZOPT_OK) return st;
   Keep k{};
   if (c.kept8 != nullptr) {
@@ -210,13 +236,12 @@ zopt_status experts_forward(const zopt_experts_job& c, float* gate_up, float* y,
   } else if (c.kept != nullptr) {
     k = Keep{1, c.kept, c.ld_kept, nullptr};
   }
-  const Matrix d{c.w_down, c.ld_down, c.hidden, c.dim, c.ld_down % 8 == 0 && (c.experts == 1 || c.stride_down % 8 == 0)};
   const auto kernel = c.act == ZOPT_ACT_GELU ? expert_down_kernel<ZOPT_ACT_GELU> : expert_down_kernel<ZOPT_ACT_SILU>;
-  st = launch_pdl(kernel, dim3(p.y_groups, p.blocks, p.slots), dim3(kThreads), smem, s, d, static_cast<long long>(c.stride_down), slots,
+  st = launch_pdl(kernel, dim3(p.y_groups, p.parts, p.slots), dim3(kThreads), smem, s, d, static_cast<long long>(c.stride_down), slots,
                   static_cast<const float*>(gate_up), p.splits, k, y);
   if (st != ZOPT_OK) return st;
   return launch_pdl(expert_y_kernel, dim3(static_cast<unsigned>((c.dim + 31) / 32), static_cast<unsigned>(c.tokens)), dim3(256), 0, s,
-                    static_cast<const float*>(y), p.blocks, slots, static_cast<long long>(c.dim), c.y, static_cast<long long>(c.ld_y));
+                    static_cast<const float*>(y), p.parts, slots, static_cast<long long>(c.dim), c.y, static_cast<long long>(c.ld_y));
 }
 
 }  // namespace few
