@@ -128,7 +128,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
     mine[e] = first + before;
     if (rank == 0) a.info[e] = make_int2(first, all);
     for (int i = static_cast<int>(rank); i < tiles; i += kPlanCtas)
-      a.tiles[first_tile + i] = make_int4(e, first + i * kTileM, first + rows, 0);
+      a.tiles[first_tile + i] = make_int4(e, first + i * kTileM, first + rows, all - i * kTileM <= kTileM / 2 ? 1 : 0);
     for (int i = all + static_cast<int>(rank); i < rows; i += kPlanCtas) a.row[first + i] = make_int2(-1, 0);
   }
   __syncthreads();
@@ -387,9 +387,7 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   p.dys = take(at, p.rows * p.dp * 2);
   p.dgu = take(at, p.rows * p.gp * 2);
   p.parts = take(at, p.rows * p.dp * 2);
-  Job j;
-  group_job(j, p, kGluBwd, false, 0, F, D, c.experts);
-  p.dot_parts = 2 * j.tiles_n;
+  p.dot_parts = static_cast<int>((F + 63) / 64);
   p.dots = take(at, 4 * p.rows * p.dot_parts);
   p.total = std::max(p.total, at);
   return p;
@@ -566,7 +564,7 @@ struct Call {
       group_job(j, p, kGluFwd, false, 0, F, D, c.experts);
       j.b_mn = 1;
       glu(j);
-      TRY(map_rows(fn, j, &j.P, at<uint16_t>(p.xs), p.rows, D, p.dp, 0, 128));
+      TRY(map_rows(fn, j, &j.P, at<uint16_t>(p.xs), p.rows, D, p.dp, 0, 64));
       TRY(map_weights(fn, j, &j.Q, w.gate, D, F, w.pg, c.experts, w.sg, 1, 0));
       TRY(map_weights(fn, j, &j.Up, w.up, D, F, w.pu, c.experts, w.su, 1, 0));
       j.out = at<uint16_t>(p.h);
@@ -578,7 +576,7 @@ struct Call {
     Job& j = b.job[0];
     group_job(j, p, kStore, false, 0, D, F, c.experts);
     j.b_mn = 1;
-    TRY(map_rows(fn, j, &j.P, at<uint16_t>(p.h), p.rows, F, p.fp, 0, 128));
+    TRY(map_rows(fn, j, &j.P, at<uint16_t>(p.h), p.rows, F, p.fp, 0, 64));
     TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 1, 0));
     parts(j);
     TRY(launch_grouped(fn, b, kStore, p.tiles, s));
@@ -599,7 +597,7 @@ struct Call {
       Job& j = b.job[0];
       group_job(j, p, kGluBwd, false, 0, F, D, c.experts);
       glu(j);
-      TRY(map_rows(fn, j, &j.P, dys, p.rows, D, p.dp, 0, 128));
+      TRY(map_rows(fn, j, &j.P, dys, p.rows, D, p.dp, 0, 64));
       TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 0, j.tile_n / 2));
       j.out = dgu, j.ld_out = p.gp;
       j.out_h = h, j.ld_h = p.fp;
@@ -611,7 +609,7 @@ struct Call {
     {
       Job& j = b.job[0];  // dx's parts
       group_job(j, p, kStore, false, 0, D, 2 * F, c.experts);
-      TRY(map_rows(fn, j, &j.P, dgu, p.rows, 2 * F, p.gp, 0, 128));
+      TRY(map_rows(fn, j, &j.P, dgu, p.rows, 2 * F, p.gp, 0, 64));
       TRY(map_weights(fn, j, &j.Q, w.gate, D, 2 * F, w.pg, c.experts, w.sg, 0, j.tile_n / 2));
       parts(j);
     }

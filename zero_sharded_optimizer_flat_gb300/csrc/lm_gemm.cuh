@@ -29,7 +29,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kFirstEpi = 3;  // warp 0 loads P, warp 1 issues the MMAs, warp 2 loads Q, warps 3 .. 10 epilogue
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kBoxBytes = 32 * 128;  // an epilogue warp's results on their way to memory: 32 rows of 128 bytes
-constexpr int kSwapBytes = 4 * 64 * 2;  // kGluFwd: two warps' block exponents for each quarter of the rows
+constexpr int kSwapBytes = 2 * 4 * 64 * 2;  // kGluFwd: the warps' block exponents, of tiles of 256 rows and of 128
 constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxBytes + kSwapBytes + 1024 + 256;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr int kMaxJobs = 3;
@@ -95,7 +95,7 @@ struct Job {
   int by_inner;          // the experts' rows are the inner length (else the rows of D)
   long long out_stride;  // by_inner: elements between the experts' D
   float* part_scale;     // kStore by rows: D is fp16 in units of powers of two, at [64 columns][row]
-  float* dots;           // kGluBwd: the parts of dh . h, at [2 tile column + half][row]
+  float* dots;           // kGluBwd: the parts of dh . h, at [64 columns][row]
   long long rows_ld;     // what these two's rows of rows are apart
 };
 
@@ -104,7 +104,7 @@ struct Job {
 // not known before the tokens have chosen is read from device memory.
 struct Groups {
   const int* head;    // [0] row tiles, [1] rows
-  const int4* tiles;  // a row tile's expert, first row, and where its expert's rows (with the zeros) end
+  const int4* tiles;  // a row tile's expert, first row, where its expert's rows (with the zeros) end, and 1 for at most 128 rows
   const int2* info;   // an expert's first row and its number of rows (without the zeros)
   const int2* row;    // a row's slot (-1: zeros) and its weight's bits
   int experts;

@@ -246,7 +246,23 @@ struct Unit {
   int tj, split, kb0, kb1;
   int row0, rows;    // the tile's first row, and where the rows of D end
   int expert, krow;  // grouped: whose matrices; by_inner: the row of both operands that k = 0 is
+  bool half;         // grouped: a tile of at most 128 rows
 };
+// A warp's part of a tile: its first row, and its columns (kGluFwd: hidden ones) in the accumulator and in D.
+//
+// A tile of 256 rows gives each CTA 128, a TMEM lane each, and all columns (the pair's MMA with M = 256); one
+// of 128 rows gives each CTA 64, whose first half of the columns lies in lanes 0 .. 63 and whose second in
+// lanes 64 .. 127 (M = 128), in half the accumulator's columns and half the time.
+struct Part {
+  int row0, tcol, col, width;
+};
+template <bool kGrouped>
+__device__ __forceinline__ Part part_of_tile(const Unit& w, int width, uint32_t rank, int quad, int h) {
+  if (kGrouped && w.half)
+    return Part{w.row0 + static_cast<int>(rank) * 64 + 32 * (quad & 1), (width >> 2) * h,
+                w.tj * width + (width >> 1) * (quad >> 1) + (width >> 2) * h, width >> 2};
+  return Part{w.row0 + static_cast<int>(rank) * 128 + 32 * quad, (width >> 1) * h, w.tj * width + (width >> 1) * h, width >> 1};
+}
 template <bool kGrouped>
 __device__ __forceinline__ Unit unit_of(const Batch& B, const Job& j, int u) {
   Unit w;
@@ -256,6 +272,7 @@ __device__ __forceinline__ Unit unit_of(const Batch& B, const Job& j, int u) {
     w.tj = u - line * j.tiles_n;
     w.split = 0, w.kb0 = 0, w.kb1 = j.nk;
     w.expert = t.x, w.row0 = t.y, w.rows = t.z, w.krow = 0;
+    w.half = t.w != 0;
     return w;
   }
   w.split = static_cast<int>(j.per_split(static_cast<uint32_t>(u)));
@@ -265,6 +282,7 @@ __device__ __forceinline__ Unit unit_of(const Batch& B, const Job& j, int u) {
   w.tj = j.rows_fast ? line : at;
   w.row0 = ti * kTileM, w.rows = j.M;
   w.expert = 0, w.krow = 0;
+  w.half = false;
   if (kGrouped) {
     const int2 e = __ldcg(B.groups.info + w.split);
     w.expert = w.split, w.split = 0;
@@ -491,22 +509,21 @@ __device__ __forceinline__ float half_words(const uint32_t (&v)[2][32], uint32_t
 }
 
 template <bool kGrouped>
-__device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Acc& acc, int row0, int lane, int h,
-                                          uint32_t box) {
-  const int row = row0 + lane;
+__device__ __forceinline__ void epi_store(const Job& j, const Unit& w, const Part& part, const Acc& acc, int lane, uint32_t box) {
+  const int row0 = part.row0, row = row0 + lane;
   const float alpha = !kGrouped && j.alpha != nullptr && j.splits == 1 ? __ldcg(j.alpha) : 1.0f;
   const bool wide = !kGrouped && j.out_mode == kOutF32;
-  const int width = j.tile_n >> 1;
+  const int width = part.width;
   void* const first = kGrouped ? static_cast<void*>(static_cast<uint16_t*>(j.out) + w.expert * j.out_stride)
                       : wide   ? static_cast<void*>(static_cast<float*>(j.out) + w.split * j.split_stride)
                                : j.out;
-  const Out<128> out(first, j.ld_out, wide ? 4 : 2, row0, w.rows, w.tj * j.tile_n + width * h, j.N, lane);
+  const Out<128> out(first, j.ld_out, wide ? 4 : 2, row0, w.rows, part.col, j.N, lane);
 #pragma unroll 1
   for (int half = 0; 64 * half < width; ++half) {
     uint32_t v[2][32];
-    acc.read64(width * h + 64 * half, v);
+    acc.read64(part.tcol + 64 * half, v);
     if (64 * half + 64 == width) acc.done();
-    const int col0 = w.tj * j.tile_n + width * h + 64 * half;
+    const int col0 = part.col + 64 * half;
     if (col0 >= j.N || row0 >= w.rows) continue;  // (warp-uniform)
     if (kGrouped && w.kb1 == 0) {  // a sum of nothing
 #pragma unroll
@@ -667,16 +684,16 @@ __device__ __forceinline__ void epi_ce_bwd(const Job& j, const Unit& w, const Ac
   }
 }
 
-// Whether both of the two warps that share barrier `bar` bring ok. Every lane of both has to come.
-__device__ __forceinline__ bool both_warps(int ok, int bar) {
+// Whether all of the warps (`threads` in all) that share barrier `bar` bring ok. Every lane of them has to come.
+__device__ __forceinline__ bool both_warps(int ok, int bar, int threads) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 64, p;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(ok), "r"(bar)
+      : "r"(ok), "r"(bar), "r"(threads)
       : "memory");
   return r != 0;
 }
@@ -686,55 +703,76 @@ __device__ __forceinline__ bool both_warps(int ok, int bar) {
 // (128): a block's largest magnitude is found within a lane and its partner in the warp that has the
 // other half, through `swap` (two bytes a lane; the two warps share barrier `bar`).
 template <int kAct, int kKept, bool kGrouped>
-__device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const Acc& acc, int row0, const Row& mine, int lane, int h,
-                                            uint32_t box, uint16_t* swap, int bar) {
-  const int width = kKept == kKeep8 ? 128 : j.tile_n >> 1;  // hidden columns of a tile
-  const int row = kGrouped ? mine.slot : row0 + lane, n0 = w.tj * width;
-  if (row0 >= w.rows) {  // (the partner warp has the same rows)
+__device__ __forceinline__ void epi_glu_fwd(const Job& j, const Unit& w, const Part& part, const Acc& acc, const Row& mine, int lane,
+                                            int h, uint32_t box, uint16_t* swap, int quad) {
+  // the gate's columns in the accumulator, and the up's behind them
+  const int row0 = part.row0, count = part.width, up = kGrouped && w.half ? 2 * part.width : (kKept == kKeep8 ? 128 : j.tile_n >> 1);
+  const int row = kGrouped ? mine.slot : row0 + lane;
+  if (row0 >= w.rows) {  // (the partner warps have the same rows)
     acc.done();
     return;
   }
   float inv[2] = {1.0f, 1.0f};
   if constexpr (kKept == kKeep8) {
     uint32_t e[2];
-    uint32_t v[2][32];
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      acc.read64(128 * part + 64 * h, v);
+    for (int p = 0; p < 2; ++p) {
+      uint32_t v[2][32];
       float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const int n = j.hidden - n0 - 64 * h;
-      if (n >= 64) {
+      const int n = j.hidden - part.col;
+      if (kGrouped && w.half) {
+        tc::tmem_ld32(acc.base + static_cast<uint32_t>(up * p + part.tcol), v[0]);
+        tc::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 64; ++k) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
+        for (int k = 0; k < 32; ++k)
+          if (k < n) top[k & 3] = act8::amax_step(top[k & 3], f(v[0][k]));
       } else {
+        acc.read64(128 * p + 64 * h, v);
+        if (n >= 64) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
-          if (k < n) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
+          for (int k = 0; k < 64; ++k) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k < n) top[k & 3] = act8::amax_step(top[k & 3], f(v[k >> 5][k & 31]));
+        }
       }
-      e[part] = act8::exponent_byte(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+      e[p] = act8::exponent_byte(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
     }
-    swap[32 * h + lane] = static_cast<uint16_t>(e[0] | (e[1] << 8));
-    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
-    const uint32_t other = swap[32 * (1 - h) + lane];  // (both_warps comes between this and the next tile's)
-    e[0] = max(e[0], other & 255u), e[1] = max(e[1], other >> 8);  // the byte grows with the magnitude
+    // (both_warps comes between this and the same warps' next; the byte grows with the magnitude)
+    if (kGrouped && w.half) {  // four warps have the block's columns: two quarters' two halves
+      uint16_t* const all = swap - 64 * quad + 256 + 128 * (quad & 1);  // (not where pairs have theirs)
+      all[32 * (2 * (quad >> 1) + h) + lane] = static_cast<uint16_t>(e[0] | (e[1] << 8));
+      asm volatile("bar.sync %0, 128;" ::"r"(5 + (quad & 1)) : "memory");
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t other = all[32 * q + lane];
+        e[0] = max(e[0], other & 255u), e[1] = max(e[1], other >> 8);
+      }
+    } else {
+      swap[32 * h + lane] = static_cast<uint16_t>(e[0] | (e[1] << 8));
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory");
+      const uint32_t other = swap[32 * (1 - h) + lane];
+      e[0] = max(e[0], other & 255u), e[1] = max(e[1], other >> 8);
+    }
     const long long nb = act8::blocks_of(j.hidden);
-    if (kGrouped ? row >= 0 : row < w.rows)
+    if ((kGrouped ? row >= 0 : row < w.rows) && !(kGrouped && w.half && quad >= 2))
       j.kept_scale[static_cast<long long>(row) * 2 * nb + h * nb + w.tj] = static_cast<uint8_t>(h == 0 ? e[0] : e[1]);
     inv[0] = act8::inv_scale(e[0]), inv[1] = act8::inv_scale(e[1]);
   }
   constexpr int kSize = kKept == kKeep8 ? 1 : 2;
-  const int first = n0 + (width >> 1) * h;
+  const int first = part.col;
   const Out<64> out(j.out, j.ld_out, 2, row0, w.rows, first, j.hidden, lane);
   const auto gate_out = part_of<32 * kSize, kGrouped>(j.kept, j.ld_kept, kSize, row0, w.rows, row, first, j.hidden, lane);
   const auto up_out = part_of<32 * kSize, kGrouped>(static_cast<uint8_t*>(j.kept) + static_cast<long long>(j.hidden) * kSize,
                                                     j.ld_kept, kSize, row0, w.rows, row, first, j.hidden, lane);
 #pragma unroll 1
-  for (int c = 0; 64 * c < width; ++c) {
+  for (int c = 0; 32 * c < count; ++c) {
     uint32_t g[32], u[32];
-    tc::tmem_ld32(acc.base + static_cast<uint32_t>((width >> 1) * h + 32 * c), g);
-    tc::tmem_ld32(acc.base + static_cast<uint32_t>(width + (width >> 1) * h + 32 * c), u);
+    tc::tmem_ld32(acc.base + static_cast<uint32_t>(part.tcol + 32 * c), g);
+    tc::tmem_ld32(acc.base + static_cast<uint32_t>(up + part.tcol + 32 * c), u);
     tc::tmem_wait_ld();
-    if (64 * c + 64 >= width) acc.done();
+    if (32 * c + 32 >= count) acc.done();
     if (first + 32 * c >= j.hidden) continue;
     if constexpr (kKept == kKeepBf16) {  // a box: a row's 32 gates, then its 32 ups
       uint32_t words[32];
@@ -909,16 +947,15 @@ struct Scales {
 // tile's first (from row next_row0 and column next_col on): gate and up come from HBM, and a tile that
 // began by waiting for them would take longer than its products.
 // Grouped, dg, du and h carry the row's weight, and the weight's own gradient, the sum over the columns
-// of dh h without it, leaves in parts, one for each half of a tile.
+// of dh h without it, leaves in parts.
 struct Next {  // the tile after this one
   int row0, rows, col;
   Row mine;
 };
 template <int kAct, int kKept, bool kWide, bool kGrouped>
-__device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Acc& acc, int row0, const Row& mine, int lane, int h,
+__device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Part& part, const Acc& acc, const Row& mine, int lane,
                                             uint32_t box, Kept<kKept, kWide, kGrouped>& k, Scales& sc, const Next& n) {
-  const int width = j.tile_n >> 1;
-  const int col0 = w.tj * j.tile_n + width * h;
+  const int row0 = part.row0, width = part.width, col0 = part.col;
   const Out<64> dgate(j.out, j.ld_out, 2, row0, w.rows, col0, j.N, lane);
   const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, w.rows, col0, j.N, lane);
   const Out<64> hout(j.out_h, j.ld_h, 2, row0, w.rows, col0, j.N, lane);
@@ -932,7 +969,7 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const A
     const int col = col0 + 32 * c;
     const bool last = 32 * c + 32 == width;
     uint32_t v[32];
-    acc.read32(width * h + 32 * c, v);
+    acc.read32(part.tcol + 32 * c, v);
     if (last) acc.done();
     Kept<kKept, kWide, kGrouped> next;
     next.load(j, last ? n.row0 : row0, last ? n.rows : w.rows, last ? n.mine.slot : mine.slot, last ? n.col : col + 32, lane);
@@ -975,15 +1012,14 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const A
       hout.template put<0>(box, lane, 64 * c);
       __syncwarp();
     }
+    if (kGrouped && (c & 1) != 0) {  // a part for every 64 columns
+      const float2 two = f2(dot);
+      if (mine.slot >= 0 && col - 32 < j.N) j.dots[static_cast<long long>(col >> 6) * j.rows_ld + row0 + lane] = two.x + two.y;
+      dot = f2(0.0f, 0.0f);
+    }
     k = next;
   }
   sc = next_sc;
-  if constexpr (kGrouped) {
-    if (mine.slot >= 0) {
-      const float2 two = f2(dot);
-      j.dots[(2 * w.tj + h) * j.rows_ld + row0 + lane] = two.x + two.y;
-    }
-  }
 }
 
 // ---------------------------------------------------------------------- the kernel
@@ -1064,12 +1100,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool mn = (is_p ? j.a_mn : j.b_mn) != 0;
         const int width = j.tile_n >> 1;  // this CTA's columns of Q
         // this CTA's first row of P, or column of Q
-        const int first = is_p                        ? w.row0 + static_cast<int>(rank) * 128
-                          : (kKinds & kGluFwd) != 0 ? w.tj * width
+        const bool halved = kGrouped && w.half;
+        const int first = is_p                        ? w.row0 + static_cast<int>(rank) * (halved ? 64 : 128)
+                          : (kKinds & kGluFwd) != 0 ? w.tj * width + (halved ? static_cast<int>(rank) * 64 : 0)
                                                     : w.tj * j.tile_n + static_cast<int>(rank) * width;
         // (a single tile of at most 128 rows: the other rows' accumulators are of no use to anyone)
         const bool any = !is_p || leader || j.a_rows == 128, two = is_p || width == 128;
-        const uint32_t tx = static_cast<uint32_t>(j.tx);
+        const uint32_t tx = static_cast<uint32_t>(halved ? j.tx - 128 * kTileK * 2 : j.tx);
         // (grouped: activations are one matrix of all experts' rows, weights an expert's)
         const int depth = kGrouped && !is_p && !j.by_inner ? w.expert : 0, krow = kGrouped ? w.krow : 0;
         const int k_end = w.kb1 * kTileK;
@@ -1082,6 +1119,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t bar = lead0 + 8 * s, to = s0 + s * kHalfBytes;
           if (!mn) {
             if (any) load_box<kGrouped>(to, map, bar, k, first, depth);
+            if (kGrouped && is_p && !halved) load_box<kGrouped>(to + kMnBoxBytes, map, bar, k, first + 64, depth);
+          } else if ((kKinds & kGluFwd) != 0 && halved) {  // 64 gate and the matching up columns in either CTA
+            load_box<kGrouped>(to, &j.Q, bar, first, krow + k, depth);
+            load_box<kGrouped>(to + kMnBoxBytes, &j.Up, bar, first, krow + k, depth);
           } else {
             load_box<kGrouped>(to, map, bar, first, krow + k, depth);
             if (two) load_box<kGrouped>(to + kMnBoxBytes, map, bar, first + 64, krow + k, depth);
@@ -1111,7 +1152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Job& j = B.job[ji];
         const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
         const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
-        const uint32_t idesc = tc::idesc_bf16_f32(kTileM, j.tile_n, amn, bmn);
+        const uint32_t idesc = tc::idesc_bf16_f32(kGrouped && w.half ? 128 : kTileM, j.tile_n, amn, bmn);
         // a stage's descriptors differ in the address alone (16-byte units), and so do a stage's steps
         const uint64_t ad0 = tc::smem_desc_sw128(tc::smem_u32(sA), amn ? kMnBoxBytes : 16u, 1024u);
         const uint64_t bd0 = tc::smem_desc_sw128(tc::smem_u32(sB), bmn ? kMnBoxBytes : 16u, 1024u);
@@ -1158,7 +1199,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                        tc::map_to_rank(tc::smem_u32(tempty + 1), 0)};
     const uint32_t box = tc::smem_u32(sEpi) + (warp - kFirstEpi) * kBoxBytes;
     uint16_t* swap = sSwap + 64 * quad;
-    const int rows0 = static_cast<int>(rank) * 128 + 32 * quad;  // this warp's rows within a tile
+    // a tile's columns of D (kGluFwd: hidden ones)
+    auto columns = [](const Job& j) { return (kKinds & kGluFwd) == 0 ? j.tile_n : kKept == kKeep8 ? 128 : j.tile_n >> 1; };
     Kept<kKept, kWide, kGrouped> kept;
     Scales scales;
     Row mine{-1, 0.0f};
@@ -1166,8 +1208,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Next n{0, 0, 0, Row{-1, 0.0f}};
       if (t >= total) return n;
       const Unit w = unit_of<kGrouped>(B, B.job[0], t);
-      n.row0 = w.row0 + rows0, n.rows = w.rows;
-      n.col = w.tj * B.job[0].tile_n + (B.job[0].tile_n >> 1) * half;
+      const Part part = part_of_tile<kGrouped>(w, columns(B.job[0]), rank, quad, half);
+      n.row0 = part.row0, n.rows = w.rows, n.col = part.col;
       n.mine = Row::at<kGrouped>(B, n.row0 + lane, n.rows);
       return n;
     };
@@ -1186,7 +1228,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int ji = starts.job(B, t);
       const Job& j = B.job[ji];
       const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
-      const int row0 = w.row0 + rows0;
+      const Part part = part_of_tile<kGrouped>(w, columns(j), rank, quad, half);
+      const int row0 = part.row0;
       Next next{};
       if constexpr ((kKinds & kGluBwd) != 0) next = first_of(unit_at(B, pair, npairs, it));
       if constexpr (kGrouped && (kKinds & kGluFwd) != 0) mine = Row::at<kGrouped>(B, row0 + lane, w.rows);
@@ -1194,20 +1237,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) ok = wait(tc::smem_u32(tfull + b), tph, err) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       // Two warps wait for one another within such a tile: if one's wait has run out, neither begins it.
-      if constexpr ((kKinds & kGluFwd) != 0 && kKept == kKeep8) ok = both_warps(ok, 1 + quad);
+      if constexpr ((kKinds & kGluFwd) != 0 && kKept == kKeep8) ok = kGrouped && w.half ? both_warps(ok, 5 + (quad & 1), 128) : both_warps(ok, 1 + quad, 64);
       if (!ok) {
         if (lane == 0) tell_pair(gave_up);
         break;
       }
       tc::fence_after_sync();
       const Acc acc{tmem + (static_cast<uint32_t>(32 * quad) << 16) + static_cast<uint32_t>(b * kTileN), tempty_leader[b], lane};
-      if ((kKinds & kStore) && j.kind == kStore) epi_store<kGrouped>(j, w, acc, row0, lane, half, box);
+      if ((kKinds & kStore) && j.kind == kStore) epi_store<kGrouped>(j, w, part, acc, lane, box);
       if ((kKinds & kCeFwd) && j.kind == kCeFwd) epi_ce_fwd(j, w, acc, row0, lane, half);
       if ((kKinds & kCeBwd) && j.kind == kCeBwd) epi_ce_bwd(j, w, acc, row0, lane, half, box);
       if constexpr ((kKinds & kGluFwd) != 0)
-        epi_glu_fwd<kAct, kKept, kGrouped>(j, w, acc, row0, mine, lane, half, box, swap, 1 + quad);
+        epi_glu_fwd<kAct, kKept, kGrouped>(j, w, part, acc, mine, lane, half, box, swap, quad);
       if constexpr ((kKinds & kGluBwd) != 0) {
-        epi_glu_bwd<kAct, kKept, kWide, kGrouped>(j, w, acc, row0, mine, lane, half, box, kept, scales, next);
+        epi_glu_bwd<kAct, kKept, kWide, kGrouped>(j, w, part, acc, mine, lane, box, kept, scales, next);
         mine = next.mine;
       }
     }
