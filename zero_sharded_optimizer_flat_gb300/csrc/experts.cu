@@ -38,6 +38,7 @@ constexpr long long kMaxElems = 1LL << 44;  // of any matrix: tile numbers stay 
 // ---------------------------------------------------------------------- the plan
 
 constexpr int kPlanCtas = 8, kPlanWarps = 32;
+constexpr int kPlanKept = 8;  // times 32 slots that a warp keeps in registers
 
 struct PlanArgs {
   const int32_t* index;
@@ -74,10 +75,24 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
   int* const my = count + warp * E;
   for (int e = lane; e < E; e += 32) my[e] = 0;
   __syncwarp();
-  for (long long s = s0; s < s1; s += 32) {
+  int kept[kPlanKept];  // the first of the run's, and which of the 32 are the same
+  unsigned same[kPlanKept];
+#pragma unroll
+  for (int k = 0; k < kPlanKept; ++k) {
+    const long long s = s0 + 32 * k + lane;
+    kept[k] = s < s1 ? __ldg(a.index + s) : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kPlanKept; ++k) {
+    if (s0 + 32 * k >= s1) break;
+    same[k] = __match_any_sync(0xFFFFFFFFu, kept[k]);
+    if (kept[k] >= 0 && kept[k] < E && lane == __ffs(same[k]) - 1) my[kept[k]] += __popc(same[k]);
+    __syncwarp();
+  }
+  for (long long s = s0 + 32 * kPlanKept; s < s1; s += 32) {
     const int e = s + lane < s1 ? a.index[s + lane] : -1;
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, e);
-    if (e >= 0 && e < E && lane == __ffs(same) - 1) my[e] += __popc(same);
+    const unsigned m = __match_any_sync(0xFFFFFFFFu, e);
+    if (e >= 0 && e < E && lane == __ffs(m) - 1) my[e] += __popc(m);
     __syncwarp();
   }
   __syncthreads();
@@ -132,20 +147,29 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
     for (int i = all + static_cast<int>(rank); i < rows; i += kPlanCtas) a.row[first + i] = make_int2(-1, 0);
   }
   __syncthreads();
-  for (long long s = s0; s < s1; s += 32) {
-    const bool in = s + lane < s1;
-    const int x = in ? a.index[s + lane] : -1;
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, x);
+  auto place = [&](long long s, int x, unsigned same, float weight) {  // 32 slots from s on
     const bool on = x >= 0 && x < E;
     int at = x == -1 ? -1 : -2;
     if (on) {
       at = mine[x] + my[x] + __popc(same & ((1u << lane) - 1u));
-      a.row[at] = make_int2(static_cast<int>(s) + lane, __float_as_int(a.weight[s + lane]));
+      a.row[at] = make_int2(static_cast<int>(s) + lane, __float_as_int(weight));
     }
-    if (in) a.row_of[s + lane] = at;
+    if (s + lane < s1) a.row_of[s + lane] = at;
     __syncwarp();
     if (on && lane == __ffs(same) - 1) my[x] += __popc(same);
     __syncwarp();
+  };
+  float weight[kPlanKept];
+#pragma unroll
+  for (int k = 0; k < kPlanKept; ++k) weight[k] = kept[k] >= 0 && kept[k] < E ? __ldg(a.weight + s0 + 32 * k + lane) : 0.0f;
+#pragma unroll
+  for (int k = 0; k < kPlanKept; ++k) {
+    if (s0 + 32 * k >= s1) break;
+    place(s0 + 32 * k, kept[k], same[k], weight[k]);
+  }
+  for (long long s = s0 + 32 * kPlanKept; s < s1; s += 32) {
+    const int x = s + lane < s1 ? a.index[s + lane] : -1;
+    place(s, x, __match_any_sync(0xFFFFFFFFu, x), x >= 0 && x < E ? a.weight[s + lane] : 0.0f);
   }
 }
 
@@ -160,49 +184,67 @@ struct Source {
 struct GatherArgs {
   Source from[2];
   int n;
-  long long cols, pitch;
-  const int* head;
-  const int2* row;
-  Divisor per_token;  // slots
+  long long tokens, cols, pitch;
+  const int* row_of;
+  const int2* info;
+  int top_k, experts;
+  int fill;  // the backward multiplies by the rows that only fill up
 };
 
-// Rows of x (and dy) in the plan's order, zeros where a row only fills up and behind the last column. A
-// warp takes a row; bound by what it writes.
+// 16 bytes of a token's row, zeros behind the last column.
+__device__ __forceinline__ uint4 piece_of(const Source& f, long long cols, long long token, int p) {
+  if (f.x != nullptr) return row_piece8(f.x + token * f.ld + 8 * p, cols - 8 * p);
+  const uint8_t* const q = f.q + token * cols;  // (a piece of eight columns lies in one block of 128)
+  uint32_t w[4];
+  const float power = act8::scale(f.scale[token * act8::blocks_of(cols) + (p >> 4)]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long c = 8 * p + 2 * i;
+    const uint32_t two = (c < cols ? q[c] : 0u) | ((c + 1 < cols ? q[c + 1] : 0u) << 8);
+    const float2 v = act8::decode2(two);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x * power, v.y * power);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows of x (and dy) in the plan's order, zeros behind the last column and (fill) where a row only fills up. A warp
+// reads a token's row, 1024 columns of it at a time, and writes it wherever the token's slots have theirs;
+// bound by what it writes.
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int lane = threadIdx.x & 31, rows = __ldcg(a.head + 1);
-  const int pieces = static_cast<int>(a.pitch / 8);
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8) {
-    const int slot = __ldcg(a.row + r).x;
-    const long long token = slot < 0 ? 0 : a.per_token(static_cast<uint32_t>(slot));
-    for (int k = 0; k < a.n; ++k) {
-      const Source& f = a.from[k];
-      uint16_t* const to = f.to + r * a.pitch;
-      if (slot < 0) {
-        for (int p = lane; p < pieces; p += 32) *reinterpret_cast<uint4*>(to + 8 * p) = make_uint4(0, 0, 0, 0);
-      } else if (f.x != nullptr) {
-        const uint16_t* const s = f.x + token * f.ld;
-#pragma unroll 4
-        for (int p = lane; p < pieces; p += 32) *reinterpret_cast<uint4*>(to + 8 * p) = row_piece8(s + 8 * p, a.cols - 8 * p);
-      } else {  // (a piece of eight columns lies in one block of 128)
-        const uint8_t* const q = f.q + token * a.cols;
-        const uint8_t* const sc = f.scale + token * act8::blocks_of(a.cols);
-        for (int p = lane; p < pieces; p += 32) {
-          uint32_t w[4];
-          const float power = act8::scale(sc[p >> 4]);
+  constexpr int kAtOnce = 4;
+  const int lane = threadIdx.x & 31, warps = gridDim.x * 8, me = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int pieces = static_cast<int>(a.pitch / 8), chunks = (pieces + 32 * kAtOnce - 1) / (32 * kAtOnce);
+  const long long items = a.tokens * a.n * chunks;
+  for (long long i = me; i < items; i += warps) {
+    const long long token = i / (a.n * chunks);
+    const int k = static_cast<int>(i - token * (a.n * chunks)), from = k / chunks, p0 = (k - from * chunks) * 32 * kAtOnce + lane;
+    const int mine = lane < a.top_k ? __ldcg(a.row_of + token * a.top_k + lane) : -1;
+    if (!__any_sync(0xFFFFFFFFu, mine >= 0)) continue;  // (a row that nobody takes is not read)
+    const Source& f = a.from[from];
+    uint4 v[kAtOnce];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const long long c = 8 * p + 2 * i;
-            const uint32_t two = (c < a.cols ? q[c] : 0u) | ((c + 1 < a.cols ? q[c + 1] : 0u) << 8);
-            const float2 v = act8::decode2(two);
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x * power, v.y * power);
-            w[i] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          *reinterpret_cast<uint4*>(to + 8 * p) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+    for (int q = 0; q < kAtOnce; ++q)
+      if (p0 + 32 * q < pieces) v[q] = piece_of(f, a.cols, token, p0 + 32 * q);
+    for (int j = 0; j < a.top_k; ++j) {
+      const int r = __shfl_sync(0xFFFFFFFFu, mine, j);
+      if (r < 0) continue;
+      uint16_t* const to = f.to + r * a.pitch;
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        if (p0 + 32 * q < pieces) *reinterpret_cast<uint4*>(to + 8 * (p0 + 32 * q)) = v[q];
     }
+  }
+  if (!a.fill) return;
+  for (int i = me; i < a.experts * (kGroupRows - 1); i += warps) {  // the rows that only fill up
+    const int e = i / (kGroupRows - 1), k = i - e * (kGroupRows - 1);
+    const int2 at = __ldcg(a.info + e);
+    if (k >= (kGroupRows - at.y % kGroupRows) % kGroupRows) continue;
+    for (int q = 0; q < a.n; ++q)
+      for (int p = lane; p < pieces; p += 32)
+        *reinterpret_cast<uint4*>(a.from[q].to + (at.x + at.y + k) * a.pitch + 8 * p) = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -215,14 +257,15 @@ struct CombineArgs {
   uint16_t* out;
   long long ld;
   long long tokens, cols;
-  int top_k, chunks;  // chunks: of 256 columns
-  // the weights' gradient (backward): n_dots parts of each row's, rows_ld apart
+  int top_k, chunks;  // chunks: of 256 columns, and in the backward one more
+  // the weights' gradient (backward): n_dots parts of each row's
   const float* dots;
   int n_dots;
   float* dweight;
 };
 
-// A token's parts added up in the order of its slots. A warp takes 256 columns of a token.
+// A token's parts added up in the order of its slots. A warp takes 256 columns of a token, or (behind the
+// last ones, in the backward) its weights' gradients.
 __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
@@ -232,6 +275,20 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
     const long long t = i / a.chunks;
     const int chunk = static_cast<int>(i - t * a.chunks), col = 256 * chunk + 8 * lane;
     const int mine = lane < a.top_k ? a.row_of[t * a.top_k + lane] : -1;
+    if (256LL * chunk >= a.cols) {
+#pragma unroll 4
+      for (int j = 0; j < a.top_k; ++j) {  // (a row's parts lie side by side)
+        const int r = __shfl_sync(0xFFFFFFFFu, mine, j);
+        float x = 0.0f;
+        if (r >= 0) {
+          for (int p = lane; p < a.n_dots; p += 32) x += __ldcg(a.dots + static_cast<long long>(r) * a.n_dots + p);
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+        if (lane == j) a.dweight[t * a.top_k + j] = r == -2 ? __uint_as_float(0x7FC00000u) : x;
+      }
+      continue;
+    }
     float acc[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
@@ -269,14 +326,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
         for (int k = 0; k < 8; ++k)
           if (col + k < a.cols) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
       }
-    }
-    if (a.dweight != nullptr && chunk == 0 && lane < a.top_k) {
-      float s = mine == -2 ? __uint_as_float(0x7FC00000u) : 0.0f;
-      if (mine >= 0) {
-#pragma unroll 8
-        for (int p = 0; p < a.n_dots; ++p) s += __ldcg(a.dots + p * a.rows_ld + mine);
-      }
-      a.dweight[t * a.top_k + lane] = s;
     }
   }
 }
@@ -508,10 +557,10 @@ struct Call {
     a.from[0] = Source{c.x, c.ld_x, nullptr, nullptr, at<uint16_t>(p.xs)};
     if (c.x8 != nullptr) a.from[0] = Source{nullptr, 0, c.x8->q, c.x8->scale, at<uint16_t>(p.xs)};
     if (backward) a.from[1] = Source{c.dy, c.ld_dy, nullptr, nullptr, at<uint16_t>(p.dys)};
-    a.cols = c.dim, a.pitch = p.dp;
-    a.head = at<int>(p.head), a.row = at<int2>(p.row);
-    a.per_token = Divisor(static_cast<uint32_t>(c.top_k));
-    return launch_pdl(gather_kernel, dim3(blocks_for(32 * p.rows, sms)), dim3(256), 0, s, a);
+    a.tokens = c.tokens, a.cols = c.dim, a.pitch = p.dp;
+    a.row_of = at<int>(p.row_of), a.info = at<int2>(p.info);
+    a.top_k = c.top_k, a.experts = c.experts, a.fill = backward;
+    return launch_pdl(gather_kernel, dim3(blocks_for(32 * a.n * c.tokens * ((p.dp + 1023) / 1024), sms)), dim3(256), 0, s, a);
   }
   zopt_status combine(bool backward) const {
     CombineArgs a{};
@@ -520,7 +569,7 @@ struct Call {
     a.row_of = at<int>(p.row_of);
     a.out = backward ? c.dx : c.y, a.ld = backward ? c.ld_dx : c.ld_y;
     a.tokens = c.tokens, a.cols = c.dim;
-    a.top_k = c.top_k, a.chunks = static_cast<int>((c.dim + 255) / 256);
+    a.top_k = c.top_k, a.chunks = static_cast<int>((c.dim + 255) / 256) + (backward ? 1 : 0);
     if (backward) a.dots = at<float>(p.dots), a.n_dots = p.dot_parts, a.dweight = c.dweight;
     return launch_pdl(combine_kernel, dim3(blocks_for(32 * a.tokens * a.chunks, sms)), dim3(256), 0, s, a);
   }
@@ -601,7 +650,7 @@ struct Call {
       TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 0, j.tile_n / 2));
       j.out = dgu, j.ld_out = p.gp;
       j.out_h = h, j.ld_h = p.fp;
-      j.dots = at<float>(p.dots), j.rows_ld = p.rows;
+      j.dots = at<float>(p.dots), j.n_dots = p.dot_parts;
       TRY(launch_grouped(fn, b, kGluBwd, p.tiles, s));
     }
     Batch b{};

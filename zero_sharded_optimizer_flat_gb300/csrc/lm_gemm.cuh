@@ -95,8 +95,9 @@ struct Job {
   int by_inner;          // the experts' rows are the inner length (else the rows of D)
   long long out_stride;  // by_inner: elements between the experts' D
   float* part_scale;     // kStore by rows: D is fp16 in units of powers of two, at [64 columns][row]
-  float* dots;           // kGluBwd: the parts of dh . h, at [64 columns][row]
-  long long rows_ld;     // what these two's rows of rows are apart
+  long long rows_ld;     // (what its rows are apart)
+  float* dots;           // kGluBwd: the parts of dh . h, at [row][64 columns]
+  int n_dots;            // (of a row)
 };
 
 // The rows of a grouped batch's operands: each expert's one after another, filled up with rows of zeros to

@@ -1014,7 +1014,7 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const P
     }
     if (kGrouped && (c & 1) != 0) {  // a part for every 64 columns
       const float2 two = f2(dot);
-      if (mine.slot >= 0 && col - 32 < j.N) j.dots[static_cast<long long>(col >> 6) * j.rows_ld + row0 + lane] = two.x + two.y;
+      if (mine.slot >= 0 && col - 32 < j.N) j.dots[static_cast<long long>(row0 + lane) * j.n_dots + (col >> 6)] = two.x + two.y;
       dot = f2(0.0f, 0.0f);
     }
     k = next;
