@@ -750,7 +750,8 @@ typedef struct zopt_experts_job {
 
 /* Workspace bytes for a forward (backward = 0) or backward call, or either (backward = 1 covers
  * both), of a job: from its tokens, dim, hidden, experts, top_k and the ld_* and stride_* of the
- * direction's inputs; no pointer is looked at. 0 for a shape that the calls refuse. */
+ * weights and of kept (0: any; a known one may need less); no pointer is looked at. 0 for a shape that
+ * the calls refuse. */
 ZOPT_API size_t zopt_experts_workspace(const zopt_experts_job* job, int32_t backward);
 /* Errors of both: EINVAL for NULL or misaligned pointers (matrices 16 bytes, vectors their element,
  * scale bytes any), tokens < 0, dim, hidden, experts or top_k < 1, experts above 1024, top_k above 32,

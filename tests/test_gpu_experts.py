@@ -443,3 +443,13 @@ def test_a_few_slots(zopt, case, extra):
     y = b.y.clone()
     b.forward(zopt)
     assert torch.equal(y, b.y)
+
+
+@pytest.mark.parametrize("case", [(70, 64, 40, 3, 2, "silu", "e4m3", 4), (70, 64, 44, 3, 2, "gelu", "bf16", 4), (300, 33, 171, 5, 3, "silu", "e4m3", 9),
+                                  (200, 96, 266, 1, 1, "silu", "bf16", 0), (333, 40, 24, 2, 2, "gelu", "e4m3", 0)])
+def test_kept_rows_that_start_anywhere(zopt, case):
+    """Widths whose kept rows, or their ups, do not start on 16 bytes, and tiles of 128 rows with tails of few."""
+    b = Block(*case, seed=14)
+    b.forward(zopt)
+    b.backward(zopt)
+    b.check(zopt)

@@ -44,7 +44,7 @@ struct PlanArgs {
   const int32_t* index;
   const float* weight;
   long long slots;
-  int experts;
+  int experts, tile_rows;
   int* head;
   int4* tiles;
   int2* info;
@@ -117,7 +117,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
     }
   }
   // the experts before: their rows, and their row tiles
-  const int rows = (all + kGroupRows - 1) / kGroupRows * kGroupRows, tiles = (all + kTileM - 1) / kTileM;
+  const int rows = (all + kGroupRows - 1) / kGroupRows * kGroupRows, tiles = (all + a.tile_rows - 1) / a.tile_rows;
   int r = rows, t = tiles;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -143,7 +143,8 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
     mine[e] = first + before;
     if (rank == 0) a.info[e] = make_int2(first, all);
     for (int i = static_cast<int>(rank); i < tiles; i += kPlanCtas)
-      a.tiles[first_tile + i] = make_int4(e, first + i * kTileM, first + rows, all - i * kTileM <= kTileM / 2 ? 1 : 0);
+      a.tiles[first_tile + i] = make_int4(e, first + i * a.tile_rows, min(first + rows, first + (i + 1) * a.tile_rows),
+                                          min(all - i * a.tile_rows, a.tile_rows) <= kTileM / 2 ? 1 : 0);
     for (int i = all + static_cast<int>(rank); i < rows; i += kPlanCtas) a.row[first + i] = make_int2(-1, 0);
   }
   __syncthreads();
@@ -342,6 +343,32 @@ __global__ void __launch_bounds__(256) stage_kernel(uint16_t* dst, long long dst
   }
 }
 
+// The kept rows of the slots that have an expert, gate and up each from a 16-byte boundary on, zeros behind them
+// (the epilogue that reads them takes 16 bytes of a row at a time; rows that start anywhere, a lane each, would
+// take it 32 times as long). A warp takes a slot.
+template <typename Element>
+__global__ void __launch_bounds__(256) kept_kernel(const Element* kept, long long ld, long long hidden, const int* row_of, long long slots,
+                                                   uint8_t* out, long long part) {
+  tc::pdl_launch_dependents();
+  tc::pdl_wait();
+  constexpr int kSize = sizeof(Element), kPer = 16 / kSize;
+  const int lane = threadIdx.x & 31;
+  const long long step = static_cast<long long>(gridDim.x) * 8, pieces = 2 * part / 16;
+  for (long long s = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); s < slots; s += step) {
+    if (__ldcg(row_of + s) < 0) continue;
+#pragma unroll 2
+    for (long long p = lane; p < pieces; p += 32) {
+      const long long col = (p * 16 < part ? p : p - part / 16) * kPer;
+      const Element* const from = kept + s * ld + (p * 16 < part ? 0 : hidden) + col;
+      uint32_t w[4] = {};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (col + i < hidden) w[i * kSize / 4] |= static_cast<uint32_t>(__ldg(from + i)) << (8 * (i * kSize % 4));
+      *reinterpret_cast<uint4*>(out + s * 2 * part + 16 * p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // dst[e][r][c] = 0 for c < cols
 __global__ void __launch_bounds__(256) zero_kernel(uint16_t* dst, long long ld, long long stride, long long experts, long long rows,
                                                    long long cols) {
@@ -359,8 +386,10 @@ __global__ void __launch_bounds__(256) zero_kernel(uint16_t* dst, long long ld, 
 struct Layout {
   long long dp, fp, gp;  // dim, hidden and 2 hidden rounded up to 8
   long long slots, rows, tiles;
-  bool stage_gate, stage_up, stage_down;
-  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, few_gate_up, few_y, total;
+  int tile_rows;
+  bool stage_gate, stage_up, stage_down, stage_kept;
+  long long kept_row;  // bytes of a part of a staged row
+  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, kept, few_gate_up, few_y, total;
   int dot_parts;
   bool few;
 };
@@ -405,7 +434,11 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   p.dp = round_up(D, 8), p.fp = round_up(F, 8), p.gp = round_up(2 * F, 8);
   const long long used = std::min<long long>(E, p.slots);
   p.rows = round_up(p.slots + (kGroupRows - 1) * used, kGroupRows);
-  p.tiles = p.slots / kTileM + used;
+  // Tiles of 128 rows throughout where those of 256 (with half of one left over for every expert) would leave
+  // pairs idle: the gate's product has the fewest columns (backward, 1023 x 2 slots
+  // of 256 x 768 in eight experts: 37 us for 45, with the rounds of units in turn and back).
+  p.tile_rows = (p.slots / kTileM + (used + 1) / 2) * ((F + kTileN - 1) / kTileN) <= kPairs ? kTileM / 2 : kTileM;
+  p.tiles = p.slots / p.tile_rows + used;
   p.stage_gate = c.ld_gate_up % 8 != 0 || (E > 1 && c.stride_gate_up % 8 != 0);
   p.stage_up = p.stage_gate || F % 8 != 0;  // (the forward reads up's columns from column hidden on)
   p.stage_down = c.ld_down % 8 != 0 || (E > 1 && c.stride_down % 8 != 0);
@@ -435,7 +468,13 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   if (!backward) return p;
   p.dys = take(at, p.rows * p.dp * 2);
   p.dgu = take(at, p.rows * p.gp * 2);
-  p.parts = take(at, p.rows * p.dp * 2);
+  // dx's parts; before them, where they have to be copied, the kept rows (of whichever format: a query may not
+  // know which, nor the distance of their rows, which it then has as 0)
+  const long long size = c.kept8 != nullptr ? 1 : 2;
+  p.stage_kept = F * size % 16 != 0 || (c.kept8 == nullptr && c.ld_kept % 8 != 0);
+  p.kept_row = round_up(F * size, 16);
+  const bool may = F % 16 != 0 || c.ld_kept == 0 || c.ld_kept % 8 != 0;
+  p.kept = p.parts = take(at, std::max(p.rows * p.dp * 2, may ? p.slots * 2 * round_up(2 * F, 16) : 0));
   p.dot_parts = static_cast<int>((F + 63) / 64);
   p.dots = take(at, 4 * p.rows * p.dot_parts);
   p.total = std::max(p.total, at);
@@ -548,7 +587,7 @@ struct Call {
     ZOPT_CUDA_TRY(once_per_device([] {
       return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kPlanWarps + 1) * kMaxExperts * 4);
     }));
-    const PlanArgs a{c.index, c.weight, p.slots, c.experts, at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), at<int>(p.row_of)};
+    const PlanArgs a{c.index, c.weight, p.slots, c.experts, p.tile_rows, at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), at<int>(p.row_of)};
     return launch_pdl(plan_kernel, dim3(kPlanCtas), dim3(32 * kPlanWarps), smem, s, a);
   }
   zopt_status gather(bool backward) const {
@@ -587,6 +626,7 @@ struct Call {
   void glu(Job& j) const {
     j.act = c.act;
     j.hidden = static_cast<int>(c.hidden);
+    j.kept_up = c.hidden;
     if (c.kept8 != nullptr) {
       j.kept_mode = kKeep8;
       j.kept = c.kept8->q;
@@ -597,6 +637,21 @@ struct Call {
       j.kept = c.kept;
       j.ld_kept = c.ld_kept;
     }
+  }
+  zopt_status stage_kept(Job& j) const {
+    uint8_t* const to = at<uint8_t>(p.kept);
+    const int* const row_of = at<int>(p.row_of);
+    const dim3 grid(blocks_for(32 * p.slots, sms));
+    const long long hidden = c.hidden, ld = j.ld_kept;
+    j.kept = to;
+    if (c.kept8 != nullptr) {
+      j.ld_kept = 2 * p.kept_row, j.kept_up = p.kept_row;
+      return launch_pdl(kept_kernel<uint8_t>, grid, dim3(256), 0, s, static_cast<const uint8_t*>(c.kept8->q), ld, hidden, row_of, p.slots, to,
+                        p.kept_row);
+    }
+    j.ld_kept = p.kept_row, j.kept_up = p.kept_row / 2;
+    return launch_pdl(kept_kernel<uint16_t>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(c.kept), ld, hidden, row_of, p.slots, to,
+                      p.kept_row);
   }
 
   zopt_status forward() const {
@@ -646,6 +701,7 @@ struct Call {
       Job& j = b.job[0];
       group_job(j, p, kGluBwd, false, 0, F, D, c.experts);
       glu(j);
+      if (p.stage_kept) TRY(stage_kept(j));
       TRY(map_rows(fn, j, &j.P, dys, p.rows, D, p.dp, 0, 64));
       TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 0, j.tile_n / 2));
       j.out = dgu, j.ld_out = p.gp;

@@ -218,6 +218,7 @@ zopt_status stage_inputs(const char* fn, const zopt_ffn_job& c, const FfnPlan& p
 void glu_fields(Job& j, const zopt_ffn_job& c) {
   j.act = c.act;
   j.hidden = static_cast<int>(c.hidden);
+  j.kept_up = c.hidden;
   if (c.kept8 != nullptr) {
     j.kept_mode = kKeep8;
     j.kept = c.kept8->q;

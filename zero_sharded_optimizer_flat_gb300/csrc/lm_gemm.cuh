@@ -87,8 +87,9 @@ struct Job {
   float* tlogit;  // kCeFwd: the target's logit
   // kGluFwd, kGluBwd
   int act, kept_mode;
-  void* kept;  // gate and up as the caller keeps them: row r's gate at r * ld_kept, its up hidden later
+  void* kept;  // gate and up as the caller keeps them: row r's gate at r * ld_kept, its up kept_up later
   long long ld_kept;
+  long long kept_up;    // from a row's gate to its up
   uint8_t* kept_scale;  // kKeep8: row r's block exponents at r * 2 blocks, the gate's first
   int hidden;           // the gate's width, N
   // grouped batches

@@ -295,7 +295,11 @@ __device__ __forceinline__ Unit unit_of(const Batch& B, const Job& j, int u) {
   return w;
 }
 // Pair p's i-th unit, or a number beyond the last.
+// (Grouped: units are the longer the earlier they come, and those that begin every other round go to the
+// pairs whose last ones were the shortest.)
+template <bool kGrouped>
 __device__ __forceinline__ int unit_at(const Batch& b, int pair, int npairs, int i) {
+  if constexpr (kGrouped) return i * npairs + ((i & 1) != 0 ? npairs - 1 - pair : pair);
   if (!b.listed) return pair + i * npairs;
   const int at = b.first[pair] + i;
   return at < b.first[pair + 1] ? b.order[at] : 0x7FFFFFFF;
@@ -851,13 +855,14 @@ struct Kept {
       const int at = col * kSize + 16 * (lane % kPerRow);
       const long long pitch = j.ld_kept * kSize, up = static_cast<long long>(j.hidden) * kSize;
       const uint8_t* const p = static_cast<const uint8_t*>(j.kept) + at;
+      const long long to_up = j.kept_up * kSize;
 #pragma unroll
       for (int i = 0; i < kPerRow; ++i) {
         uint4 g = make_uint4(0, 0, 0, 0), u = g;
         const int from = __shfl_sync(0xFFFFFFFFu, slot, lane / kPerRow + i * kAtOnce);
         if (at < up && from >= 0) {
           g = __ldg(reinterpret_cast<const uint4*>(p + from * pitch));
-          u = __ldg(reinterpret_cast<const uint4*>(p + from * pitch + up));
+          u = __ldg(reinterpret_cast<const uint4*>(p + from * pitch + to_up));
         }
         x[0][4 * i] = g.x, x[0][4 * i + 1] = g.y, x[0][4 * i + 2] = g.z, x[0][4 * i + 3] = g.w;
         x[1][4 * i] = u.x, x[1][4 * i + 1] = u.y, x[1][4 * i + 2] = u.z, x[1][4 * i + 3] = u.w;
@@ -876,8 +881,7 @@ struct Kept {
         row += kAtOnce, p += kAtOnce * pitch;
       }
     } else {
-      const int row = kGrouped ? slot : row0 + lane;
-      load_row(j, row, kGrouped ? row >= 0 : row < rows, col);
+      load_row(j, row0 + lane, row0 + lane < rows, col);
     }
   }
   // What was loaded becomes the lane's row (through the warp's box).
@@ -1091,7 +1095,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t s = 0, ph = 1;
       long long done = 0;  // stages armed so far
       bool ok = true;
-      for (int i = 0, t; ok && (t = unit_at(B, pair, npairs, i)) < total; ++i) {
+      for (int i = 0, t; ok && (t = unit_at<kGrouped>(B, pair, npairs, i)) < total; ++i) {
         const int ji = starts.job(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
@@ -1147,7 +1151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int it = 0;
       bool ok = true;
       const uint32_t tempty0 = tc::smem_u32(tempty);
-      for (int t; ok && (t = unit_at(B, pair, npairs, it)) < total; ++it) {
+      for (int t; ok && (t = unit_at<kGrouped>(B, pair, npairs, it)) < total; ++it) {
         const int ji = starts.job(B, t);
         const Job& j = B.job[ji];
         const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
@@ -1214,14 +1218,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return n;
     };
     if constexpr ((kKinds & kGluBwd) != 0) {
-      const Next n = first_of(unit_at(B, pair, npairs, 0));
+      const Next n = first_of(unit_at<kGrouped>(B, pair, npairs, 0));
       mine = n.mine;
       kept.load(B.job[0], n.row0, n.rows, mine.slot, n.col, lane);
       if constexpr (kKept == kKeep8)
         scales.load(B.job[0], kGrouped ? mine.slot : n.row0 + lane, kGrouped ? mine.slot >= 0 : n.row0 + lane < n.rows, n.col);
     }
     int it = 0;
-    for (int t; (t = unit_at(B, pair, npairs, it)) < total;) {
+    for (int t; (t = unit_at<kGrouped>(B, pair, npairs, it)) < total;) {
       const int b = it & 1;
       const uint32_t tph = static_cast<uint32_t>(it >> 1) & 1u;
       ++it;
@@ -1231,7 +1235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Part part = part_of_tile<kGrouped>(w, columns(j), rank, quad, half);
       const int row0 = part.row0;
       Next next{};
-      if constexpr ((kKinds & kGluBwd) != 0) next = first_of(unit_at(B, pair, npairs, it));
+      if constexpr ((kKinds & kGluBwd) != 0) next = first_of(unit_at<kGrouped>(B, pair, npairs, it));
       if constexpr (kGrouped && (kKinds & kGluFwd) != 0) mine = Row::at<kGrouped>(B, row0 + lane, w.rows);
       int ok = 1;
       if (lane == 0) ok = wait(tc::smem_u32(tfull + b), tph, err) ? 1 : 0;
@@ -1279,10 +1283,14 @@ zopt_status launch_glu(Batch& b, dim3 grid, cudaStream_t s) {
                                  : launch_kinds<kGrouped, kGluFwd, kAct, kKeepBf16>(b, grid, s);
   }
   const int size = j.kept_mode == kKeep8 ? 1 : 2;
-  const bool wide = aligned16(j.kept) && j.ld_kept * size % 16 == 0 && static_cast<long long>(j.hidden) * size % 16 == 0;
-  if (j.kept_mode == kKeep8)
-    return wide ? launch_kinds<kGrouped, kGluBwd, kAct, kKeep8>(b, grid, s) : launch_kinds<kGrouped, kGluBwd, kAct, kKeep8, false>(b, grid, s);
-  return wide ? launch_kinds<kGrouped, kGluBwd, kAct, kKeepBf16>(b, grid, s) : launch_kinds<kGrouped, kGluBwd, kAct, kKeepBf16, false>(b, grid, s);
+  const bool wide = kGrouped || (aligned16(j.kept) && j.ld_kept * size % 16 == 0 && j.kept_up * size % 16 == 0);  // (grouped: always)
+  if constexpr (!kGrouped) {
+    if (!wide)
+      return j.kept_mode == kKeep8 ? launch_kinds<kGrouped, kGluBwd, kAct, kKeep8, false>(b, grid, s)
+                                   : launch_kinds<kGrouped, kGluBwd, kAct, kKeepBf16, false>(b, grid, s);
+  }
+  return j.kept_mode == kKeep8 ? launch_kinds<kGrouped, kGluBwd, kAct, kKeep8>(b, grid, s)
+                               : launch_kinds<kGrouped, kGluBwd, kAct, kKeepBf16>(b, grid, s);
 }
 
 }  // namespace
