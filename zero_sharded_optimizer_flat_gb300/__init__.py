@@ -209,7 +209,8 @@ def _find_current_stream():
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    device = torch.cuda.current_device
+    torch.cuda.current_device()
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return lambda: raw(device())
 
 
@@ -647,7 +648,7 @@ def _on_device(*tensors) -> None:
             raise ValueError("tensors must be on the GPU")
 
 
-I64 = 64  # not a zopt_dtype: no matrix may have it
+I64, I32, U8 = 64, 65, 66  # not zopt_dtypes: no matrix may have them
 _CODES = {}
 
 
@@ -655,7 +656,8 @@ def _code(t) -> int:
     """_dtype_code from a table (filled on the first call)."""
     if not _CODES:
         import torch
-        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int64: I64})
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int64: I64, torch.int32: I32, torch.uint8: U8,
+                       torch.bool: U8})
     return _CODES.get(t.dtype, -1)
 
 
@@ -808,25 +810,27 @@ def linear_ce_backward(x, w, target, lse, dloss, dx, dw, ws, *, ignore_index: in
 
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
-I32, U8 = 65, 66  # not zopt_dtypes either
 _ELEMENTS = {F32: "fp32", I32: "int32", U8: "bool or byte"}
 
 
 def _array(t, shape, code: int, name: str):
     """The address of a contiguous array on the GPU."""
-    if I32 not in _CODES.values():
-        import torch
-        _code(t)
-        _CODES.update({torch.int32: I32, torch.uint8: U8, torch.bool: U8})
     if t.shape != shape or not t.is_contiguous() or not t.is_cuda or _code(t) != code:
         raise ValueError(f"{name} must be a contiguous {_ELEMENTS[code]} array of {' x '.join(map(str, shape))} on the GPU")
     return t.data_ptr()
 
 
+_current_device = None
+
+
 def _one_device(*tensors) -> None:
     """The calls launch on the current device: everything has to be there."""
-    import torch
-    here = torch.cuda.current_device()
+    global _current_device
+    if _current_device is None:
+        import torch
+        torch.cuda.current_device()  # (initialises CUDA, which the cheaper one does not)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    here = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"tensors must be on the current device, cuda:{here}")
@@ -836,24 +840,22 @@ def _route_job(logits, index, weight, counts, bias, live, score, groups, top_gro
                dlogits=None) -> _RouteJob:
     tokens, experts = logits.shape
     top_k = index.shape[-1]
-    dtype = _code(logits)
     slots = (tokens, top_k)
-    j = _RouteJob(tokens, experts, top_k, int(groups), int(top_groups),
-                  _SCORES.get(score, score if isinstance(score, int) else -1), int(bool(renormalise)), float(scale),
-                  dtype if dtype in (F32, BF16) else -1, *_matrix(logits, tokens, experts, "logits"))
-    j.index = _array(index, slots, I32, "index")
-    j.weight = _array(weight, slots, F32, "weight")
-    if counts is not None:
-        j.counts = _array(counts, (experts,), I32, "counts")
-    if bias is not None:
-        j.bias = _array(bias, (experts,), F32, "bias")
-    if live is not None:
-        j.live = _array(live, (tokens,), U8, "live")
+    dtype = _code(logits)
+    if dtype != F32 and dtype != BF16:
+        dtype = -1
+    pd = ld = None
     if dlogits is not None:
-        j.dweight = _array(dweight, slots, F32, "dweight")
-        j.dlogits, j.ld_dlogits = _matrix(dlogits, tokens, experts, "dlogits")
+        pd, ld = _matrix(dlogits, tokens, experts, "dlogits")
         if _code(dlogits) != dtype:
-            j.dtype = -1
+            dtype = -1
+    j = _RouteJob(
+        tokens, experts, top_k, groups, top_groups, _SCORES.get(score, score if isinstance(score, int) else -1),
+        1 if renormalise else 0, scale, dtype, *_matrix(logits, tokens, experts, "logits"),
+        None if bias is None else _array(bias, (experts,), F32, "bias"), None if live is None else _array(live, (tokens,), U8, "live"),
+        _array(index, slots, I32, "index"), _array(weight, slots, F32, "weight"),
+        None if counts is None else _array(counts, (experts,), I32, "counts"),
+        None if dweight is None else _array(dweight, slots, F32, "dweight"), pd, ld or 0)
     _one_device(logits, index, weight, counts, bias, live, dweight, dlogits)
     return j
 

@@ -356,15 +356,21 @@ __global__ void __launch_bounds__(256) kept_kernel(const Element* kept, long lon
   const long long step = static_cast<long long>(gridDim.x) * 8, pieces = 2 * part / 16;
   for (long long s = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); s < slots; s += step) {
     if (__ldcg(row_of + s) < 0) continue;
-#pragma unroll 2
+#pragma unroll 4
     for (long long p = lane; p < pieces; p += 32) {
       const long long col = (p * 16 < part ? p : p - part / 16) * kPer;
       const Element* const from = kept + s * ld + (p * 16 < part ? 0 : hidden) + col;
-      uint32_t w[4] = {};
+      uint4 v;
+      if constexpr (kSize == 2) {
+        v = row_piece8(from, hidden - col);
+      } else {
+        uint32_t w[4] = {};
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (col + i < hidden) w[i * kSize / 4] |= static_cast<uint32_t>(__ldg(from + i)) << (8 * (i * kSize % 4));
-      *reinterpret_cast<uint4*>(out + s * 2 * part + 16 * p) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < kPer; ++i)
+          if (col + i < hidden) w[i / 4] |= static_cast<uint32_t>(__ldg(from + i)) << (8 * (i % 4));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *reinterpret_cast<uint4*>(out + s * 2 * part + 16 * p) = v;
     }
   }
 }

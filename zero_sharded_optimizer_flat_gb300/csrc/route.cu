@@ -494,10 +494,8 @@ struct Chooser {
     }
   }
 
-  // A row's choice, into the lanes from lane0 on.
-  __device__ __forceinline__ void row(const float (&l)[V], long long at, int lane0, bool here, Batch& batch) const {
-    uint32_t w[V];
-    Batch r;
+  // A row's words, sorted, and what else its lanes have to know of it.
+  __device__ __forceinline__ void words(const float (&l)[V], long long at, uint32_t (&w)[V], Batch& r) const {
     // (of a 1024th of each: no sum of finite ones overflows)
     float size = 0.0f;
 #pragma unroll
@@ -556,16 +554,35 @@ struct Chooser {
         sort_words<V>(w);
       }
     }
+  }
+
+  // kRows rows' choices, the k-th row's into the `width` lanes from (k0 + k) width on. Rows that take turns hide
+  // one another's latencies; a choice that there is not is 0, and so is any after it.
+  template <int kRows>
+  __device__ __forceinline__ void rows(const float (&l)[kRows][V], long long at, int k0, Batch& batch) const {
+    uint32_t w[kRows][V];
+    Batch r[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) words(l[k], at + k, w[k], r[k]);
+    const int slot = lane - k0 * a.width;
+#pragma unroll 2
     for (int n = 0; n < a.top_k; ++n) {
-      const uint32_t top = __reduce_max_sync(kAll, w[0]);
-      if (top == 0) break;  // (the whole warp's)
-      if (lane == lane0 + n) batch.mine = top;
-      drop_first<V>(w, w[0] == top);
+      uint32_t top[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) top[k] = __reduce_max_sync(kAll, w[k][0]);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (slot - k * a.width == n) batch.mine = top[k];
+        drop_first<V>(w[k], w[k][0] == top[k]);
+      }
     }
-    r.left = __reduce_max_sync(kAll, w[0]);
-    if (here) {
-      r.mine = batch.mine;
-      batch = r;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      r[k].left = __reduce_max_sync(kAll, w[k][0]);
+      if (slot >= k * a.width && slot < (k + 1) * a.width) {
+        r[k].mine = batch.mine;
+        batch = r[k];
+      }
     }
   }
 };
@@ -588,16 +605,32 @@ __global__ void __launch_bounds__(kThreads, V >= 16 ? 2 : V >= 8 ? 3 : 4) forwar
     // bit r: row row0 + r is no padding
     const uint32_t live = __ballot_sync(kAll, lane < n && (a.live == nullptr || a.live[row0 + lane] != 0));
     Batch r;
-    float next[V];
+    // (the next rows are on their way while some are worked on; padding has none)
+    constexpr int kRows = V <= 8 ? 2 : 1;
+    float next[kRows][V];
+    auto fetch = [&](int k) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) next[v] = -INFINITY;
-    if (live & 1u) load_row<V>(a, row0, chooser.first, next);
-    for (int k = 0; k < n; ++k) {  // (the next row is on its way while one is worked on)
-      float l[V];
+      for (int q = 0; q < kRows; ++q) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) l[v] = next[v];
-      if ((live >> k) & 2u) load_row<V>(a, row0 + k + 1, chooser.first, next);
-      if ((live >> k) & 1u) chooser.row(l, row0 + k, k * W, which == k, r);
+        for (int v = 0; v < V; ++v) next[q][v] = -INFINITY;
+        if (k + q < n && ((live >> (k + q)) & 1u)) load_row<V>(a, row0 + k + q, chooser.first, next[q]);
+      }
+    };
+    fetch(0);
+    for (int k = 0; k < n; k += kRows) {
+      float l[kRows][V];
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[q][v] = next[q][v];
+      if (k + kRows < n) fetch(k + kRows);
+      if ((live >> k) == 0) break;
+      if (kRows == 2 && ((live >> k) & 2u) != 0) {
+        chooser.template rows<kRows>(l, row0 + k, k, r);
+      } else if ((live >> k) & 1u) {
+        const float (&one)[1][V] = reinterpret_cast<const float (&)[1][V]>(l);
+        chooser.template rows<1>(one, row0 + k, k, r);
+      }
     }
     const long long row = row0 + which;
     const bool there = which < n && ((live >> which) & 1u) != 0;
