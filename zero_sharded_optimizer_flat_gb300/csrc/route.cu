@@ -696,68 +696,70 @@ __global__ void __launch_bounds__(kThreads, V >= 16 ? 2 : V >= 8 ? 3 : 4) forwar
 //   softmax:                dl_i = scale p_i ([i chosen] dw_i - sum_k dw_k p_k)
 //   logistic:               as the first with a factor 1 - s_j; without the sum where not renormalised.
 //
-// A warp writes its row whole, with what the chosen experts' entries would be if they had not been
-// chosen, and then the chosen ones' again, a lane each. Bound by what it writes.
+// As in the forward the slots of a warp's rows lie side by side in its lanes. A row is written whole, with
+// what the chosen experts' entries would be if they had not been chosen, and then all the chosen ones' again,
+// a lane each. Bound by what it writes.
 template <int V>
 __global__ void __launch_bounds__(kThreads) backward_kernel(const Args a) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = lane * V;
+  const int lane = threadIdx.x & 31, first = lane * V, W = a.width, j = lane & (W - 1), which = lane / W;
   const float nan = __uint_as_float(0x7FC00000u);
-  for (long long row = static_cast<long long>(blockIdx.x) * kWarps + warp; row < a.tokens;
-       row += static_cast<long long>(gridDim.x) * kWarps) {
+  const bool dense = a.softmax && !a.renormalise;
+  const long long step = static_cast<long long>(gridDim.x) * kWarps * a.rows;
+  for (long long row0 = (static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * a.rows; row0 < a.tokens; row0 += step) {
+    const int n = static_cast<int>(min(static_cast<long long>(a.rows), a.tokens - row0));
+    const long long row = row0 + which, slot = row * a.top_k + j;
     int mine = -1;
-    float w = 0.0f, g = 0.0f;
-    if (lane < a.top_k) mine = a.index[row * a.top_k + lane];
-    const bool on = mine >= 0 && mine < a.experts, bad = __any_sync(kAll, mine != -1 && !on);
-    float ml = 0.0f;
+    float w = 0.0f, g = 0.0f, ml = 0.0f;
+    if (which < n && j < a.top_k) mine = a.index[slot];
+    const bool on = mine >= 0 && mine < a.experts;
+    const unsigned none = __ballot_sync(kAll, mine != -1 && !on), some = __ballot_sync(kAll, on);
     if (on) {
-      w = a.weight[row * a.top_k + lane];
-      g = a.dweight[row * a.top_k + lane];
-      if (!a.softmax) ml = load(a, row, mine);
+      w = a.weight[slot];
+      g = a.dweight[slot];
+      if (a.softmax ? dense : true) ml = load(a, row, mine);
     }
-    const float mean = warp_sum(g * w) / a.scale;
+    const float mean = lanes_sum(g * w, W) / a.scale;
     float d = (a.renormalise ? g - mean : g) * w;
     if (!a.softmax) d *= 1.0f / (1.0f + expf(ml));  // 1 - s
-    float out[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) out[v] = 0.0f;
     float rest = 0.0f;  // what the lane's expert would have if it were not chosen
-    if (a.softmax && !a.renormalise && __any_sync(kAll, on)) {
-      float m, z = 0.0f;
-      load_row<V>(a, row, first, out);
-      m = out[0];
+    const unsigned lanes = W == 32 ? kAll : (1u << W) - 1u;  // a row's
+    for (int k = 0; k < n; ++k) {
+      const bool bad = ((none >> (k * W)) & lanes) != 0;
+      float out[V];
 #pragma unroll
-      for (int v = 1; v < V; ++v) m = fmaxf(m, out[v]);
-      m = warp_max(m);
+      for (int v = 0; v < V; ++v) out[v] = bad ? nan : 0.0f;
+      if (dense && !bad && ((some >> (k * W)) & lanes) != 0) {
+        load_row<V>(a, row0 + k, first, out);
+        float m = out[0], z = 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        out[v] = out[v] == -INFINITY ? 0.0f : expf(out[v] - m);
-        z += out[v];
+        for (int v = 1; v < V; ++v) m = fmaxf(m, out[v]);
+        m = warp_max(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          out[v] = out[v] == -INFINITY ? 0.0f : expf(out[v] - m);
+          z += out[v];
+        }
+        const float f = -__shfl_sync(kAll, mean, k * W) * a.scale / warp_sum(z);
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] *= f;
+        if (which == k && on) rest = expf(ml - m) * f;
       }
-      const float f = -mean * a.scale / warp_sum(z);
-#pragma unroll
-      for (int v = 0; v < V; ++v) out[v] *= f;
-      if (on) rest = expf(load(a, row, mine) - m) * f;
+      store_row<V>(a, row0 + k, first, out);
     }
-    if (bad) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) out[v] = nan;
-    }
-    store_row<V>(a, row, first, out);
-    if (bad) continue;
-    // an expert that the row names more than once takes all its slots' parts, in their order
-    const unsigned same = __match_any_sync(kAll, on ? mine : -1 - lane);
+    // an expert that a row names more than once takes all its slots' parts, in their order
+    const unsigned same = __match_any_sync(kAll, on ? which * kMaxExperts + mine : -1 - lane);
     float sum = d;
     if (__any_sync(kAll, __popc(same) > 1)) {
       sum = 0.0f;
-      for (int j = 0; j < a.top_k; ++j) {
-        const float x = __shfl_sync(kAll, d, j);
-        if ((same >> j) & 1u) sum += x;
+      for (int q = 0; q < 32; ++q) {
+        const float x = __shfl_sync(kAll, d, q);
+        if ((same >> q) & 1u) sum += x;
       }
     }
     __syncwarp();  // (orders the two stores to one address)
-    if (on && (same & ((1u << lane) - 1u)) == 0) {
+    if (on && (same & ((1u << lane) - 1u)) == 0 && ((none >> (which * W)) & lanes) == 0) {
       const long long at = row * a.ld_d + mine;
       if (a.bf16) {
         static_cast<__nv_bfloat16*>(a.dlogits)[at] = __float2bfloat16_rn(rest + sum);
@@ -816,14 +818,18 @@ Args args_of(const zopt_route_job& c) {
 
 // Rows of a warp at a time: as many as its lanes hold the choices of, but not so many that fewer than 16
 // warps an SM have some.
+void set_rows(Args& a, int sms) {
+  for (a.width = 1; a.width < a.top_k;) a.width *= 2;
+  a.rows = static_cast<int>(std::max<long long>(1, std::min<long long>(32 / a.width, a.tokens / (16LL * sms))));
+}
+
 template <int V>
 zopt_status launch_forward(Args a, int sms, cudaStream_t s) {
   const uintptr_t size = a.bf16 ? 2 : 4, piece = std::min<uintptr_t>(16, V * size);
   a.vec = reinterpret_cast<uintptr_t>(a.logits) % piece == 0 && a.ld * size % piece == 0;
   const int per = static_cast<int>(a.per_group.d), lanes = per / V;
   a.lanes_per_group = per % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-  for (a.width = 1; a.width < a.top_k;) a.width *= 2;
-  a.rows = static_cast<int>(std::max<long long>(1, std::min<long long>(32 / a.width, a.tokens / (16LL * sms))));
+  set_rows(a, sms);
   const auto kernel = a.bias == nullptr && a.groups == 1 ? forward_kernel<V, true> : forward_kernel<V, false>;
   const long long rows = static_cast<long long>(kWarps) * a.rows;
   const unsigned blocks = static_cast<unsigned>(std::min<long long>((a.tokens + rows - 1) / rows, 8LL * sms));
@@ -836,7 +842,9 @@ zopt_status launch_backward(Args a, int sms, cudaStream_t s) {
   const uintptr_t size = a.bf16 ? 2 : 4, piece = std::min<uintptr_t>(16, V * size);
   a.vec = reinterpret_cast<uintptr_t>(a.logits) % piece == 0 && a.ld * size % piece == 0;
   a.vec_d = reinterpret_cast<uintptr_t>(a.dlogits) % piece == 0 && a.ld_d * size % piece == 0;
-  const unsigned blocks = static_cast<unsigned>(std::min<long long>((a.tokens + kWarps - 1) / kWarps, 8LL * sms));
+  set_rows(a, sms);
+  const long long rows = static_cast<long long>(kWarps) * a.rows;
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((a.tokens + rows - 1) / rows, 8LL * sms));
   return launch_pdl(backward_kernel<V>, dim3(blocks), dim3(kThreads), 0, s, a);
 }
 
