@@ -182,6 +182,21 @@ struct Source {
   const uint8_t *q, *scale;  // or a checkpoint (x null)
   uint16_t* to;              // rows of `pitch` elements
 };
+// An operand that the TMA cannot read where it is: dst[e][r][c] = src[e][r][c] for c < cols, 0 up to dst_cols.
+struct Copy {
+  uint16_t* dst;
+  const uint16_t* src;
+  long long dst_cols, ld, stride, rows, cols;
+};
+// The kept rows of the slots that have an expert, gate and up each from a 16-byte boundary on, zeros behind them
+// (the epilogue that reads them takes 16 bytes of a row at a time; rows that start anywhere, a lane each, would
+// take it 32 times as long).
+struct KeptCopy {
+  uint8_t* dst;  // rows of two parts of `part` bytes; null: none
+  const void* src;
+  long long ld, hidden, part;
+  int size;  // of an entry
+};
 struct GatherArgs {
   Source from[2];
   int n;
@@ -190,6 +205,9 @@ struct GatherArgs {
   const int2* info;
   int top_k, experts;
   int fill;  // the backward multiplies by the rows that only fill up
+  Copy copy[3];
+  int copies;
+  KeptCopy kept;
 };
 
 // 16 bytes of a token's row, zeros behind the last column.
@@ -209,9 +227,40 @@ __device__ __forceinline__ uint4 piece_of(const Source& f, long long cols, long 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ void copy_rows(const Copy& c, int experts, long long thread, long long threads) {
+  const long long per_row = c.dst_cols / 8, n = experts * c.rows * per_row;
+#pragma unroll 2
+  for (long long g = thread; g < n; g += threads) {
+    const long long row = g / per_row, col = (g - row * per_row) * 8, e = row / c.rows;
+    *reinterpret_cast<uint4*>(c.dst + row * c.dst_cols + col) = row_piece8(c.src + e * c.stride + (row - e * c.rows) * c.ld + col, c.cols - col);
+  }
+}
+__device__ __forceinline__ void copy_kept(const KeptCopy& c, const int* row_of, long long slots, int lane, int warp, int warps) {
+  const long long pieces = 2 * c.part / 16;
+  const int per = 16 / c.size;
+  for (long long s = warp; s < slots; s += warps) {
+    if (__ldcg(row_of + s) < 0) continue;
+#pragma unroll 4
+    for (long long p = lane; p < pieces; p += 32) {
+      const long long col = (p * 16 < c.part ? p : p - c.part / 16) * per, at = s * c.ld + (p * 16 < c.part ? 0 : c.hidden) + col;
+      uint4 v;
+      if (c.size == 2) {
+        v = row_piece8(static_cast<const uint16_t*>(c.src) + at, c.hidden - col);
+      } else {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (col + i < c.hidden) w[i / 4] |= static_cast<uint32_t>(__ldg(static_cast<const uint8_t*>(c.src) + at + i)) << (8 * (i % 4));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *reinterpret_cast<uint4*>(c.dst + s * 2 * c.part + 16 * p) = v;
+    }
+  }
+}
+
 // Rows of x (and dy) in the plan's order, zeros behind the last column and (fill) where a row only fills up. A warp
 // reads a token's row, 1024 columns of it at a time, and writes it wherever the token's slots have theirs;
-// bound by what it writes.
+// bound by what it writes. What else has to be copied first is, in the same launch.
 __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   tc::pdl_launch_dependents();
   tc::pdl_wait();
@@ -238,6 +287,9 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
         if (p0 + 32 * q < pieces) *reinterpret_cast<uint4*>(to + 8 * (p0 + 32 * q)) = v[q];
     }
   }
+  for (int k = 0; k < a.copies; ++k)
+    copy_rows(a.copy[k], a.experts, blockIdx.x * 256LL + threadIdx.x, gridDim.x * 256LL);
+  if (a.kept.dst != nullptr) copy_kept(a.kept, a.row_of, a.tokens * a.top_k, lane, me, warps);
   if (!a.fill) return;
   for (int i = me; i < a.experts * (kGroupRows - 1); i += warps) {  // the rows that only fill up
     const int e = i / (kGroupRows - 1), k = i - e * (kGroupRows - 1);
@@ -327,50 +379,6 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineArgs a) {
         for (int k = 0; k < 8; ++k)
           if (col + k < a.cols) o[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
       }
-    }
-  }
-}
-
-// dst[e][r][c] = src[e][r][c] for c < cols, 0 up to dst_cols.
-__global__ void __launch_bounds__(256) stage_kernel(uint16_t* dst, long long dst_cols, const uint16_t* src, long long ld,
-                                                    long long stride, long long experts, long long rows, long long cols) {
-  tc::pdl_launch_dependents();
-  tc::pdl_wait();
-  const long long per_row = dst_cols / 8, n = experts * rows * per_row, step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long g = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; g < n; g += step) {
-    const long long row = g / per_row, col = (g - row * per_row) * 8, e = row / rows;
-    *reinterpret_cast<uint4*>(dst + row * dst_cols + col) = row_piece8(src + e * stride + (row - e * rows) * ld + col, cols - col);
-  }
-}
-
-// The kept rows of the slots that have an expert, gate and up each from a 16-byte boundary on, zeros behind them
-// (the epilogue that reads them takes 16 bytes of a row at a time; rows that start anywhere, a lane each, would
-// take it 32 times as long). A warp takes a slot.
-template <typename Element>
-__global__ void __launch_bounds__(256) kept_kernel(const Element* kept, long long ld, long long hidden, const int* row_of, long long slots,
-                                                   uint8_t* out, long long part) {
-  tc::pdl_launch_dependents();
-  tc::pdl_wait();
-  constexpr int kSize = sizeof(Element), kPer = 16 / kSize;
-  const int lane = threadIdx.x & 31;
-  const long long step = static_cast<long long>(gridDim.x) * 8, pieces = 2 * part / 16;
-  for (long long s = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); s < slots; s += step) {
-    if (__ldcg(row_of + s) < 0) continue;
-#pragma unroll 4
-    for (long long p = lane; p < pieces; p += 32) {
-      const long long col = (p * 16 < part ? p : p - part / 16) * kPer;
-      const Element* const from = kept + s * ld + (p * 16 < part ? 0 : hidden) + col;
-      uint4 v;
-      if constexpr (kSize == 2) {
-        v = row_piece8(from, hidden - col);
-      } else {
-        uint32_t w[4] = {};
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (col + i < hidden) w[i / 4] |= static_cast<uint32_t>(__ldg(from + i)) << (8 * (i % 4));
-        v = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      *reinterpret_cast<uint4*>(out + s * 2 * part + 16 * p) = v;
     }
   }
 }
@@ -569,24 +577,22 @@ struct Call {
     return reinterpret_cast<T*>(ws + off);
   }
 
-  zopt_status copy(size_t off, long long pitch, const uint16_t* src, long long ld, long long stride, long long rows, long long cols,
-                   const uint16_t** to, long long* pitch_to, long long* stride_to) const {
+  void copy(GatherArgs& a, size_t off, long long pitch, const uint16_t* src, long long ld, long long stride, long long rows,
+            long long cols, const uint16_t** to, long long* pitch_to, long long* stride_to) const {
     uint16_t* d = at<uint16_t>(off);
     *to = d, *pitch_to = pitch, *stride_to = rows * pitch;
-    return launch_pdl(stage_kernel, dim3(blocks_for(c.experts * rows * (pitch / 8), sms)), dim3(256), 0, s, d, pitch, src, ld,
-                      stride, static_cast<long long>(c.experts), rows, cols);
+    a.copy[a.copies++] = Copy{d, src, pitch, ld, stride, rows, cols};
   }
   // The forward reads gate's and up's columns, the backward gate_up's rows whole.
-  zopt_status weights(bool backward, Weights& w) const {
+  Weights weights(bool backward, GatherArgs& a) const {
     const long long D = c.dim, F = c.hidden;
-    w = Weights{c.w_gate_up, c.w_gate_up + F, c.w_down, c.ld_gate_up, c.stride_gate_up, c.ld_gate_up, c.stride_gate_up,
-                c.ld_down, c.stride_down};
+    Weights w{c.w_gate_up, c.w_gate_up + F, c.w_down, c.ld_gate_up, c.stride_gate_up, c.ld_gate_up, c.stride_gate_up,
+              c.ld_down, c.stride_down};
     if (p.stage_gate)
-      TRY(copy(p.gate, p.gp, c.w_gate_up, c.ld_gate_up, c.stride_gate_up, D, backward ? 2 * F : F, &w.gate, &w.pg, &w.sg));
-    if (p.stage_up && !backward)
-      TRY(copy(p.up, p.fp, c.w_gate_up + F, c.ld_gate_up, c.stride_gate_up, D, F, &w.up, &w.pu, &w.su));
-    if (p.stage_down) TRY(copy(p.down, p.dp, c.w_down, c.ld_down, c.stride_down, F, D, &w.down, &w.pd, &w.sd));
-    return ok();
+      copy(a, p.gate, p.gp, c.w_gate_up, c.ld_gate_up, c.stride_gate_up, D, backward ? 2 * F : F, &w.gate, &w.pg, &w.sg);
+    if (p.stage_up && !backward) copy(a, p.up, p.fp, c.w_gate_up + F, c.ld_gate_up, c.stride_gate_up, D, F, &w.up, &w.pu, &w.su);
+    if (p.stage_down) copy(a, p.down, p.dp, c.w_down, c.ld_down, c.stride_down, F, D, &w.down, &w.pd, &w.sd);
+    return w;
   }
   zopt_status plan() const {
     const size_t smem = static_cast<size_t>(kPlanWarps + 1) * c.experts * 4;
@@ -596,8 +602,7 @@ struct Call {
     const PlanArgs a{c.index, c.weight, p.slots, c.experts, p.tile_rows, at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), at<int>(p.row_of)};
     return launch_pdl(plan_kernel, dim3(kPlanCtas), dim3(32 * kPlanWarps), smem, s, a);
   }
-  zopt_status gather(bool backward) const {
-    GatherArgs a{};
+  zopt_status gather(bool backward, GatherArgs& a) const {
     a.n = backward ? 2 : 1;
     a.from[0] = Source{c.x, c.ld_x, nullptr, nullptr, at<uint16_t>(p.xs)};
     if (c.x8 != nullptr) a.from[0] = Source{nullptr, 0, c.x8->q, c.x8->scale, at<uint16_t>(p.xs)};
@@ -605,7 +610,10 @@ struct Call {
     a.tokens = c.tokens, a.cols = c.dim, a.pitch = p.dp;
     a.row_of = at<int>(p.row_of), a.info = at<int2>(p.info);
     a.top_k = c.top_k, a.experts = c.experts, a.fill = backward;
-    return launch_pdl(gather_kernel, dim3(blocks_for(32 * a.n * c.tokens * ((p.dp + 1023) / 1024), sms)), dim3(256), 0, s, a);
+    long long threads = 32 * a.n * c.tokens * ((p.dp + 1023) / 1024);
+    for (int k = 0; k < a.copies; ++k) threads = std::max(threads, c.experts * a.copy[k].rows * (a.copy[k].dst_cols / 8));
+    if (a.kept.dst != nullptr) threads = std::max(threads, 32 * p.slots);
+    return launch_pdl(gather_kernel, dim3(blocks_for(threads, sms)), dim3(256), 0, s, a);
   }
   zopt_status combine(bool backward) const {
     CombineArgs a{};
@@ -644,28 +652,20 @@ struct Call {
       j.ld_kept = c.ld_kept;
     }
   }
-  zopt_status stage_kept(Job& j) const {
-    uint8_t* const to = at<uint8_t>(p.kept);
-    const int* const row_of = at<int>(p.row_of);
-    const dim3 grid(blocks_for(32 * p.slots, sms));
-    const long long hidden = c.hidden, ld = j.ld_kept;
-    j.kept = to;
-    if (c.kept8 != nullptr) {
-      j.ld_kept = 2 * p.kept_row, j.kept_up = p.kept_row;
-      return launch_pdl(kept_kernel<uint8_t>, grid, dim3(256), 0, s, static_cast<const uint8_t*>(c.kept8->q), ld, hidden, row_of, p.slots, to,
-                        p.kept_row);
-    }
-    j.ld_kept = p.kept_row, j.kept_up = p.kept_row / 2;
-    return launch_pdl(kept_kernel<uint16_t>, grid, dim3(256), 0, s, static_cast<const uint16_t*>(c.kept), ld, hidden, row_of, p.slots, to,
-                      p.kept_row);
+  // The kept rows where the epilogue can read them.
+  void stage_kept(Job& j, GatherArgs& a) const {
+    const int size = c.kept8 != nullptr ? 1 : 2;
+    a.kept = KeptCopy{at<uint8_t>(p.kept), j.kept, j.ld_kept, c.hidden, p.kept_row, size};
+    j.kept = a.kept.dst;
+    j.ld_kept = 2 * p.kept_row / size, j.kept_up = p.kept_row / size;
   }
 
   zopt_status forward() const {
     if (p.few) return few::experts_forward(c, at<float>(p.few_gate_up), at<float>(p.few_y), s);
-    Weights w;
+    GatherArgs rows{};
+    const Weights w = weights(false, rows);
     TRY(plan());
-    TRY(gather(false));
-    TRY(weights(false, w));
+    TRY(gather(false, rows));
     const long long D = c.dim, F = c.hidden;
     {
       Batch b{};
@@ -694,10 +694,9 @@ struct Call {
   }
 
   zopt_status backward() const {
-    Weights w;
+    GatherArgs rows{};
+    const Weights w = weights(true, rows);
     TRY(plan());
-    TRY(gather(true));
-    TRY(weights(true, w));
     const long long D = c.dim, F = c.hidden;
     uint16_t *const xs = at<uint16_t>(p.xs), *const dys = at<uint16_t>(p.dys), *const h = at<uint16_t>(p.h),
              *const dgu = at<uint16_t>(p.dgu);
@@ -707,7 +706,8 @@ struct Call {
       Job& j = b.job[0];
       group_job(j, p, kGluBwd, false, 0, F, D, c.experts);
       glu(j);
-      if (p.stage_kept) TRY(stage_kept(j));
+      if (p.stage_kept) stage_kept(j, rows);
+      TRY(gather(true, rows));
       TRY(map_rows(fn, j, &j.P, dys, p.rows, D, p.dp, 0, 64));
       TRY(map_weights(fn, j, &j.Q, w.down, F, D, w.pd, c.experts, w.sd, 0, j.tile_n / 2));
       j.out = dgu, j.ld_out = p.gp;
