@@ -453,3 +453,82 @@ def test_kept_rows_that_start_anywhere(zopt, case):
     b.forward(zopt)
     b.backward(zopt)
     b.check(zopt)
+
+
+@pytest.mark.parametrize("case", [(100, 16, 8, 1024, 4, "silu", "bf16", 0), (70, 24, 16, 40, 32, "gelu", "e4m3", 6), (9, 8, 16, 33, 32, "silu", "bf16", 0),
+                                  (2100, 8, 8, 2, 1, "silu", "bf16", 0)])
+def test_many_experts_and_many_slots(zopt, case):
+    b = Block(*case, seed=15)
+    b.forward(zopt)
+    b.backward(zopt)
+    b.check(zopt)
+
+
+def test_one_expert_is_the_dense_block(zopt):
+    """Every token to the one expert with weight 1: the dense block's bits but for its y (whose part carries 12 bits)."""
+    b = Block(300, 72, 136, 1, 1, "silu", "bf16", 0, seed=16)
+    b.weight.fill_(1.0)
+    b.forward(zopt)
+    b.backward(zopt)
+    y, kept, dx = torch.empty_like(b.y), torch.empty_like(b.kept), torch.empty_like(b.dx)
+    dwgu, dwd = torch.empty_like(b.wgu[0]), torch.empty_like(b.wd[0])
+    ws = zopt.new_ffn_workspace(b.x, b.wgu[0], b.wd[0])
+    zopt.ffn_forward(b.x, b.wgu[0], b.wd[0], y, ws, kept=kept)
+    zopt.ffn_backward(b.dy, b.x, kept, b.wgu[0], b.wd[0], dx, dwgu, dwd, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(kept, b.kept) and torch.equal(dwgu, b.dwgu[0]) and torch.equal(dwd, b.dwd[0])
+    for got, want in ((b.y, y), (b.dx, dx)):
+        assert bool(((got.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 1e-6).all())
+
+
+def test_rows_past_two_to_the_31(zopt):
+    """Kept gate and up of 2.3e9 bytes, slots and rows in the hundred thousands: tokens from both ends against the
+    formula."""
+    t, d, f, e, k = 270000, 16, 2144, 3, 2
+    g = torch.Generator(device="cuda").manual_seed(17)
+    new = lambda *s, sigma=1.0: (torch.randn(*s, generator=g, device="cuda") * sigma).bfloat16()  # noqa: E731
+    x, dy, wgu, wd = new(t, d), new(t, d), new(e, d, 2 * f, sigma=0.25), new(e, f, d, sigma=0.02)
+    index = torch.rand(t, e, generator=g, device="cuda").topk(k, dim=1).indices.int()
+    weight = torch.rand(t, k, generator=g, device="cuda")
+    kept = zopt.new_act8(t * k, 2 * f, parts=2)
+    assert kept.q.numel() > 1 << 31
+    ws = zopt.new_experts_workspace(x, index, wgu, wd)
+    y, dx, dweight, dwgu, dwd = torch.empty_like(x), torch.empty_like(x), torch.empty_like(weight), torch.empty_like(wgu), torch.empty_like(wd)
+    zopt.experts_forward(x, index, weight, wgu, wd, y, ws, kept=kept)
+    zopt.experts_backward(dy, x, index, weight, kept, wgu, wd, dx, dweight, dwgu, dwd, ws)
+    torch.cuda.synchronize()
+    assert zopt.take_device_error() == 0
+    pick = torch.cat((torch.arange(40), torch.arange(t - 40, t))).cuda()
+    n = lambda a: a[pick].cpu()  # noqa: E731
+    W, D = f64(wgu), f64(wd)
+    want, gu, size = OE.experts_forward(f64(n(x)), n(index).numpy(), f64(n(weight)), W, D, "silu")
+    close(n(y), want, OE.block_bound(want, size))
+    rows = (pick[:, None] * k + torch.arange(k, device="cuda")).flatten()
+    nb = lm.BLOCK
+    scale = kept.scale.view(t * k, -1)[rows].cpu().numpy()
+    values = lm.act8_unpack(kept.q[rows].cpu().numpy(), scale, 2)
+    top = np.abs(gu).max(axis=1, keepdims=True)
+    terms = np.abs(f64(n(x))).sum(1).repeat(k)[:, None] * np.abs(W).max()
+    assert (np.abs(values - gu) <= 2.0 ** -4 * np.abs(gu) + 2.0 ** -17 * top + 2.0 ** -13 * terms).all() and nb == 128
+    ref = OE.experts_backward(f64(n(dy)), f64(n(x)), n(index).numpy(), f64(n(weight)), values, W, D, "silu")
+    close(n(dx), ref["dx"][0], OE.block_bound(*ref["dx"]))
+    close(n(dweight), ref["dweight"][0], OE.dweight_bound(ref["dweight"][1], d, f))
+    # the gradients of the weights, in norm, from sums over pieces of the tokens
+    dgu_ref, dwd_ref = torch.zeros(e, d, 2 * f, dtype=torch.float64, device="cuda"), torch.zeros(e, f, d, dtype=torch.float64, device="cuda")
+    for c in range(0, t, 27000):
+        s = slice(c * k, (c + 27000) * k)
+        piece = zopt.Act8(kept.q[s], kept.scale.view(t * k, -1)[s].reshape(-1), 2)
+        v = torch.empty(27000 * k, 2 * f, dtype=torch.bfloat16, device="cuda")
+        zopt.act_unpack(piece, v)
+        flat = index[c:c + 27000].reshape(-1)
+        for i in range(e):
+            slots = (flat == i).nonzero()[:, 0]
+            r, w = c + slots // k, weight.reshape(-1)[c * k + slots][:, None]
+            gg, u = v[slots, :f].float(), v[slots, f:].float()
+            sg = torch.sigmoid(gg)
+            a, da = gg * sg, sg * (1 + gg * (1 - sg))
+            dh = dy[r].float() @ wd[i].float().t()
+            dgu_ref[i] += (x[r].float().t() @ (w * torch.cat((dh * u * da, dh * a), 1))).double()
+            dwd_ref[i] += ((w * a * u).t() @ dy[r].float()).double()
+    for got, want in ((dwgu, dgu_ref), (dwd, dwd_ref)):
+        assert float((got.double() - want).norm()) <= 3.2e-3 * float(want.norm())
