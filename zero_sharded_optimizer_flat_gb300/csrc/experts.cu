@@ -713,6 +713,7 @@ struct Call {
       j.out = dgu, j.ld_out = p.gp;
       j.out_h = h, j.ld_h = p.fp;
       j.dots = at<float>(p.dots), j.n_dots = p.dot_parts;
+      TRY(map_results(fn, b, p.rows));
       TRY(launch_grouped(fn, b, kGluBwd, p.tiles, s));
     }
     Batch b{};

@@ -326,6 +326,7 @@ zopt_status backward(const zopt_ffn_job* cp, void* d_ws, size_t ws_bytes, cudaSt
     j.ld_out = p.gp;
     j.out_h = h;
     j.ld_h = p.fp;
+    TRY(map_results(fn, b, c.tokens));
     TRY(launch(fn, b, kGluBwd, s));
   }
   Batch b{};

@@ -105,6 +105,24 @@ zopt_status map_up(const char* fn, Job& j, const void* base, long long columns, 
   return make_map(fn, &j.Up, base, columns, j.K, pitch, 64);
 }
 
+zopt_status map_results(const char* fn, Batch& b, long long rows) {
+  Job& j = b.job[0];
+  j.bulk = j.N % 8 == 0 && j.ld_out % 8 == 0 && j.ld_h % 8 == 0 && aligned16(j.out) && aligned16(j.out_h);
+  if (!j.bulk) return ok();
+  auto enc = ns::encode_fn();
+  if (enc == nullptr) return fail(ZOPT_ECUDA, std::string(fn) + ": cuTensorMapEncodeTiled is unavailable");
+  void* const base[3] = {j.out, static_cast<uint16_t*>(j.out) + j.N, j.out_h};
+  for (int k = 0; k < 3; ++k) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(j.N), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k == 2 ? j.ld_h : j.ld_out) * 2};
+    const cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+    const CUresult r = enc(&b.outs[k], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base[k], dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ZOPT_ECUDA, std::string(fn) + ": cuTensorMapEncodeTiled failed (" + std::to_string(r) + ")");
+  }
+  return ok();
+}
+
 void set_tiles(Job& j) {
   j.tiles_m = (j.M + kTileM - 1) / kTileM;
   j.nk = (j.K + kTileK - 1) / kTileK;

@@ -22,7 +22,6 @@ namespace lm {
 
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kPairs = 76;  // GB300's CTA pairs, what work is shared out for
-constexpr int kStages = 6;
 constexpr int kHalfBytes = 128 * kTileK * 2;  // one CTA's half of a stage's P or Q: 16 KiB
 constexpr int kMnBoxBytes = 64 * kTileK * 2;  // one 64 (MN) x 64 (K) box of an MN-major operand
 constexpr int kEpiWarps = 8;
@@ -30,8 +29,6 @@ constexpr int kFirstEpi = 3;  // warp 0 loads P, warp 1 issues the MMAs, warp 2 
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
 constexpr int kBoxBytes = 32 * 128;  // an epilogue warp's results on their way to memory: 32 rows of 128 bytes
 constexpr int kSwapBytes = 2 * 4 * 64 * 2;  // kGluFwd: the warps' block exponents, of tiles of 256 rows and of 128
-constexpr int kSmemBytes = kStages * 2 * kHalfBytes + kEpiWarps * kBoxBytes + kSwapBytes + 1024 + 256;
-static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr int kMaxJobs = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 // The longest inner length: an epilogue waits for a whole tile's products (those that are not cut) with a
@@ -48,6 +45,14 @@ enum Kind : int {
   kGluFwd = 8,  // h = a(gate) * up, gate and up kept
   kGluBwd = 16  // dgate, dup and h from dh
 };
+
+// kGluBwd holds a stage less and, of each warp, three results on their way to memory beside the box.
+__host__ __device__ constexpr int stages_of(int kinds) { return (kinds & kGluBwd) != 0 ? 5 : 6; }
+__host__ __device__ constexpr int box_bytes_of(int kinds) { return (kinds & kGluBwd) != 0 ? 2 * kBoxBytes : kBoxBytes; }
+__host__ __device__ constexpr int smem_of(int kinds) {
+  return stages_of(kinds) * 2 * kHalfBytes + kEpiWarps * box_bytes_of(kinds) + kSwapBytes + 1024 + 256;
+}
+static_assert(smem_of(kGluBwd) <= 232448 && smem_of(kGluFwd) <= 232448, "shared memory per CTA");
 
 enum OutMode : int { kOutBf16 = 0, kOutF32 = 1 };                   // kStore
 enum KeptMode : int { kKeepNone = 0, kKeepBf16 = 1, kKeep8 = 2 };  // kGluFwd, kGluBwd
@@ -92,6 +97,7 @@ struct Job {
   long long kept_up;    // from a row's gate to its up
   uint8_t* kept_scale;  // kKeep8: row r's block exponents at r * 2 blocks, the gate's first
   int hidden;           // the gate's width, N
+  int bulk;             // kGluBwd: the results leave through the batch's maps
   // grouped batches
   int by_inner;          // the experts' rows are the inner length (else the rows of D)
   long long out_stride;  // by_inner: elements between the experts' D
@@ -123,6 +129,7 @@ struct Batch {
   int listed;
   int* err;
   Job job[kMaxJobs];
+  CUtensorMap outs[3];  // kGluBwd, where bulk: dgate, dup and h
   uint16_t first[kPairs + 1];
   uint16_t order[kMaxListed];
   Groups groups;
@@ -136,6 +143,9 @@ struct Batch {
 zopt_status map_p(const char* fn, Job& j, const void* base, long long pitch);
 zopt_status map_q(const char* fn, Job& j, const void* base, long long columns, long long pitch);
 zopt_status map_up(const char* fn, Job& j, const void* base, long long columns, long long pitch);
+
+// The maps by which kGluBwd's results leave (rows of them), if they can: rows, and dup's first column, on 16 bytes.
+zopt_status map_results(const char* fn, Batch& b, long long rows);
 
 // Fills a job's tiling from kind, M, N, K, a_mn, b_mn and kept_mode.
 void set_tiles(Job& j);

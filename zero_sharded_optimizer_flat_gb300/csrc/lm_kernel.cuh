@@ -77,7 +77,11 @@ __device__ __forceinline__ bool elect_one() {
 // lanes at a time meet every bank once, whether they are eight rows' one piece, one row's eight, two
 // rows' four or four rows' two. (Through 2 KiB boxes handed to the TMA a tile of bf16 results took its
 // warps 6000 cycles, this way 3700.)
+// Boxes of 64-byte rows (kRow), which the TMA takes to memory, hold piece q at q ^ r', r' the row's bits 1 and 2: its
+// 64-byte swizzle. Eight lanes meet every bank once where they are eight rows' one piece.
+template <int kRow = 128>
 __device__ __forceinline__ uint32_t box_piece(uint32_t box, int row, int q) {
+  if constexpr (kRow == 64) return box + static_cast<uint32_t>(row * 64) + ((static_cast<uint32_t>(q) ^ (static_cast<uint32_t>(row >> 1) & 3u)) << 4);
   return box + static_cast<uint32_t>(row * 128) + ((static_cast<uint32_t>(q) ^ (__brev(static_cast<uint32_t>(row & 7)) >> 29)) << 4);
 }
 // Pieces q0 .. of the lane's row. (box is a multiple of 128.)
@@ -91,8 +95,9 @@ __device__ __forceinline__ void box_put(uint32_t box, int lane, int q0, const ui
                  : "memory");
 }
 
+template <int kRow = 128>
 __device__ __forceinline__ void box_put4(uint32_t box, int lane, int q, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_piece(box, lane, 0) ^ static_cast<uint32_t>(q << 4)), "r"(a),
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box_piece<kRow>(box, lane, 0) ^ static_cast<uint32_t>(q << 4)), "r"(a),
                "r"(b), "r"(c), "r"(d)
                : "memory");
 }
@@ -884,25 +889,40 @@ struct Kept {
       load_row(j, row0 + lane, row0 + lane < rows, col);
     }
   }
-  // What was loaded becomes the lane's row (through the warp's box).
+  // Piece q of a row of 64 bytes, where neither eight rows' one nor two pieces of four rows meet a bank twice.
+  static __device__ __forceinline__ uint32_t piece(uint32_t box, int row, int q) {
+    return box + static_cast<uint32_t>(row * 64) + ((static_cast<uint32_t>(q) ^ (__brev(static_cast<uint32_t>(row & 6)) >> 29)) << 4);
+  }
+  // What was loaded becomes the lane's row (through a box of 64-byte rows: both parts, or of bf16 one after the
+  // other).
   __device__ __forceinline__ void turn(uint32_t box, int lane) {
     if constexpr (kWide) {
+      constexpr int kParts = kKept == kKeep8 ? 2 : 1;  // at a time
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+      for (int p0 = 0; p0 < 2; p0 += kParts) {
 #pragma unroll
-        for (int i = 0; i < kPerRow; ++i)
-          box_put4(box, lane / kPerRow + i * kAtOnce, part * kPerRow + lane % kPerRow, x[part][4 * i], x[part][4 * i + 1],
-                   x[part][4 * i + 2], x[part][4 * i + 3]);
-      __syncwarp();
+        for (int part = 0; part < kParts; ++part)
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+          for (int i = 0; i < kPerRow; ++i) {
+            const uint32_t* const v = x[p0 + part] + 4 * i;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             piece(box, lane / kPerRow + i * kAtOnce, part * kPerRow + lane % kPerRow)),
+                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                         : "memory");
+          }
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kPerRow; ++i)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[part][4 * i]), "=r"(x[part][4 * i + 1]), "=r"(x[part][4 * i + 2]), "=r"(x[part][4 * i + 3])
-                       : "r"(box_piece(box, lane, part * kPerRow + i))
-                       : "memory");
-      __syncwarp();
+        for (int part = 0; part < kParts; ++part)
+#pragma unroll
+          for (int i = 0; i < kPerRow; ++i) {
+            uint32_t* const v = x[p0 + part] + 4 * i;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(piece(box, lane, part * kPerRow + i))
+                         : "memory");
+          }
+        __syncwarp();
+      }
     }
   }
   __device__ __forceinline__ void load_row(const Job& j, int row, bool there, int col) {
@@ -946,10 +966,19 @@ struct Scales {
 };
 
 // dgate = dh up a'(gate), dup = dh a(gate), h = a(gate) up, each rounded to bf16 once: they are
-// operands of the three products that follow. `k` holds the kept values of the warp's first 32
+// operands of the three products that follow, and leave by the TMA, a box of 32 rows and columns each. (This is
+// the longest epilogue, and what bounds it is the L1 data path, which the MMAs' operands and their copies keep
+// busy: boxes read back and stored row by row took BULK_BEFORE us for BULK_AFTER, 8192 x 6 slots of 2048 x 1408, 8 bits
+// kept; sixteen warps in eight's place changed nothing.) `k` holds the kept values of the warp's first 32
 // columns; while 32 columns are worked on the next ones are on their way, at a tile's end the next
 // tile's first (from row next_row0 and column next_col on): gate and up come from HBM, and a tile that
 // began by waiting for them would take longer than its products.
+constexpr int kTurnBytes = 32 * 64;  // a box of 32 rows of 64 bytes
+__device__ __forceinline__ void store_box(const CUtensorMap* m, uint32_t box, int col, int row) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(box), "r"(col), "r"(row)
+               : "memory");
+}
+
 // Grouped, dg, du and h carry the row's weight, and the weight's own gradient, the sum over the columns
 // of dh h without it, leaves in parts.
 struct Next {  // the tile after this one
@@ -958,11 +987,13 @@ struct Next {  // the tile after this one
 };
 template <int kAct, int kKept, bool kWide, bool kGrouped>
 __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const Part& part, const Acc& acc, const Row& mine, int lane,
-                                            uint32_t box, Kept<kKept, kWide, kGrouped>& k, Scales& sc, const Next& n) {
+                                            uint32_t box, const CUtensorMap* maps, Kept<kKept, kWide, kGrouped>& k, Scales& sc,
+                                            const Next& n) {
   const int row0 = part.row0, width = part.width, col0 = part.col;
   const Out<64> dgate(j.out, j.ld_out, 2, row0, w.rows, col0, j.N, lane);
   const Out<64> dup(static_cast<uint16_t*>(j.out) + j.N, j.ld_out, 2, row0, w.rows, col0, j.N, lane);
   const Out<64> hout(j.out_h, j.ld_h, 2, row0, w.rows, col0, j.N, lane);
+  const uint32_t out = box + kTurnBytes;  // the results' boxes, one after another
   Scales next_sc;
   if constexpr (kKept == kKeep8)
     next_sc.load(j, kGrouped ? n.mine.slot : n.row0 + lane, kGrouped ? n.mine.slot >= 0 : n.row0 + lane < n.rows, n.col);
@@ -979,6 +1010,10 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const P
     next.load(j, last ? n.row0 : row0, last ? n.rows : w.rows, last ? n.mine.slot : mine.slot, last ? n.col : col + 32, lane);
     if (col < j.N && row0 < w.rows) {
       k.turn(box, lane);
+      if (j.bulk) {  // (the boxes' last contents have been read)
+        if (lane == 0) tc::bulk_wait_read<0>();
+        __syncwarp();
+      }
       if (kGrouped && mine.slot < 0) {  // a row of zeros, whatever the weights hold
 #pragma unroll
         for (int p = 0; p < 32; ++p) v[p] = 0u;
@@ -1004,17 +1039,33 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const P
           du[i] = pack2(d * a);
           hh[p] = pack2(au);
         }
-        box_put4(box, lane, q, dg[0], dg[1], dg[2], dg[3]);  // a row's 32 dgates, then its 32 dups
-        box_put4(box, lane, 4 + q, du[0], du[1], du[2], du[3]);
+        if (j.bulk) {
+          box_put4<64>(out, lane, q, dg[0], dg[1], dg[2], dg[3]);
+          box_put4<64>(out + kTurnBytes, lane, q, du[0], du[1], du[2], du[3]);
+          box_put4<64>(out + 2 * kTurnBytes, lane, q, hh[4 * q], hh[4 * q + 1], hh[4 * q + 2], hh[4 * q + 3]);
+        } else {
+          box_put4(out, lane, q, dg[0], dg[1], dg[2], dg[3]);  // a row's 32 dgates, then its 32 dups
+          box_put4(out, lane, 4 + q, du[0], du[1], du[2], du[3]);
+        }
       }
-      __syncwarp();
-      dgate.template put<0>(box, lane, 64 * c);
-      dup.template put<64>(box, lane, 64 * c);
-      __syncwarp();
-      box_put(box, lane, 0, hh);
-      __syncwarp();
-      hout.template put<0>(box, lane, 64 * c);
-      __syncwarp();
+      if (j.bulk) {
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int r = 0; r < 3; ++r) store_box(&maps[r], out + r * kTurnBytes, col, row0);
+          tc::bulk_commit();
+        }
+      } else {
+        __syncwarp();
+        dgate.template put<0>(out, lane, 64 * c);
+        dup.template put<64>(out, lane, 64 * c);
+        __syncwarp();
+        box_put(out, lane, 0, hh);
+        __syncwarp();
+        hout.template put<0>(out, lane, 64 * c);
+        __syncwarp();
+      }
     }
     if (kGrouped && (c & 1) != 0) {  // a part for every 64 columns
       const float2 two = f2(dot);
@@ -1031,12 +1082,13 @@ __device__ __forceinline__ void epi_glu_bwd(const Job& j, const Unit& w, const P
 template <int kKinds, int kAct, int kKept, bool kWide, bool kGrouped>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_gemm_kernel(const __grid_constant__ Batch B) {
+  constexpr int kStages = stages_of(kKinds), kBox = box_bytes_of(kKinds);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kHalfBytes;
   uint8_t* sEpi = sB + kStages * kHalfBytes;
-  uint16_t* sSwap = reinterpret_cast<uint16_t*>(sEpi + kEpiWarps * kBoxBytes);
+  uint16_t* sSwap = reinterpret_cast<uint16_t*>(sEpi + kEpiWarps * kBox);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sSwap) + kSwapBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
@@ -1201,7 +1253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int half = (warp - kFirstEpi) >> 2;   // and takes this half of the columns
     const uint32_t tempty_leader[2] = {tc::map_to_rank(tc::smem_u32(tempty), 0),
                                        tc::map_to_rank(tc::smem_u32(tempty + 1), 0)};
-    const uint32_t box = tc::smem_u32(sEpi) + (warp - kFirstEpi) * kBoxBytes;
+    const uint32_t box = tc::smem_u32(sEpi) + (warp - kFirstEpi) * kBox;
     uint16_t* swap = sSwap + 64 * quad;
     // a tile's columns of D (kGluFwd: hidden ones)
     auto columns = [](const Job& j) { return (kKinds & kGluFwd) == 0 ? j.tile_n : kKept == kKeep8 ? 128 : j.tile_n >> 1; };
@@ -1254,11 +1306,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr ((kKinds & kGluFwd) != 0)
         epi_glu_fwd<kAct, kKept, kGrouped>(j, w, part, acc, mine, lane, half, box, swap, quad);
       if constexpr ((kKinds & kGluBwd) != 0) {
-        epi_glu_bwd<kAct, kKept, kWide, kGrouped>(j, w, part, acc, mine, lane, box, kept, scales, next);
+        epi_glu_bwd<kAct, kKept, kWide, kGrouped>(j, w, part, acc, mine, lane, box, B.outs, kept, scales, next);
         mine = next.mine;
       }
     }
   }
+  if ((kKinds & kGluBwd) != 0 && warp >= kFirstEpi && lane == 0) tc::bulk_wait_all();  // results on their way out of the boxes
   tc::fence_before_sync();
   tc::cluster_sync();  // every MMA, copy and remote arrival of the pair is done
   if (*reinterpret_cast<volatile uint32_t*>(gave_up) != 0) settle();
@@ -1271,8 +1324,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 template <bool kGrouped, int kKinds, int kAct = 0, int kKept = kKeepNone, bool kWide = true>
 zopt_status launch_kinds(Batch& b, dim3 grid, cudaStream_t s) {
   const auto kernel = lm_gemm_kernel<kKinds, kAct, kKept, kWide, kGrouped>;
-  ZOPT_CUDA_TRY(once_per_device([=] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes); }));
-  return launch_pdl(kernel, grid, dim3(kThreads), static_cast<size_t>(kSmemBytes), s, b);
+  ZOPT_CUDA_TRY(once_per_device([=] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kKinds)); }));
+  return launch_pdl(kernel, grid, dim3(kThreads), static_cast<size_t>(smem_of(kKinds)), s, b);
 }
 template <bool kGrouped, int kAct>
 zopt_status launch_glu(Batch& b, dim3 grid, cudaStream_t s) {
