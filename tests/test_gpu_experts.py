@@ -532,3 +532,31 @@ def test_rows_past_two_to_the_31(zopt):
             dwd_ref[i] += ((w * a * u).t() @ dy[r].float()).double()
     for got, want in ((dwgu, dgu_ref), (dwd, dwd_ref)):
         assert float((got.double() - want).norm()) <= 3.2e-3 * float(want.norm())
+
+
+@pytest.mark.parametrize("case", [(60, 40, 24, 4, 2, "silu", "bf16", 3), (4, 40, 24, 4, 2, "gelu", "e4m3", 0)])
+@pytest.mark.parametrize("gap", [8, 3])
+def test_matrices_any_distance_apart(zopt, case, gap):
+    """Strides that are no multiple of the rows' distance, of the weights and of their gradients."""
+    b = Block(*case, seed=18)
+
+    def apart(a):
+        n, r, c = a.shape
+        flat = torch.full((n * (r * c + gap) + 8,), SENTINEL, dtype=a.dtype, device="cuda")
+        v = flat.as_strided((n, r, c), (r * c + gap, c, 1))
+        v.copy_(a)
+        return flat, v
+
+    b.wgu, b.wd = apart(b.wgu)[1], apart(b.wd)[1]
+    b.forward(zopt)
+    b.backward(zopt)
+    b.check(zopt)
+    (flat_a, a), (flat_b, c) = apart(torch.zeros_like(b.dwgu)), apart(torch.zeros_like(b.dwd))
+    ws = zopt.new_experts_workspace(b.x, b.index, b.wgu, b.wd)
+    zopt.experts_backward(b.dy, b.x, b.index, b.weight, b.kept, b.wgu, b.wd, b.dx, b.dweight, a, c, ws, act=b.act)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b.dwgu) and torch.equal(c, b.dwd)
+    for flat, v in ((flat_a, a), (flat_b, c)):
+        keep = torch.ones_like(flat, dtype=torch.bool)
+        keep.as_strided(v.shape, v.stride()).fill_(False)
+        assert bool((flat[keep] == SENTINEL).all())

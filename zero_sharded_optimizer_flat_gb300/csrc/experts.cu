@@ -453,9 +453,10 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   // of 256 x 768 in eight experts: 37 us for 45, with the rounds of units in turn and back).
   p.tile_rows = (p.slots / kTileM + (used + 1) / 2) * ((F + kTileN - 1) / kTileN) <= kPairs ? kTileM / 2 : kTileM;
   p.tiles = p.slots / p.tile_rows + used;
-  p.stage_gate = c.ld_gate_up % 8 != 0 || (E > 1 && c.stride_gate_up % 8 != 0);
+  // (a tensor map's strides are multiples of 16 bytes, and the outer one of the inner)
+  p.stage_gate = c.ld_gate_up % 8 != 0 || (E > 1 && c.stride_gate_up % c.ld_gate_up != 0);
   p.stage_up = p.stage_gate || F % 8 != 0;  // (the forward reads up's columns from column hidden on)
-  p.stage_down = c.ld_down % 8 != 0 || (E > 1 && c.stride_down % 8 != 0);
+  p.stage_down = c.ld_down % 8 != 0 || (E > 1 && c.stride_down % c.ld_down != 0);
   size_t at = 0;
   p.head = take(at, 8);
   p.tile = take(at, 16 * p.tiles);
@@ -629,7 +630,7 @@ struct Call {
   void begin(Batch& b, int n) const {
     b.err = err;
     b.n = n;
-    b.groups = Groups{at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), c.experts};
+    b.groups = Groups{at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), c.experts, static_cast<int>(p.tiles)};
   }
   void parts(Job& j) const {
     j.out = at<uint16_t>(p.parts);

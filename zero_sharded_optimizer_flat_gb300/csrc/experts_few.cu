@@ -206,7 +206,7 @@ bool takes(const zopt_experts_job& c) {
   const ExpertPlan p = plan_of(c);
   if (p.splits > 65535 || p.parts > 65535) return false;  // (a grid's second dimension)
   const bool in_place = c.ld_gate_up % 8 == 0 && c.ld_down % 8 == 0 && c.hidden % 8 == 0 &&
-                        (c.experts == 1 || (c.stride_gate_up % 8 == 0 && c.stride_down % 8 == 0));
+                        (c.experts == 1 || (c.stride_gate_up % c.ld_gate_up == 0 && c.stride_down % c.ld_down == 0));
   const double mb = 6e-6 * static_cast<double>(c.dim) * static_cast<double>(c.hidden);
   double missed = 1.0;  // an expert's chance not to be named
   for (long long i = 0; i < slots; ++i) missed *= 1.0 - 1.0 / c.experts;

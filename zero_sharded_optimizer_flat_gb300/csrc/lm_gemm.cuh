@@ -115,7 +115,7 @@ struct Groups {
   const int4* tiles;  // a row tile's expert, first row, where its expert's rows (with the zeros) end, and 1 for at most 128 rows
   const int2* info;   // an expert's first row and its number of rows (without the zeros)
   const int2* row;    // a row's slot (-1: zeros) and its weight's bits
-  int experts;
+  int experts, most_tiles;  // (row tiles that there can be)
 };
 
 // Units of work are numbered job by job, a job's runs of k one after another. Pair p takes units p,

@@ -268,12 +268,13 @@ __device__ __forceinline__ Part part_of_tile(const Unit& w, int width, uint32_t 
                 w.tj * width + (width >> 1) * (quad >> 1) + (width >> 2) * h, width >> 2};
   return Part{w.row0 + static_cast<int>(rank) * 128 + 32 * quad, (width >> 1) * h, w.tj * width + (width >> 1) * h, width >> 1};
 }
+// (tile: grouped, by rows: the unit's row tile, where it has been read already)
 template <bool kGrouped>
-__device__ __forceinline__ Unit unit_of(const Batch& B, const Job& j, int u) {
+__device__ __forceinline__ Unit unit_of(const Batch& B, const Job& j, int u, const int4* tile = nullptr) {
   Unit w;
   if (kGrouped && !j.by_inner) {  // columns of a row tile one after another
     const int line = static_cast<int>(j.per_line(static_cast<uint32_t>(u)));
-    const int4 t = __ldcg(B.groups.tiles + line);
+    const int4 t = tile != nullptr ? *tile : __ldcg(B.groups.tiles + line);
     w.tj = u - line * j.tiles_n;
     w.split = 0, w.kb0 = 0, w.kb1 = j.nk;
     w.expert = t.x, w.row0 = t.y, w.rows = t.z, w.krow = 0;
@@ -313,8 +314,10 @@ __device__ __forceinline__ int unit_at(const Batch& b, int pair, int npairs, int
 template <bool kGrouped>
 struct Starts {
   int at[kMaxJobs + 1];
-  __device__ __forceinline__ explicit Starts(const Batch& b) {
+  int4 tile0;  // the pair's first unit's row tile, on its way beside their number (job 0 is by rows)
+  __device__ __forceinline__ Starts(const Batch& b, int pair) {
     if constexpr (kGrouped) {  // (as many row tiles as the tokens' choices made)
+      tile0 = __ldcg(b.groups.tiles + min(static_cast<int>(b.job[0].per_line(static_cast<uint32_t>(pair))), b.groups.most_tiles - 1));
       const int tiles = __ldcg(b.groups.head);
       at[0] = 0;
 #pragma unroll
@@ -329,6 +332,7 @@ struct Starts {
     while (j + 1 < b.n && t >= b.start[j + 1]) ++j;
     return j;
   }
+  __device__ __forceinline__ const int4* tile(int job, int i) const { return kGrouped && job == 0 && i == 0 ? &tile0 : nullptr; }
   __device__ __forceinline__ int start(const Batch& b, int j) const {
     if constexpr (kGrouped) return j == 0 ? 0 : j == 1 ? at[1] : at[2];
     return b.start[j];
@@ -1130,7 +1134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::pdl_launch_dependents();
   tc::pdl_wait();  // the previous launch's outputs are complete and visible
 
-  const Starts<kGrouped> starts(B);
+  const Starts<kGrouped> starts(B, pair);
   const int total = starts.total(B);
   int* const err = B.err;
   const uint32_t full0 = tc::smem_u32(full), empty0 = tc::smem_u32(empty);
@@ -1150,7 +1154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int i = 0, t; ok && (t = unit_at<kGrouped>(B, pair, npairs, i)) < total; ++i) {
         const int ji = starts.job(B, t);
         const Job& j = B.job[ji];
-        const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
+        const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji), starts.tile(ji, i));
         const bool up = (kKinds & kGluFwd) != 0 && !leader;  // one CTA has the gate's columns, the other up's
         const CUtensorMap* const map = is_p ? &j.P : up ? &j.Up : &j.Q;
         const bool mn = (is_p ? j.a_mn : j.b_mn) != 0;
@@ -1206,7 +1210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t; ok && (t = unit_at<kGrouped>(B, pair, npairs, it)) < total; ++it) {
         const int ji = starts.job(B, t);
         const Job& j = B.job[ji];
-        const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
+        const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji), starts.tile(ji, it));
         const bool amn = j.a_mn != 0, bmn = j.b_mn != 0;
         const uint32_t idesc = tc::idesc_bf16_f32(kGrouped && w.half ? 128 : kTileM, j.tile_n, amn, bmn);
         // a stage's descriptors differ in the address alone (16-byte units), and so do a stage's steps
@@ -1283,7 +1287,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++it;
       const int ji = starts.job(B, t);
       const Job& j = B.job[ji];
-      const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji));
+      const Unit w = unit_of<kGrouped>(B, j, t - starts.start(B, ji), starts.tile(ji, it - 1));
       const Part part = part_of_tile<kGrouped>(w, columns(j), rank, quad, half);
       const int row0 = part.row0;
       Next next{};
