@@ -9,6 +9,10 @@
 //   3. y = the sum of a token's slots' parts.
 // Everything is added in a fixed order. A slot without an expert reads and writes nothing. An expert that
 // several slots name is read for each, from L2 as a rule.
+//
+// One token through six of 64 experts, 2048 x 1408 (104 MB): 25.5 us = 4.1 TB/s; the launches by themselves 18.5
+// (4.9 TB/s with the prefetched matrices), 12.8 and 6.8. Without the prefetch and with CTAs of 128 hidden columns
+// 33.4; on the tensor cores 45.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -19,7 +23,6 @@
 #include "f2.cuh"
 #include "few.cuh"
 #include "launch.cuh"
-#include "per_device.h"
 #include "tc.cuh"
 
 namespace zopt {

@@ -10,6 +10,10 @@
 // other accumulator into the operator's outputs meanwhile. A lane holds whole row pieces, so softmax
 // statistics and the 8-bit blocks need no exchange between lanes.
 //
+// A grouped batch (kGrouped) has the rows of many experts one after another: its units are found through
+// tables in device memory (Groups in lm_gemm.cuh), weights come through maps with the expert as a third
+// coordinate, and a tile of at most 128 rows takes the pair's M = 128 MMA.
+//
 // Bound by the tensor cores where the inner length is long enough to hide a tile's epilogue (12 to 30
 // k-blocks' time): 521 cycles a k-block of 512, tensor pipe 92 % of elapsed in the cross entropy's
 // forward (4096 x 768 x 50304), 89 % in the block's first product and 90 % in its backward's second
@@ -972,8 +976,8 @@ struct Scales {
 // dgate = dh up a'(gate), dup = dh a(gate), h = a(gate) up, each rounded to bf16 once: they are
 // operands of the three products that follow, and leave by the TMA, a box of 32 rows and columns each. (This is
 // the longest epilogue, and what bounds it is the L1 data path, which the MMAs' operands and their copies keep
-// busy: boxes read back and stored row by row took BULK_BEFORE us for BULK_AFTER, 8192 x 6 slots of 2048 x 1408, 8 bits
-// kept; sixteen warps in eight's place changed nothing.) `k` holds the kept values of the warp's first 32
+// busy: with boxes read back and stored row by row the experts' whole backward of 8192 x 6 slots, 2048 x 1408, 8
+// bits kept, took 1480 us for 1452; sixteen warps in eight's place changed nothing.) `k` holds the kept values of the warp's first 32
 // columns; while 32 columns are worked on the next ones are on their way, at a tile's end the next
 // tile's first (from row next_row0 and column next_col on): gate and up come from HBM, and a tile that
 // began by waiting for them would take longer than its products.
