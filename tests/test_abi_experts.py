@@ -147,3 +147,15 @@ def test_python_refusals():
         Z.experts_workspace(x, index, torch.zeros(3, 8, 10, dtype=torch.bfloat16), wd)
     with pytest.raises(ValueError, match="GPU"):
         Z.route_forward(torch.zeros(4, 3), index, torch.zeros(4, 2))
+
+
+@pytest.mark.parametrize("packer,job", [(Z._ROUTE_JOB, Z._RouteJob), (Z._EXPERTS_JOB, Z._ExpertsJob)])
+def test_packed_jobs_have_the_structs_layout(packer, job):
+    """The calls pack a job's fields in their order: each value lands in its field."""
+    n = len(packer.unpack(bytes(packer.size)))
+    j = job.from_buffer_copy(packer.pack(*range(1, n + 1)))
+    names = [name for name, _ in job._fields_ if name != "reserved"]
+    assert len(names) == n and packer.size == ctypes.sizeof(job)
+    for k, name in enumerate(names, 1):
+        v = getattr(j, name)
+        assert (ctypes.cast(v, ctypes.c_void_p).value if isinstance(v, ctypes._Pointer) else v) == k, name

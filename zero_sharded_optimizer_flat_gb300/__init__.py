@@ -649,16 +649,22 @@ def _on_device(*tensors) -> None:
 
 
 I64, I32, U8 = 64, 65, 66  # not zopt_dtypes: no matrix may have them
-_CODES = {}
+
+
+class _Codes(dict):
+    def __missing__(self, dtype):  # (filled on the first call)
+        import torch
+        self.update({torch.float32: F32, torch.bfloat16: BF16, torch.int64: I64, torch.int32: I32, torch.uint8: U8,
+                     torch.bool: U8})
+        return self.setdefault(dtype, -1)
+
+
+_CODES = _Codes()
 
 
 def _code(t) -> int:
-    """_dtype_code from a table (filled on the first call)."""
-    if not _CODES:
-        import torch
-        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int64: I64, torch.int32: I32, torch.uint8: U8,
-                       torch.bool: U8})
-    return _CODES.get(t.dtype, -1)
+    """_dtype_code from a table."""
+    return _CODES[t.dtype]
 
 
 def _matrix(t, rows: int, cols: int, name: str):
@@ -814,8 +820,10 @@ _ELEMENTS = {F32: "fp32", I32: "int32", U8: "bool or byte"}
 
 
 def _array(t, shape, code: int, name: str):
-    """The address of a contiguous array on the GPU."""
-    if t.shape != shape or not t.is_contiguous() or not t.is_cuda or _code(t) != code:
+    """The address of a contiguous array on the GPU; 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != shape or not t.is_contiguous() or not t.is_cuda or _CODES[t.dtype] != code:
         raise ValueError(f"{name} must be a contiguous {_ELEMENTS[code]} array of {' x '.join(map(str, shape))} on the GPU")
     return t.data_ptr()
 
@@ -836,6 +844,9 @@ def _one_device(*tensors) -> None:
             raise ValueError(f"tensors must be on the current device, cuda:{here}")
 
 
+_ROUTE_JOB = struct.Struct("=q6ifiQqQQQQQQQq8x")  # zopt_route_job
+
+
 def _route_job(logits, index, weight, counts, bias, live, score, groups, top_groups, renormalise, scale, dweight=None,
                dlogits=None) -> _RouteJob:
     tokens, experts = logits.shape
@@ -844,18 +855,18 @@ def _route_job(logits, index, weight, counts, bias, live, score, groups, top_gro
     dtype = _code(logits)
     if dtype != F32 and dtype != BF16:
         dtype = -1
-    pd = ld = None
+    pd = ld = 0
     if dlogits is not None:
         pd, ld = _matrix(dlogits, tokens, experts, "dlogits")
         if _code(dlogits) != dtype:
             dtype = -1
-    j = _RouteJob(
+    # (packing a job costs a small call a fifth of what filling its fields does)
+    j = _RouteJob.from_buffer_copy(_ROUTE_JOB.pack(
         tokens, experts, top_k, groups, top_groups, _SCORES.get(score, score if isinstance(score, int) else -1),
         1 if renormalise else 0, scale, dtype, *_matrix(logits, tokens, experts, "logits"),
-        None if bias is None else _array(bias, (experts,), F32, "bias"), None if live is None else _array(live, (tokens,), U8, "live"),
-        _array(index, slots, I32, "index"), _array(weight, slots, F32, "weight"),
-        None if counts is None else _array(counts, (experts,), I32, "counts"),
-        None if dweight is None else _array(dweight, slots, F32, "dweight"), pd, ld or 0)
+        _array(bias, (experts,), F32, "bias"), _array(live, (tokens,), U8, "live"), _array(index, slots, I32, "index"),
+        _array(weight, slots, F32, "weight"), _array(counts, (experts,), I32, "counts"), _array(dweight, slots, F32, "dweight"),
+        pd, ld))
     _one_device(logits, index, weight, counts, bias, live, dweight, dlogits)
     return j
 
@@ -888,6 +899,9 @@ def _stack(t, n: int, rows: int, cols: int, name: str):
     return t.data_ptr(), ld, stride if n > 1 else rows * ld
 
 
+_EXPERTS_JOB = struct.Struct("=qqq4iQQQqqQqqQqQQqQQqQqQqQQqqQqq")  # zopt_experts_job
+
+
 def _experts_job(x, index, weight, w_gate_up, w_down, act, kept=None, y=None, dy=None, dx=None, dweight=None,
                  dw_gate_up=None, dw_down=None) -> _ExpertsJob:
     experts, hidden, dim = w_down.shape
@@ -895,39 +909,43 @@ def _experts_job(x, index, weight, w_gate_up, w_down, act, kept=None, y=None, dy
     wgu = _stack(w_gate_up, experts, dim, 2 * hidden, "w_gate_up")
     wd = _stack(w_down, experts, hidden, dim, "w_down")
     dtype = _same_dtype(w_gate_up, w_down)
+    x8, kept8, kp = None, None, (0, 0)
     if isinstance(x, Act8):
-        rows, xp, x8 = x.rows, (None, 0), ctypes.pointer(x._c)
+        rows, xp, x8, x = x.rows, (0, 0), x._c, x.q
     else:
-        rows, x8 = x.shape[0], None
+        rows = x.shape[0]
         xp = _matrix(x, rows, dim, "x")
         if _code(x) != dtype:
             dtype = -1
     slots = (rows, top_k)
-    j = _ExpertsJob(rows, dim, hidden, experts, top_k, _ACTS.get(act, act if isinstance(act, int) else -1), dtype,
-                    _array(index, slots, I32, "index"), None if weight is None else _array(weight, slots, F32, "weight"),
-                    *wgu, *wd, *xp, x8)
     if isinstance(kept, Act8):
-        j.kept8 = ctypes.pointer(kept._c)
+        kept8, kept = kept._c, kept.q
     elif kept is not None:
         if _code(kept) != BF16:
             raise ValueError("kept must be bf16 or an Act8")
-        j.kept, j.ld_kept = _matrix(kept, rows * top_k, 2 * hidden, "kept")
+        kp = _matrix(kept, rows * top_k, 2 * hidden, "kept")
+    more = []
     for t, name in ((y, "y"), (dy, "dy"), (dx, "dx")):
-        if t is not None:
-            p, ld = _matrix(t, rows, dim, name)
-            setattr(j, name, p)
-            setattr(j, "ld_" + name, ld)
+        if t is None:
+            more += (0, 0)
+        else:
+            more += _matrix(t, rows, dim, name)
             if _code(t) != dtype:
-                j.dtype = -1
-    if dweight is not None:
-        j.dweight = _array(dweight, slots, F32, "dweight")
+                dtype = -1
+    gradients = (0, 0, 0, 0, 0, 0)
     if dw_gate_up is not None:
-        j.dw_gate_up, j.ld_dw_gate_up, j.stride_dw_gate_up = _stack(dw_gate_up, experts, dim, 2 * hidden, "dw_gate_up")
-        j.dw_down, j.ld_dw_down, j.stride_dw_down = _stack(dw_down, experts, hidden, dim, "dw_down")
+        gradients = (*_stack(dw_gate_up, experts, dim, 2 * hidden, "dw_gate_up"), *_stack(dw_down, experts, hidden, dim, "dw_down"))
         if _same_dtype(dw_gate_up, dw_down) != dtype:
-            j.dtype = -1
-    _one_device(x.q if x8 is not None else x, index, weight, w_gate_up, w_down, kept.q if isinstance(kept, Act8) else kept, y, dy, dx,
-                dweight, dw_gate_up, dw_down)
+            dtype = -1
+    j = _ExpertsJob.from_buffer_copy(_EXPERTS_JOB.pack(
+        rows, dim, hidden, experts, top_k, _ACTS.get(act, act if isinstance(act, int) else -1), dtype,
+        _array(index, slots, I32, "index"), _array(weight, slots, F32, "weight"), *wgu, *wd, *xp, 0, *kp, 0, *more,
+        _array(dweight, slots, F32, "dweight"), *gradients))
+    if x8 is not None:
+        j.x8 = ctypes.pointer(x8)
+    if kept8 is not None:
+        j.kept8 = ctypes.pointer(kept8)
+    _one_device(x, index, weight, w_gate_up, w_down, kept, y, dy, dx, dweight, dw_gate_up, dw_down)
     return j
 
 
