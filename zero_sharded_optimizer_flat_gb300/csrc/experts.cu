@@ -619,6 +619,7 @@ struct Call {
     long long threads = 32 * a.n * c.tokens * ((p.dp + 1023) / 1024);
     for (int k = 0; k < a.copies; ++k) threads = std::max(threads, c.experts * a.copy[k].rows * (a.copy[k].dst_cols / 8));
     if (a.kept.dst != nullptr) threads = std::max(threads, 32 * p.slots);
+    if (backward) threads = std::max(threads, 32 * (kGroupRows - 1) * std::min<long long>(c.experts, p.slots));  // a warp a row to fill up
     return launch_pdl(gather_kernel, dim3(blocks_for(threads, sms)), dim3(256), 0, s, a);
   }
   zopt_status combine(bool backward) const {
