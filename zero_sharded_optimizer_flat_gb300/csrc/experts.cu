@@ -85,7 +85,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
 #pragma unroll
   for (int k = 0; k < kPlanKept; ++k) {
     const long long s = s0 + 32 * k + lane;
-    kept[k] = s < s1 ? __ldg(a.index + s) : -1;
+    kept[k] = s < s1 ? a.index[s] : -1;
   }
 #pragma unroll
   for (int k = 0; k < kPlanKept; ++k) {
@@ -167,7 +167,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
   };
   float weight[kPlanKept];
 #pragma unroll
-  for (int k = 0; k < kPlanKept; ++k) weight[k] = kept[k] >= 0 && kept[k] < E ? __ldg(a.weight + s0 + 32 * k + lane) : 0.0f;
+  for (int k = 0; k < kPlanKept; ++k) weight[k] = kept[k] >= 0 && kept[k] < E ? a.weight[s0 + 32 * k + lane] : 0.0f;
 #pragma unroll
   for (int k = 0; k < kPlanKept; ++k) {
     if (s0 + 32 * k >= s1) break;
@@ -255,7 +255,7 @@ __device__ __forceinline__ void copy_kept(const KeptCopy& c, const int* row_of, 
         uint32_t w[4] = {};
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-          if (col + i < c.hidden) w[i / 4] |= static_cast<uint32_t>(__ldg(static_cast<const uint8_t*>(c.src) + at + i)) << (8 * (i % 4));
+          if (col + i < c.hidden) w[i / 4] |= static_cast<uint32_t>(static_cast<const uint8_t*>(c.src)[at + i]) << (8 * (i % 4));
         v = make_uint4(w[0], w[1], w[2], w[3]);
       }
       *reinterpret_cast<uint4*>(c.dst + s * 2 * c.part + 16 * p) = v;

@@ -71,17 +71,17 @@ __device__ __forceinline__ void load_row(const Args& a, long long row, int first
       if constexpr (V >= 8) {
 #pragma unroll
         for (int q = 0; q < V / 8; ++q) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p) + q);
+          const uint4 x = reinterpret_cast<const uint4*>(p)[q];
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) l[8 * q + 2 * k] = __uint_as_float(w[k] << 16), l[8 * q + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
         }
       } else if constexpr (V == 4) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
         l[0] = __uint_as_float(x.x << 16), l[1] = __uint_as_float(x.x & 0xFFFF0000u);
         l[2] = __uint_as_float(x.y << 16), l[3] = __uint_as_float(x.y & 0xFFFF0000u);
       } else if constexpr (V == 2) {
-        const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(p));
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
         l[0] = __uint_as_float(x << 16), l[1] = __uint_as_float(x & 0xFFFF0000u);
       }
     } else {
@@ -89,11 +89,11 @@ __device__ __forceinline__ void load_row(const Args& a, long long row, int first
       if constexpr (V >= 4) {
 #pragma unroll
         for (int q = 0; q < V / 4; ++q) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(p) + q);
+          const float4 x = reinterpret_cast<const float4*>(p)[q];
           l[4 * q] = x.x, l[4 * q + 1] = x.y, l[4 * q + 2] = x.z, l[4 * q + 3] = x.w;
         }
       } else if constexpr (V == 2) {
-        const float2 x = __ldg(reinterpret_cast<const float2*>(p));
+        const float2 x = *reinterpret_cast<const float2*>(p);
         l[0] = x.x, l[1] = x.y;
       }
     }
@@ -418,7 +418,7 @@ struct Chooser {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (first + v >= a.experts) continue;
-      b[v] = __ldg(a.bias + first + v);
+      b[v] = a.bias[first + v];
       lo = fminf(lo, b[v]), hi = fmaxf(hi, b[v]);
     }
     lo = -warp_max(-lo), hi = warp_max(hi);
