@@ -534,6 +534,18 @@ def test_rows_past_two_to_the_31(zopt):
         assert float((got.double() - want).norm()) <= 3.2e-3 * float(want.norm())
 
 
+@pytest.mark.parametrize("tokens", [1, 3, 17])
+@pytest.mark.parametrize("extra", [0, 8, 5])
+def test_wide_gradients_of_experts_without_rows(zopt, tokens, extra):
+    """Parts of a gradient that are whole, end inside the matrix's rows or columns, or start anywhere."""
+    b = Block(tokens, 300, 200, 12, 2, "silu", "bf16", 0, extra=extra, seed=19)
+    b.index[:, 1] = b.index[:, 0]  # (half the experts or more have no rows)
+    b.forward(zopt)
+    b.backward(zopt)
+    b.check(zopt)
+    assert len(set(b.index.flatten().tolist())) < 12
+
+
 @pytest.mark.parametrize("case", [(60, 40, 24, 4, 2, "silu", "bf16", 3), (4, 40, 24, 4, 2, "gelu", "e4m3", 0)])
 @pytest.mark.parametrize("gap", [8, 3])
 def test_matrices_any_distance_apart(zopt, case, gap):
