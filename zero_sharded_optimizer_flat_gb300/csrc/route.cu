@@ -552,7 +552,8 @@ struct Chooser {
       // (a number that is none has other leading bits than 2^23's)
       r.all = __any_sync(kAll, (seen >> 23) != (__float_as_uint(kMagic) >> 23)) || !(range < INFINITY);
       const float off = kUnit * (2.0f * (a.softmax ? (V + 15) * rz : 5.0f) + 4.0f * (fabsf(lo) + fabsf(hi) + range));
-      r.near = static_cast<int>(off * scale) + 4;  // (and two units of each of the two)
+      // (and two units of each of the two; biases may be so much larger than the range that every rank is this near)
+      r.near = static_cast<int>(fminf(off * scale, static_cast<float>(kTopRank))) + 4;
       r.scale = scale;
       if (a.groups > 1) {
         choose_groups(w, at, range * (1.0f / (kTopRank - 3)), r.near, r);
