@@ -45,3 +45,14 @@ def test_biases_far_larger_than_scores(zopt, e, score, low):
     l = logits_of(12, e, e)
     same(zopt, l, 6, score, masks(e, low))
     same(zopt, l, 6, score, masks(e, low), 4, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e", [8, 24, 32, 60, 256])
+@pytest.mark.parametrize("low", [-1e38, torch.finfo(torch.float32).min])
+def test_biases_of_the_lowest_value(zopt, e, score, low):
+    """The range's reciprocal is no normal number: no fixed point holds such ranks."""
+    l = logits_of(12, e, e)
+    same(zopt, l, 3, score, masks(e, low))
+    if e >= 24:
+        same(zopt, l, 3, score, masks(e, low), 4, 2)

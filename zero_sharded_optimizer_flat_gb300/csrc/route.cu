@@ -549,8 +549,9 @@ struct Chooser {
         seen |= u;
         w[v] = l[v] == -INFINITY ? 0u : (u << kIndexBits) | name(v);
       }
-      // (a number that is none has other leading bits than 2^23's)
-      r.all = __any_sync(kAll, (seen >> 23) != (__float_as_uint(kMagic) >> 23)) || !(range < INFINITY);
+      // (a number that is none has other leading bits than 2^23's; a range from 2^104 on leaves no word a meaning:
+      // its reciprocal flushes to 0 from 2^126 on)
+      r.all = __any_sync(kAll, (seen >> 23) != (__float_as_uint(kMagic) >> 23)) || !(range < 0x1p104f);
       const float off = kUnit * (2.0f * (a.softmax ? (V + 15) * rz : 5.0f) + 4.0f * (fabsf(lo) + fabsf(hi) + range));
       // (and two units of each of the two; biases may be so much larger than the range that every rank is this near)
       r.near = static_cast<int>(fminf(off * scale, static_cast<float>(kTopRank))) + 4;
