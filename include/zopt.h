@@ -645,8 +645,10 @@ ZOPT_API zopt_status zopt_linear_ce_backward(const zopt_linear_ce_job* job, void
  *   two largest c (of the one, where there is one), and only the top_groups best runs take part;
  *   index = the top_k experts with the largest c, best first;
  *   weight = s of those (without the bias), over their sum where renormalise, times scale.
- * The order is that of the exact numbers (without a bias: of the logits), the lowest index (of
- * experts, of runs) first among equal ones. An expert with a logit of -inf is never chosen; a slot
+ * The order is that of the exact numbers (without a bias, or where two biases are equal: of the logits), the
+ * lowest index (of experts, of runs) first among equal ones. Its limits: a score (of a logistic one above 1/2
+ * what it lacks of 1) is known to 2^-50 of itself, a sum to 106 bits, and in a run's score nothing is below
+ * e^-700 of the row's largest. An expert with a logit of -inf is never chosen; a slot
  * that no expert is left for has index -1 and weight 0, and so has every slot of a row whose live
  * byte is 0, whatever its logits hold. A NaN ranks above every number and makes its weight NaN (its
  * row's, for softmax or where renormalised), and so does +inf for softmax, so that found_inf sees it.

@@ -1,5 +1,5 @@
 """The experts that a row of logits chooses, in exact order: sums of scores and biases as decimal numbers of
-400 digits, in which neither a score of e^-700 beside a bias of 3e38 nor the distance of two logistic scores
+140 digits, in which neither a score of e^-200 beside a bias of 3e38 nor the distance of two logistic scores
 from 1 is lost."""
 from __future__ import annotations
 
@@ -7,12 +7,12 @@ import decimal
 
 import numpy as np
 
-_DIGITS = decimal.Context(prec=400, Emin=-10 ** 6, Emax=10 ** 6)
+_DIGITS = decimal.Context(prec=140, Emin=-10 ** 6, Emax=10 ** 6)
 
 
 def choose(logits, top_k, kind="softmax", bias=None, groups=1, top_groups=1):
     """index [rows, top_k], the best first, the lowest index (of experts, of runs) first among equal ones; logits
-    finite, at most 800 in size."""
+    finite, at most 100 in size where there are biases."""
     with decimal.localcontext(_DIGITS):
         return np.array([_row([float(x) for x in row], top_k, kind, bias, groups, top_groups) for row in logits], np.int32)
 

@@ -218,15 +218,64 @@ __device__ __forceinline__ double exp64(double x) {
   return p * __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(1023 + static_cast<int>(k)) << 52));
 }
 
-// The best `most` of the candidates, one a lane (key 0: none), the lowest index first among equal ones.
-__device__ __forceinline__ int best64(uint64_t key, int i, int most, int lane) {
+// A number in two parts, the second what the first's rounding left out (Knuth's two-sum): neither a score
+// beside a bias of 1e10 nor the 1e-18 that a logistic score lacks of 1 is lost.
+struct Sum {
+  double hi, lo;
+};
+__device__ __forceinline__ Sum sum_of(double a, double b) {
+  const double s = a + b, v = s - a;
+  return Sum{s, (a - (s - v)) + (b - v)};
+}
+__device__ __forceinline__ Sum operator+(const Sum& a, const Sum& b) {
+  const Sum s = sum_of(a.hi, b.hi);
+  if (!(fabs(s.hi) < static_cast<double>(INFINITY))) return Sum{s.hi, 0.0};  // (inf, NaN)
+  return sum_of(s.hi, s.lo + (a.lo + b.lo));
+}
+
+// What an expert (or a group) is ranked by: the parts of s + bias in turn, then the logit, in which s grows: what 53
+// bits a part and exp64's range do not tell apart, it does where the biases are equal. hi 0: none.
+struct Rank {
+  uint64_t hi = 0, lo = 0;
+  uint32_t l = 0;
+};
+__device__ __forceinline__ Rank rank_of(const Sum& c, float l) {
+  Rank r;
+  r.hi = key_of(c.hi);
+  if (c.hi == c.hi) r.lo = key_of(c.lo), r.l = key_of(l);  // (NaN: equal to any other)
+  return r;
+}
+__device__ __forceinline__ Sum of_rank(const Rank& r, int lane) {  // lane's, in every lane
+  return Sum{of_key(__shfl_sync(kAll, r.hi, lane)), of_key(__shfl_sync(kAll, r.lo, lane))};
+}
+__device__ __forceinline__ bool above(const Rank& x, const Rank& y) {
+  return x.hi != y.hi ? x.hi > y.hi : x.lo != y.lo ? x.lo > y.lo : x.l > y.l;
+}
+// The lanes that hold the warp's largest; 0: there is none.
+__device__ __forceinline__ unsigned best_lanes(const Rank& r) {
+  const uint64_t top = warp_max(r.hi);
+  bool on = top != 0 && r.hi == top;
+  unsigned who = __ballot_sync(kAll, on);
+  if (__popc(who) > 1) {  // (the whole warp's)
+    const uint64_t lo = warp_max(on ? r.lo : uint64_t{0});
+    on = on && r.lo == lo;
+    const uint32_t l = __reduce_max_sync(kAll, on ? r.l : 0u);
+    on = on && r.l == l;
+    who = __ballot_sync(kAll, on);
+  }
+  return who;
+}
+
+// The best `most` of the candidates, one a lane, the lowest index first among equal ones.
+__device__ __forceinline__ int best64(Rank r, int i, int most, int lane) {
   int mine = -1;
   for (int j = 0; j < most; ++j) {
-    const uint64_t top = warp_max(key);
-    if (top == 0) break;
-    const int at = static_cast<int>(__reduce_min_sync(kAll, key == top ? static_cast<uint32_t>(i) : kAll));
+    const unsigned who = best_lanes(r);
+    if (who == 0) break;
+    const bool on = ((who >> lane) & 1u) != 0;
+    const int at = static_cast<int>(__reduce_min_sync(kAll, on ? static_cast<uint32_t>(i) : kAll));
     if (lane == j) mine = at;
-    if (key == top && i == at) key = 0;
+    if (on && i == at) r = Rank{};
   }
   return mine;
 }
@@ -234,13 +283,13 @@ __device__ __forceinline__ int best64(uint64_t key, int i, int most, int lane) {
 // An expert's rank: its score and the bias, without a bias (but for groups' sums) its logit.
 struct Rank64 {
   double m = 0.0, z = 1.0;
-  __device__ __forceinline__ double score(const Args& a, float l, int i) const {
-    const double x = static_cast<double>(l), e = exp64(a.softmax ? x - m : -x);
-    const double s = a.softmax ? e / z : l == INFINITY ? 1.0 : 1.0 / (1.0 + e);
-    return a.bias != nullptr ? s + static_cast<double>(a.bias[i]) : s;
+  __device__ __forceinline__ Sum score(const Args& a, float l, int i) const {
+    const double x = static_cast<double>(l), b = a.bias != nullptr ? static_cast<double>(a.bias[i]) : 0.0;
+    if (!a.softmax && l > 0.0f) return sum_of(1.0, b) + Sum{-1.0 / (1.0 + exp64(x)), 0.0};  // 1 - s is the one with all its bits
+    return Sum{a.softmax ? exp64(x - m) / z : 1.0 / (1.0 + exp64(-x)), 0.0} + Sum{b, 0.0};
   }
-  __device__ __forceinline__ uint64_t key(const Args& a, float l, int i) const {
-    return key_of(a.bias == nullptr ? static_cast<double>(l) : score(a, l, i));
+  __device__ __forceinline__ Rank rank(const Args& a, float l, int i) const {
+    return a.bias == nullptr ? rank_of(Sum{static_cast<double>(l), 0.0}, 0.0f) : rank_of(score(a, l, i), l);
   }
 };
 
@@ -286,7 +335,7 @@ __device__ __noinline__ int choose_near(const Args& a, long long row, float lo, 
   if (n > 32) return -2;
   const int i = lane < n ? list[lane] : -1;
   __syncwarp();
-  return best64(i >= 0 ? r.key(a, load(a, row, i), i) : 0ull, i, a.top_k, lane);
+  return best64(i >= 0 ? r.rank(a, load(a, row, i), i) : Rank{}, i, a.top_k, lane);
 }
 
 // A row's choice once more, from all its experts, the groups ranked again as well. Lane l looks at experts l,
@@ -305,41 +354,49 @@ __device__ __noinline__ int choose_all(const Args& a, long long row) {
   }
   uint32_t groups = kAll, gone = 0;
   if (a.groups > 1) {
-    uint64_t mine = 0;
+    Rank mine;
     const int per = static_cast<int>(a.per_group.d);
     for (int g = 0; g < a.groups; ++g) {
-      uint64_t first = 0, second = 0;
+      Rank first, second;
       for (int i = g * per + lane; i < (g + 1) * per; i += 32) {
         const float l = load(a, row, i);
         if (l == -INFINITY) continue;
-        const uint64_t k = key_of(r.score(a, l, i));
-        second = k > first ? first : k > second ? k : second;
-        first = k > first ? k : first;
+        const Rank k = rank_of(r.score(a, l, i), l);
+        if (above(k, first)) {
+          second = first, first = k;
+        } else if (above(k, second)) {
+          second = k;
+        }
       }
-      const uint64_t one = warp_max(first);
-      const int owner = __ffs(__ballot_sync(kAll, first == one)) - 1;
-      const uint64_t two = warp_max(lane == owner ? second : first);
-      if (lane == g) mine = one == 0 ? 0 : two == 0 ? one : key_of(of_key(one) + of_key(two));
+      const unsigned one = best_lanes(first);
+      if (one == 0) continue;  // (the whole warp's)
+      const int owner = __ffs(one) - 1;
+      Sum sum = of_rank(first, owner);
+      if (lane == owner) first = second;
+      const unsigned two = best_lanes(first);
+      if (two != 0) sum = sum + of_rank(first, __ffs(two) - 1);
+      if (lane == g) mine = rank_of(sum, 0.0f);
     }
     const int g = best64(mine, lane, a.top_groups, lane);
     groups = __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
   }
   int mine = -1;
   for (int j = 0; j < a.top_k; ++j) {
-    uint64_t best = 0;
+    Rank best;
     int at = -1;
     for (int i = lane, v = 0; i < a.experts; i += 32, ++v) {
       const float l = load(a, row, i);
       if (((gone >> v) & 1u) != 0 || l == -INFINITY) continue;
       if (a.groups > 1 && ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) == 0) continue;
-      const uint64_t k = r.key(a, l, i);
-      if (k > best) best = k, at = i;
+      const Rank k = r.rank(a, l, i);
+      if (above(k, best)) best = k, at = i;
     }
-    const uint64_t win = warp_max(best);
-    if (win == 0) break;
-    const int i = static_cast<int>(__reduce_min_sync(kAll, best == win ? static_cast<uint32_t>(at) : kAll));
+    const unsigned who = best_lanes(best);
+    if (who == 0) break;
+    const bool on = ((who >> lane) & 1u) != 0;
+    const int i = static_cast<int>(__reduce_min_sync(kAll, on ? static_cast<uint32_t>(at) : kAll));
     if (lane == j) mine = i;
-    if (best == win && at == i) gone |= 1u << (i >> 5);
+    if (on && at == i) gone |= 1u << (i >> 5);
   }
   return mine;
 }
@@ -348,10 +405,10 @@ __device__ __noinline__ int choose_all(const Args& a, long long row) {
 __device__ __noinline__ uint32_t groups64(const Args& a, long long row, int one, int two) {
   const Rank64 r;
   const int lane = threadIdx.x & 31;
-  double sum = 0.0;
+  Sum sum{0.0, 0.0};
   if (one >= 0) sum = r.score(a, load(a, row, one), one);
-  if (two >= 0) sum += r.score(a, load(a, row, two), two);
-  const int g = best64(one >= 0 ? key_of(sum) : 0ull, lane, a.top_groups, lane);
+  if (two >= 0) sum = sum + r.score(a, load(a, row, two), two);
+  const int g = best64(one >= 0 ? rank_of(sum, 0.0f) : Rank{}, lane, a.top_groups, lane);
   return __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
 }
 
