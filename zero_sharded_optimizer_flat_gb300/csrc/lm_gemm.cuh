@@ -16,6 +16,7 @@
 
 #include "divisor.cuh"
 #include "internal.h"
+#include "row_piece.h"
 
 namespace zopt {
 namespace lm {
@@ -184,31 +185,6 @@ zopt_status launch_stage(const char* fn, uint16_t* dst, long long dst_pitch, lon
 
 // Blocks of 256 threads for `items` threads' work, at most eight per SM.
 unsigned blocks_for(long long items, int sms);
-
-// Eight bf16 elements from s, those from n on zero.
-__device__ __forceinline__ uint4 row_piece8(const uint16_t* s, long long n) {
-  const unsigned mis = static_cast<unsigned>(reinterpret_cast<uintptr_t>(s)) & 15u;
-  if (n >= 8 && mis == 0) return *reinterpret_cast<const uint4*>(s);
-  if (n >= 8 && (mis & 7u) == 0) {
-    const uint2 a = reinterpret_cast<const uint2*>(s)[0], b = reinterpret_cast<const uint2*>(s)[1];
-    return make_uint4(a.x, a.y, b.x, b.y);
-  }
-  if (n >= 8) {
-    // words, each a whole one of memory: of a row that starts in the middle of one, five, shifted together
-    const uint32_t* const w = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(s) & ~uintptr_t{3});
-    uint32_t x[5];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = w[k];
-    x[4] = (mis & 2u) != 0 ? w[4] : 0u;
-    if ((mis & 2u) == 0) return make_uint4(x[0], x[1], x[2], x[3]);
-    return make_uint4(__funnelshift_r(x[0], x[1], 16), __funnelshift_r(x[1], x[2], 16), __funnelshift_r(x[2], x[3], 16),
-                      __funnelshift_r(x[3], x[4], 16));
-  }
-  uint32_t x[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = k < n ? s[k] : 0u;
-  return make_uint4(x[0] | (x[1] << 16), x[2] | (x[3] << 16), x[4] | (x[5] << 16), x[6] | (x[7] << 16));
-}
 
 inline long long round_up(long long x, long long a) { return (x + a - 1) / a * a; }
 
