@@ -479,6 +479,9 @@ struct Chooser {
       lo = fminf(lo, b[v]), hi = fmaxf(hi, b[v]);
     }
     lo = -warp_max(-lo), hi = warp_max(hi);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (first + v >= a.experts) b[v] = lo;  // (behind the last one: within the range, as the check in words() wants it)
   }
   __device__ __forceinline__ uint32_t name(int v) const { return kIndexMask - static_cast<uint32_t>(first + v); }
 
