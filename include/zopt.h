@@ -716,7 +716,7 @@ ZOPT_API zopt_status zopt_route_backward(const zopt_route_job* job, zopt_stream 
  * every slot, row t top_k + j. Experts' matrices lie stride_* elements apart (any distance that keeps
  * them apart). What the TMA cannot read in place (weights whose ld is not a multiple of 8 elements or
  * whose stride is none of ld, the forward's up columns where F is not a multiple of 8, kept rows or ups
- * that do not start on 16 bytes) is copied into the workspace first. A forward of a few slots (at most
+ * that do not start on 16 bytes) is copied into the workspace first, of weights those of experts with a slot. A forward of a few slots (at most
  * 64, fewer where the weights are large) runs on the CUDA cores instead, which read the weights in place
  * and keep h and the parts in fp32: a token's y may differ there from its y in a larger batch by their
  * roundings. Outputs must not overlap inputs or each other. Repeated on the same inputs a call gives the

@@ -23,6 +23,7 @@
 
 #include "act8.cuh"
 #include "act8_host.h"
+#include "divisor.cuh"
 #include "experts_few.h"
 #include "experts_gemm.h"
 #include "guarded.h"
@@ -53,6 +54,7 @@ struct PlanArgs {
   int* head;
   int4* tiles;
   int2* info;
+  int* used;     // the experts that have a slot
   int2* row;     // [rows] slot and weight
   int* row_of;   // [slots] its row; -1: none; -2: an index that is none
 };
@@ -70,7 +72,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
   extern __shared__ int smem[];
   int* count = smem;                               // [warps][experts]
   int* mine = count + kPlanWarps * a.experts;      // [experts] this block's
-  __shared__ int sums[2][kPlanWarps];
+  __shared__ uint32_t sums[2][kPlanWarps];
   tc::pdl_launch_dependents();
   tc::pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
@@ -121,32 +123,41 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(32 * kPlanWa
       all += c;
     }
   }
-  // the experts before: their rows, and their row tiles
+  // the experts before: their rows, and in one word their row tiles (fewer than 2^20) and how many have a slot
+  constexpr int kTileBits = 21;
+  static_assert(kMaxSlots / 128 + kMaxExperts < 1LL << kTileBits && static_cast<long long>(kMaxExperts) << kTileBits < 1LL << 32, "the word");
   const int rows = (all + kGroupRows - 1) / kGroupRows * kGroupRows, tiles = (all + a.tile_rows - 1) / a.tile_rows;
-  int r = rows, t = tiles;
+  const uint32_t word = static_cast<uint32_t>(tiles) | (all > 0 ? 1u << kTileBits : 0u);
+  int r = rows;
+  uint32_t t = word;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int x = __shfl_up_sync(0xFFFFFFFFu, r, d), y = __shfl_up_sync(0xFFFFFFFFu, t, d);
+    const int x = __shfl_up_sync(0xFFFFFFFFu, r, d);
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, t, d);
     if (lane >= d) r += x, t += y;
   }
-  if (lane == 31) sums[0][warp] = r, sums[1][warp] = t;
+  if (lane == 31) sums[0][warp] = static_cast<uint32_t>(r), sums[1][warp] = t;
   __syncthreads();
   if (warp == 0) {
-    int x = sums[0][lane], y = sums[1][lane];
+    uint32_t x = sums[0][lane], y = sums[1][lane];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, x, d), v = __shfl_up_sync(0xFFFFFFFFu, y, d);
+      const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, x, d), v = __shfl_up_sync(0xFFFFFFFFu, y, d);
       if (lane >= d) x += u, y += v;
     }
     sums[0][lane] = x, sums[1][lane] = y;
   }
   __syncthreads();
-  const int first = r - rows + (warp > 0 ? sums[0][warp - 1] : 0), first_tile = t - tiles + (warp > 0 ? sums[1][warp - 1] : 0);
-  if (rank == 0 && threadIdx.x == 0) a.head[0] = sums[1][kPlanWarps - 1], a.head[1] = sums[0][kPlanWarps - 1];
+  const int first = r - rows + (warp > 0 ? static_cast<int>(sums[0][warp - 1]) : 0);
+  const uint32_t before_it = t - word + (warp > 0 ? sums[1][warp - 1] : 0u), sum = sums[1][kPlanWarps - 1];
+  const int first_tile = static_cast<int>(before_it & ((1u << kTileBits) - 1u));
+  if (rank == 0 && threadIdx.x == 0)
+    a.head[0] = static_cast<int>(sum & ((1u << kTileBits) - 1u)), a.head[1] = static_cast<int>(sum >> kTileBits);
   tc::cluster_sync();  // every block has read `mine`
   if (e < E) {
     mine[e] = first + before;
     if (rank == 0) a.info[e] = make_int2(first, all);
+    if (rank == 0 && all > 0) a.used[before_it >> kTileBits] = e;
     for (int i = static_cast<int>(rank); i < tiles; i += kPlanCtas)
       a.tiles[first_tile + i] = make_int4(e, first + i * a.tile_rows, min(first + rows, first + (i + 1) * a.tile_rows),
                                           min(all - i * a.tile_rows, a.tile_rows) <= kTileM / 2 ? 1 : 0);
@@ -187,11 +198,14 @@ struct Source {
   const uint8_t *q, *scale;  // or a checkpoint (x null)
   uint16_t* to;              // rows of `pitch` elements
 };
-// An operand that the TMA cannot read where it is: dst[e][r][c] = src[e][r][c] for c < cols, 0 up to dst_cols.
+// An operand that the TMA cannot read where it is: dst[e][r][c] = src[e][r][c] for c < cols, 0 up to dst_cols. Of
+// experts that have a slot alone: no unit reads another's.
 struct Copy {
   uint16_t* dst;
   const uint16_t* src;
   long long dst_cols, ld, stride, rows, cols;
+  long long chunk;  // at most 2^30 rows, of fewer than 2^31 pieces less a grid's threads
+  Divisor per_row, per_expert;
 };
 // The kept rows of the slots that have an expert, gate and up each from a 16-byte boundary on, zeros behind them
 // (the epilogue that reads them takes 16 bytes of a row at a time; rows that start anywhere, a lane each, would
@@ -208,6 +222,7 @@ struct GatherArgs {
   long long tokens, cols, pitch;
   const int* row_of;
   const int2* info;
+  const int *head, *used;
   int top_k, experts;
   int fill;  // the backward multiplies by the rows that only fill up
   Copy copy[3];
@@ -232,12 +247,20 @@ __device__ __forceinline__ uint4 piece_of(const Source& f, long long cols, long 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void copy_rows(const Copy& c, int experts, long long thread, long long threads) {
-  const long long per_row = c.dst_cols / 8, n = experts * c.rows * per_row;
+// (Where a piece lies is found without divisions: with 64-bit ones a forward of 64 x 6 slots of 64 experts, 2047 x 1407,
+// takes 850 us for 806. `chunk` rows at a time, their pieces' numbers below 2^31.)
+__device__ __forceinline__ void copy_rows(const Copy& c, const int* used, int n, uint32_t thread, uint32_t threads) {
+  const long long rows = n * c.rows;
+  for (long long row0 = 0; row0 < rows; row0 += c.chunk) {
+    const long long k0 = row0 / c.rows;
+    const uint32_t r0 = static_cast<uint32_t>(row0 - k0 * c.rows);
+    const uint32_t all = static_cast<uint32_t>(min(c.chunk, rows - row0)) * c.per_row.d;
 #pragma unroll 2
-  for (long long g = thread; g < n; g += threads) {
-    const long long row = g / per_row, col = (g - row * per_row) * 8, e = row / c.rows;
-    *reinterpret_cast<uint4*>(c.dst + row * c.dst_cols + col) = row_piece8(c.src + e * c.stride + (row - e * c.rows) * c.ld + col, c.cols - col);
+    for (uint32_t g = thread; g < all; g += threads) {
+      const uint32_t row = c.per_row(g), k = c.per_expert(r0 + row);
+      const long long col = (g - row * c.per_row.d) * 8, r = r0 + row - k * c.per_expert.d, e = used[k0 + k];
+      *reinterpret_cast<uint4*>(c.dst + (e * c.rows + r) * c.dst_cols + col) = row_piece8(c.src + e * c.stride + r * c.ld + col, c.cols - col);
+    }
   }
 }
 __device__ __forceinline__ void copy_kept(const KeptCopy& c, const int* row_of, long long slots, int lane, int warp, int warps) {
@@ -292,8 +315,10 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
         if (p0 + 32 * q < pieces) *reinterpret_cast<uint4*>(to + 8 * (p0 + 32 * q)) = v[q];
     }
   }
-  for (int k = 0; k < a.copies; ++k)
-    copy_rows(a.copy[k], a.experts, blockIdx.x * 256LL + threadIdx.x, gridDim.x * 256LL);
+  if (a.copies > 0) {
+    const int n = a.head[1];
+    for (int k = 0; k < a.copies; ++k) copy_rows(a.copy[k], a.used, n, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+  }
   if (a.kept.dst != nullptr) copy_kept(a.kept, a.row_of, a.tokens * a.top_k, lane, me, warps);
   if (!a.fill) return;
   for (int i = me; i < a.experts * (kGroupRows - 1); i += warps) {  // the rows that only fill up
@@ -408,7 +433,7 @@ struct Layout {
   int tile_rows;
   bool stage_gate, stage_up, stage_down, stage_kept;
   long long kept_row;  // bytes of a part of a staged row
-  size_t head, tile, info, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, kept, few_gate_up, few_y, total;
+  size_t head, tile, info, used, row, row_of, gate, up, down, xs, dys, h, dgu, parts, scales, dots, kept, few_gate_up, few_y, total;
   int dot_parts;
   bool few;
 };
@@ -466,6 +491,7 @@ Layout layout(const zopt_experts_job& c, bool backward) {
   p.head = take(at, 8);
   p.tile = take(at, 16 * p.tiles);
   p.info = take(at, 8 * E);
+  p.used = take(at, 4 * E);
   p.row = take(at, 8 * p.rows);
   p.row_of = take(at, 4 * p.slots);
   if (p.stage_gate) p.gate = take(at, E * D * p.gp * 2);
@@ -587,7 +613,8 @@ struct Call {
             long long cols, const uint16_t** to, long long* pitch_to, long long* stride_to) const {
     uint16_t* d = at<uint16_t>(off);
     *to = d, *pitch_to = pitch, *stride_to = rows * pitch;
-    a.copy[a.copies++] = Copy{d, src, pitch, ld, stride, rows, cols};
+    const long long per_row = pitch / 8, chunk = std::max<long long>(1, std::min<long long>(1LL << 30, ((1LL << 31) - (1LL << 22)) / per_row));
+    a.copy[a.copies++] = Copy{d, src, pitch, ld, stride, rows, cols, chunk, Divisor(static_cast<uint32_t>(per_row)), Divisor(static_cast<uint32_t>(rows))};
   }
   // The forward reads gate's and up's columns, the backward gate_up's rows whole.
   Weights weights(bool backward, GatherArgs& a) const {
@@ -605,7 +632,8 @@ struct Call {
     ZOPT_CUDA_TRY(once_per_device([] {
       return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kPlanWarps + 1) * kMaxExperts * 4);
     }));
-    const PlanArgs a{c.index, c.weight, p.slots, c.experts, p.tile_rows, at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int2>(p.row), at<int>(p.row_of)};
+    const PlanArgs a{c.index, c.weight, p.slots, c.experts, p.tile_rows, at<int>(p.head), at<int4>(p.tile), at<int2>(p.info), at<int>(p.used), at<int2>(p.row),
+                     at<int>(p.row_of)};
     return launch_pdl(plan_kernel, dim3(kPlanCtas), dim3(32 * kPlanWarps), smem, s, a);
   }
   zopt_status gather(bool backward, GatherArgs& a) const {
@@ -615,11 +643,13 @@ struct Call {
     if (backward) a.from[1] = Source{c.dy, c.ld_dy, nullptr, nullptr, at<uint16_t>(p.dys)};
     a.tokens = c.tokens, a.cols = c.dim, a.pitch = p.dp;
     a.row_of = at<int>(p.row_of), a.info = at<int2>(p.info);
+    a.head = at<int>(p.head), a.used = at<int>(p.used);
     a.top_k = c.top_k, a.experts = c.experts, a.fill = backward;
     long long threads = 32 * a.n * c.tokens * ((p.dp + 1023) / 1024);
-    for (int k = 0; k < a.copies; ++k) threads = std::max(threads, c.experts * a.copy[k].rows * (a.copy[k].dst_cols / 8));
+    const long long used = std::min<long long>(c.experts, p.slots);
+    for (int k = 0; k < a.copies; ++k) threads = std::max(threads, used * a.copy[k].rows * (a.copy[k].dst_cols / 8));
     if (a.kept.dst != nullptr) threads = std::max(threads, 32 * p.slots);
-    if (backward) threads = std::max(threads, 32 * (kGroupRows - 1) * std::min<long long>(c.experts, p.slots));  // a warp a row to fill up
+    if (backward) threads = std::max(threads, 32 * (kGroupRows - 1) * used);  // a warp a row to fill up
     return launch_pdl(gather_kernel, dim3(blocks_for(threads, sms)), dim3(256), 0, s, a);
   }
   zopt_status combine(bool backward) const {

@@ -112,7 +112,7 @@ struct Job {
 // a multiple of 64 (a k-block, and the 32 rows of an epilogue's warp, are then one expert's). What is
 // not known before the tokens have chosen is read from device memory.
 struct Groups {
-  const int* head;    // [0] row tiles, [1] rows
+  const int* head;    // [0] row tiles, [1] experts that have a slot
   const int4* tiles;  // a row tile's expert, first row, where its expert's rows (with the zeros) end, and 1 for at most 128 rows
   const int2* info;   // an expert's first row and its number of rows (without the zeros)
   const int2* row;    // a row's slot (-1: zeros) and its weight's bits
