@@ -38,3 +38,14 @@ def test_a_common_shift_of_the_bias_costs_nothing(zopt, e, score):
     for shift in (0.01, -0.05):
         shifted = microseconds(forward(zopt, logits, spread + shift, 4, score=score))
         assert shifted <= 1.5 * centred + 2.0, (shifted, centred)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_rows_ranked_from_all_experts(zopt, score):
+    """Biases whose spread leaves no fixed point send every row to the ranking of all its experts, which a lane goes
+    through once or twice, not for every choice: in the time of a few choices, not of all eight."""
+    logits = torch.randn(8192, 256, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    bias = torch.zeros(256, device="cuda")
+    bias[::8] = torch.finfo(torch.float32).min
+    one, eight = (microseconds(forward(zopt, logits, bias, k, score=score)) for k in (1, 8))
+    assert eight <= 4.0 * one, (one, eight)

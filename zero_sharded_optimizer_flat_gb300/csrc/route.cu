@@ -218,20 +218,23 @@ __device__ __forceinline__ double exp64(double x) {
   return p * __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(1023 + static_cast<int>(k)) << 52));
 }
 
-// A number in two parts, the second what the first's rounding left out (Knuth's two-sum): neither a score
-// beside a bias of 1e10 nor the 1e-18 that a logistic score lacks of 1 is lost.
+// A number in two parts, the second what the first's rounding left out: neither a score beside a bias of 1e10 nor
+// the 1e-18 that a logistic score lacks of 1 is lost.
 struct Sum {
   double hi, lo;
 };
-__device__ __forceinline__ Sum sum_of(double a, double b) {
+__device__ __forceinline__ Sum sum_of(double a, double b) {  // (Knuth's two-sum)
   const double s = a + b, v = s - a;
   return Sum{s, (a - (s - v)) + (b - v)};
 }
-__device__ __forceinline__ Sum operator+(const Sum& a, const Sum& b) {
-  const Sum s = sum_of(a.hi, b.hi);
-  if (!(fabs(s.hi) < static_cast<double>(INFINITY))) return Sum{s.hi, 0.0};  // (inf, NaN)
-  return sum_of(s.hi, s.lo + (a.lo + b.lo));
+__device__ __forceinline__ bool finite(double x) { return x - x == 0.0; }
+// a and a small part more (Dekker's: the first is the larger one).
+__device__ __forceinline__ Sum with(const Sum& a, double lo) {
+  if (!finite(a.hi)) return Sum{a.hi, 0.0};
+  const double l = a.lo + lo, s = a.hi + l;
+  return Sum{s, l - (s - a.hi)};
 }
+__device__ __forceinline__ Sum operator+(const Sum& a, const Sum& b) { return with(sum_of(a.hi, b.hi), a.lo + b.lo); }
 
 // What an expert (or a group) is ranked by: the parts of s + bias in turn, then the logit, in which s grows: what 53
 // bits a part and exp64's range do not tell apart, it does where the biases are equal. hi 0: none.
@@ -242,7 +245,7 @@ struct Rank {
 __device__ __forceinline__ Rank rank_of(const Sum& c, float l) {
   Rank r;
   r.hi = key_of(c.hi);
-  if (c.hi == c.hi) r.lo = key_of(c.lo), r.l = key_of(l);  // (NaN: equal to any other)
+  if (c.hi == c.hi) r.lo = finite(c.hi) ? key_of(c.lo) : 0, r.l = key_of(l);  // (NaN: equal to any other)
   return r;
 }
 __device__ __forceinline__ Sum of_rank(const Rank& r, int lane) {  // lane's, in every lane
@@ -267,7 +270,7 @@ __device__ __forceinline__ unsigned best_lanes(const Rank& r) {
 }
 
 // The best `most` of the candidates, one a lane, the lowest index first among equal ones.
-__device__ __forceinline__ int best64(Rank r, int i, int most, int lane) {
+__device__ __forceinline__ int best_ranks(Rank r, int i, int most, int lane) {
   int mine = -1;
   for (int j = 0; j < most; ++j) {
     const unsigned who = best_lanes(r);
@@ -279,14 +282,42 @@ __device__ __forceinline__ int best64(Rank r, int i, int most, int lane) {
   }
   return mine;
 }
+// The same by single fp64 numbers, which is quicker; -2 in every lane where two neighbours in the order, from place
+// `from` on and as far as the best one left out, are no further apart than such a number may be off (`off` of 1 and
+// of the number itself; negative: they are exact).
+__device__ __forceinline__ int best_keys(uint64_t key, int i, int most, int lane, int from, double off) {
+  int mine = -1;
+  uint64_t mine_key = 0;
+  for (int j = 0; j < most; ++j) {
+    const uint64_t top = warp_max(key);
+    if (top == 0) break;
+    const int at = static_cast<int>(__reduce_min_sync(kAll, key == top ? static_cast<uint32_t>(i) : kAll));
+    if (lane == j) mine = at, mine_key = top;
+    if (key == top && i == at) key = 0;
+  }
+  if (off < 0.0) return mine;
+  const uint64_t left = warp_max(key), below = __shfl_down_sync(kAll, mine_key, 1), next = lane + 1 == most ? left : below;
+  const double v = of_key(mine_key);
+  const bool close = lane + 1 >= from && mine >= 0 && next != 0 && !(v - of_key(next) > off * (1.0 + fabs(v)));
+  return __any_sync(kAll, close) ? -2 : mine;
+}
 
 // An expert's rank: its score and the bias, without a bias (but for groups' sums) its logit.
 struct Rank64 {
   double m = 0.0, z = 1.0;
   __device__ __forceinline__ Sum score(const Args& a, float l, int i) const {
     const double x = static_cast<double>(l), b = a.bias != nullptr ? static_cast<double>(a.bias[i]) : 0.0;
-    if (!a.softmax && l > 0.0f) return sum_of(1.0, b) + Sum{-1.0 / (1.0 + exp64(x)), 0.0};  // 1 - s is the one with all its bits
-    return Sum{a.softmax ? exp64(x - m) / z : 1.0 / (1.0 + exp64(-x)), 0.0} + Sum{b, 0.0};
+    const double e = exp64(a.softmax ? x - m : -fabs(x));
+    if (a.softmax) return sum_of(b, e / z);
+    const double t = e / (1.0 + e);  // s, or where that is above 1/2 what it lacks of 1
+    const Sum one = sum_of(l > 0.0f ? 1.0 : 0.0, b);
+    return with(sum_of(one.hi, l > 0.0f ? -t : t), one.lo);
+  }
+  // The first part, to 2^-50 of 1 and 2^-52 of itself.
+  __device__ __forceinline__ double about(const Args& a, float l, int i) const {
+    const double x = static_cast<double>(l), e = exp64(a.softmax ? x - m : -x);
+    const double s = a.softmax ? e / z : 1.0 / (1.0 + e);
+    return a.bias != nullptr ? s + static_cast<double>(a.bias[i]) : s;
   }
   __device__ __forceinline__ Rank rank(const Args& a, float l, int i) const {
     return a.bias == nullptr ? rank_of(Sum{static_cast<double>(l), 0.0}, 0.0f) : rank_of(score(a, l, i), l);
@@ -296,7 +327,8 @@ struct Rank64 {
 // A row's choice once more, from those alone whose word is `least` or more, in the groups given: lane j gets
 // the j-th. They are few as a rule; they are listed, a lane takes each (the fp64 pipe being narrow), and more
 // than 32 are left to choose_all.
-template <int V>
+// (kPlain: no bias, no groups: by the logits alone.)
+template <int V, bool kPlain>
 __device__ __noinline__ int choose_near(const Args& a, long long row, float lo, float scale, uint32_t least, uint32_t groups,
                                         uint16_t* list) {
   const int lane = threadIdx.x & 31, first = lane * V;
@@ -304,7 +336,7 @@ __device__ __noinline__ int choose_near(const Args& a, long long row, float lo, 
   load_row<V>(a, row, first, l);
   Rank64 r;
   float m = 0.0f, rz = 1.0f;
-  if (a.softmax && scale > 0.0f) {
+  if (!kPlain && a.softmax) {
     m = l[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
@@ -319,8 +351,8 @@ __device__ __noinline__ int choose_near(const Args& a, long long row, float lo, 
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int i = first + v;
-    bool in = l[v] != -INFINITY && (a.groups == 1 || ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) != 0);
-    if (scale > 0.0f) {  // (as Chooser::row has it, but for the last bits)
+    bool in = l[v] != -INFINITY && (kPlain || a.groups == 1 || ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) != 0);
+    if (!kPlain) {  // (as Chooser::words has it, but for the last bits)
       const float s = (a.softmax ? __expf(l[v] - m) * rz : 1.0f / (1.0f + __expf(-l[v]))) + (a.bias != nullptr && i < a.experts ? a.bias[i] : 0.0f);
       in = in && (s - lo) * scale + 16.0f >= static_cast<float>(least);
     } else {
@@ -335,15 +367,21 @@ __device__ __noinline__ int choose_near(const Args& a, long long row, float lo, 
   if (n > 32) return -2;
   const int i = lane < n ? list[lane] : -1;
   __syncwarp();
-  return best64(i >= 0 ? r.rank(a, load(a, row, i), i) : Rank{}, i, a.top_k, lane);
+  const float li = i >= 0 ? load(a, row, i) : 0.0f;
+  const bool exact = kPlain || a.bias == nullptr;
+  const double c = exact ? static_cast<double>(li) : i >= 0 ? r.about(a, li, i) : 0.0;
+  const int got = best_keys(i >= 0 ? key_of(c) : 0, i, a.top_k, lane, 1, exact ? -1.0 : 0x1p-48);
+  if (kPlain || got != -2) return got;  // (-2: the whole warp's)
+  return best_ranks(i >= 0 ? r.rank(a, li, i) : Rank{}, i, a.top_k, lane);
 }
 
 // A row's choice once more, from all its experts, the groups ranked again as well. Lane l looks at experts l,
 // l + 32, ....
+template <bool kPlain>
 __device__ __noinline__ int choose_all(const Args& a, long long row) {
   const int lane = threadIdx.x & 31;
   Rank64 r;
-  if (a.softmax && (a.bias != nullptr || a.groups > 1)) {
+  if (!kPlain && a.softmax && (a.bias != nullptr || a.groups > 1)) {
     float m = -INFINITY;
     for (int i = lane; i < a.experts; i += 32) m = fmaxf(m, load(a, row, i));
     m = warp_max(m);
@@ -353,7 +391,7 @@ __device__ __noinline__ int choose_all(const Args& a, long long row) {
     if (!(m < INFINITY)) r.z = __longlong_as_double(0x7FF8000000000000ll);
   }
   uint32_t groups = kAll, gone = 0;
-  if (a.groups > 1) {
+  if (!kPlain && a.groups > 1) {
     Rank mine;
     const int per = static_cast<int>(a.per_group.d);
     for (int g = 0; g < a.groups; ++g) {
@@ -377,39 +415,56 @@ __device__ __noinline__ int choose_all(const Args& a, long long row) {
       if (two != 0) sum = sum + of_rank(first, __ffs(two) - 1);
       if (lane == g) mine = rank_of(sum, 0.0f);
     }
-    const int g = best64(mine, lane, a.top_groups, lane);
+    const int g = best_ranks(mine, lane, a.top_groups, lane);
     groups = __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
   }
-  int mine = -1;
+  // A lane keeps its two best: it looks through its experts again when both have been taken.
+  Rank best, next;
+  int mine = -1, at = -1, at_next = -1;
+  bool more = true;
   for (int j = 0; j < a.top_k; ++j) {
-    Rank best;
-    int at = -1;
-    for (int i = lane, v = 0; i < a.experts; i += 32, ++v) {
-      const float l = load(a, row, i);
-      if (((gone >> v) & 1u) != 0 || l == -INFINITY) continue;
-      if (a.groups > 1 && ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) == 0) continue;
-      const Rank k = r.rank(a, l, i);
-      if (above(k, best)) best = k, at = i;
+    if (__any_sync(kAll, at < 0 && more)) {
+      best = next = Rank{};
+      at = at_next = -1;
+      more = false;
+      for (int i = lane, v = 0; i < a.experts; i += 32, ++v) {
+        const float l = load(a, row, i);
+        if (((gone >> v) & 1u) != 0 || l == -INFINITY) continue;
+        if (!kPlain && a.groups > 1 && ((groups >> a.per_group(static_cast<uint32_t>(i))) & 1u) == 0) continue;
+        const Rank k = kPlain ? rank_of(Sum{static_cast<double>(l), 0.0}, 0.0f) : r.rank(a, l, i);
+        more = at_next >= 0;
+        if (above(k, best)) {
+          next = best, at_next = at;
+          best = k, at = i;
+        } else if (above(k, next)) {
+          next = k, at_next = i;
+        }
+      }
     }
     const unsigned who = best_lanes(best);
     if (who == 0) break;
     const bool on = ((who >> lane) & 1u) != 0;
     const int i = static_cast<int>(__reduce_min_sync(kAll, on ? static_cast<uint32_t>(at) : kAll));
     if (lane == j) mine = i;
-    if (on && at == i) gone |= 1u << (i >> 5);
+    if (on && at == i) {
+      gone |= 1u << (i >> 5);
+      best = next, at = at_next;
+      next = Rank{}, at_next = -1;
+    }
   }
   return mine;
 }
 
-// The groups that take part, from the two best experts of each (lane g: group g's; -1: there is none), in fp64.
-__device__ __noinline__ uint32_t groups64(const Args& a, long long row, int one, int two) {
+// The groups that take part, from the two best experts of each (lane g: group g's; -1: there is none), in fp64; 0:
+// it does not tell. Logistic scores; `most` is the largest bias. (Called amid a row's words: its registers are theirs.)
+__device__ __noinline__ uint32_t groups64(const Args& a, long long row, int one, int two, float most) {
   const Rank64 r;
   const int lane = threadIdx.x & 31;
-  Sum sum{0.0, 0.0};
-  if (one >= 0) sum = r.score(a, load(a, row, one), one);
-  if (two >= 0) sum = sum + r.score(a, load(a, row, two), two);
-  const int g = best64(one >= 0 ? rank_of(sum, 0.0f) : Rank{}, lane, a.top_groups, lane);
-  return __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
+  double sum = 0.0;
+  if (one >= 0) sum = r.about(a, load(a, row, one), one);
+  if (two >= 0) sum += r.about(a, load(a, row, two), two);
+  const int g = best_keys(one >= 0 ? key_of(sum) : 0, lane, a.top_groups, lane, a.top_groups, 0x1p-47 * (1.0 + static_cast<double>(most)));
+  return g == -2 ? 0u : __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
 }
 
 // ---------------------------------------------------------------------- by words
@@ -542,7 +597,8 @@ struct Chooser {
         const int from = min(lane * a.lanes_per_group, 31);
         const uint32_t x = __shfl_sync(kAll, one, from), y = __shfl_sync(kAll, two, from);
         auto expert = [&](uint32_t word) { return lane < a.groups && word != 0 ? static_cast<int>(kIndexMask - (word & kIndexMask)) : -1; };
-        mask = groups64(a, row, expert(x), expert(y));
+        mask = groups64(a, row, expert(x), expert(y), fmaxf(fabsf(lo), fabsf(hi)));
+        r.all = r.all || mask == 0;
       }
     }
     r.groups = mask;
@@ -714,9 +770,9 @@ __global__ void __launch_bounds__(kThreads, V >= 16 ? 2 : V >= 8 ? 3 : 4) forwar
       const bool all = __shfl_sync(kAll, r.all ? 1 : 0, from) != 0;
       int got = -2;
       if (!all)
-        got = choose_near<V>(a, row0 + from / W, chooser.lo, __shfl_sync(kAll, r.scale, from), static_cast<uint32_t>(max(least, 1)),
+        got = choose_near<V, kPlain>(a, row0 + from / W, chooser.lo, __shfl_sync(kAll, r.scale, from), static_cast<uint32_t>(max(least, 1)),
                              __shfl_sync(kAll, r.groups, from), list[threadIdx.x >> 5]);
-      if (got == -2) got = choose_all(a, row0 + from / W);  // (-2 in every lane)
+      if (got == -2) got = choose_all<kPlain>(a, row0 + from / W);  // (-2 in every lane)
       const int here = __shfl_sync(kAll, got, j);
       if (lane - j == from) mine = j < a.top_k ? here : -1;
       todo &= ~((W == 32 ? kAll : (1u << W) - 1u) << from);
