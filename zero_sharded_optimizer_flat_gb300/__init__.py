@@ -648,6 +648,14 @@ def _on_device(*tensors) -> None:
             raise ValueError("tensors must be on the GPU")
 
 
+def _workspace(ws):
+    """(address, bytes) of a workspace: what its elements name has to be memory of its own."""
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    _on_device(ws)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 I64, I32, U8 = 64, 65, 66  # not zopt_dtypes: no matrix may have them
 
 
@@ -750,16 +758,14 @@ def ffn_forward(x, w_gate_up, w_down, y, ws, *, kept=None, act: str = "silu", st
     """``zopt_ffn_forward``: y = (a(x Wgate) * (x Wup)) Wdown. ``kept`` takes gate and up for the
     backward: a bf16 matrix [tokens, 2 hidden], an :class:`Act8` of that shape in two parts, or None."""
     j = _ffn_job(x, w_gate_up, w_down, act, kept, y)
-    _on_device(ws)
-    _check(lib().zopt_ffn_forward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(lib().zopt_ffn_forward(j, *_workspace(ws), _stream(stream)))
 
 
 def ffn_backward(dy, x, kept, w_gate_up, w_down, dx, dw_gate_up, dw_down, ws, *, act: str = "silu",
                  stream=None) -> None:
     """``zopt_ffn_backward`` from dy, x (bf16 or :class:`Act8`) and what the forward kept."""
     j = _ffn_job(x, w_gate_up, w_down, act, kept, None, dy, dx, dw_gate_up, dw_down)
-    _on_device(ws)
-    _check(lib().zopt_ffn_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(lib().zopt_ffn_backward(j, *_workspace(ws), _stream(stream)))
 
 
 def _vector(t, n: int, code: int, name: str):
@@ -802,16 +808,14 @@ def linear_ce_forward(x, w, target, loss, lse, ws, *, ignore_index: int = -100, 
     """``zopt_linear_ce_forward``: each row's loss and log-sum-exp (fp32) of the logits x w' against
     target (int64), without storing the logits."""
     j = _linear_ce_job(x, w, ignore_index, target, loss, lse)
-    _on_device(ws)
-    _check(lib().zopt_linear_ce_forward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(lib().zopt_linear_ce_forward(j, *_workspace(ws), _stream(stream)))
 
 
 def linear_ce_backward(x, w, target, lse, dloss, dx, dw, ws, *, ignore_index: int = -100, stream=None) -> None:
     """``zopt_linear_ce_backward``: dx and dw (either may be None) from the forward's lse and the
     gradient dloss (fp32) of each row's loss."""
     j = _linear_ce_job(x, w, ignore_index, target, None, lse, dloss, dx, dw)
-    _on_device(ws)
-    _check(lib().zopt_linear_ce_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(lib().zopt_linear_ce_backward(j, *_workspace(ws), _stream(stream)))
 
 
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
@@ -967,7 +971,7 @@ def experts_forward(x, index, weight, w_gate_up, w_down, y, ws, *, kept=None, ac
     None."""
     j = _experts_job(x, index, weight, w_gate_up, w_down, act, kept, y)
     _one_device(ws)
-    _check(lib().zopt_experts_forward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(lib().zopt_experts_forward(j, *_workspace(ws), _stream(stream)))
 
 
 def experts_backward(dy, x, index, weight, kept, w_gate_up, w_down, dx, dweight, dw_gate_up, dw_down, ws, *,
@@ -976,7 +980,7 @@ def experts_backward(dy, x, index, weight, kept, w_gate_up, w_down, dx, dweight,
     is what :func:`route_backward` takes."""
     j = _experts_job(x, index, weight, w_gate_up, w_down, act, kept, None, dy, dx, dweight, dw_gate_up, dw_down)
     _one_device(ws)
-    _check(lib().zopt_experts_backward(j, ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(lib().zopt_experts_backward(j, *_workspace(ws), _stream(stream)))
 
 
 def take_device_error() -> int:
