@@ -324,6 +324,9 @@ struct Rank64 {
   }
 };
 
+// What the sum of two of `about` may be off, of 1 and of itself; `most` is the largest bias.
+__device__ __forceinline__ double group_off(float most) { return 0x1p-47 * (1.0 + static_cast<double>(most)); }
+
 // A row's choice once more, from those alone whose word is `least` or more, in the groups given: lane j gets
 // the j-th. They are few as a rule; they are listed, a lane takes each (the fp64 pipe being narrow), and more
 // than 32 are left to choose_all.
@@ -392,31 +395,52 @@ __device__ __noinline__ int choose_all(const Args& a, long long row) {
   }
   uint32_t groups = kAll, gone = 0;
   if (!kPlain && a.groups > 1) {
-    Rank mine;
     const int per = static_cast<int>(a.per_group.d);
+    uint64_t sum_key = 0;
+    float most = 0.0f;  // the largest bias
+    for (int i = lane; a.bias != nullptr && i < a.experts; i += 32) most = fmaxf(most, fabsf(a.bias[i]));
+    most = warp_max(most);
     for (int g = 0; g < a.groups; ++g) {
-      Rank first, second;
+      uint64_t first = 0, second = 0;
       for (int i = g * per + lane; i < (g + 1) * per; i += 32) {
         const float l = load(a, row, i);
         if (l == -INFINITY) continue;
-        const Rank k = rank_of(r.score(a, l, i), l);
-        if (above(k, first)) {
-          second = first, first = k;
-        } else if (above(k, second)) {
-          second = k;
-        }
+        const uint64_t k = key_of(r.about(a, l, i));
+        second = k > first ? first : k > second ? k : second;
+        first = k > first ? k : first;
       }
-      const unsigned one = best_lanes(first);
-      if (one == 0) continue;  // (the whole warp's)
-      const int owner = __ffs(one) - 1;
-      Sum sum = of_rank(first, owner);
-      if (lane == owner) first = second;
-      const unsigned two = best_lanes(first);
-      if (two != 0) sum = sum + of_rank(first, __ffs(two) - 1);
-      if (lane == g) mine = rank_of(sum, 0.0f);
+      const uint64_t one = warp_max(first);
+      const int owner = __ffs(__ballot_sync(kAll, first == one)) - 1;
+      const uint64_t two = warp_max(lane == owner ? second : first);
+      if (lane == g) sum_key = one == 0 ? 0 : two == 0 ? one : key_of(of_key(one) + of_key(two));
     }
-    const int g = best_ranks(mine, lane, a.top_groups, lane);
-    groups = __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
+    int best_group = best_keys(sum_key, lane, a.top_groups, lane, a.top_groups, group_off(most));
+    if (best_group == -2) {  // (in every lane: the same by two-part sums)
+      Rank mine;
+      for (int g = 0; g < a.groups; ++g) {
+        Rank first, second;
+        for (int i = g * per + lane; i < (g + 1) * per; i += 32) {
+          const float l = load(a, row, i);
+          if (l == -INFINITY) continue;
+          const Rank k = rank_of(r.score(a, l, i), l);
+          if (above(k, first)) {
+            second = first, first = k;
+          } else if (above(k, second)) {
+            second = k;
+          }
+        }
+        const unsigned one = best_lanes(first);
+        if (one == 0) continue;  // (the whole warp's)
+        const int owner = __ffs(one) - 1;
+        Sum sum = of_rank(first, owner);
+        if (lane == owner) first = second;
+        const unsigned two = best_lanes(first);
+        if (two != 0) sum = sum + of_rank(first, __ffs(two) - 1);
+        if (lane == g) mine = rank_of(sum, 0.0f);
+      }
+      best_group = best_ranks(mine, lane, a.top_groups, lane);
+    }
+    groups = __reduce_or_sync(kAll, best_group >= 0 ? 1u << best_group : 0u);
   }
   // A lane keeps its two best: it looks through its experts again when both have been taken.
   Rank best, next;
@@ -463,7 +487,7 @@ __device__ __noinline__ uint32_t groups64(const Args& a, long long row, int one,
   double sum = 0.0;
   if (one >= 0) sum = r.about(a, load(a, row, one), one);
   if (two >= 0) sum += r.about(a, load(a, row, two), two);
-  const int g = best_keys(one >= 0 ? key_of(sum) : 0, lane, a.top_groups, lane, a.top_groups, 0x1p-47 * (1.0 + static_cast<double>(most)));
+  const int g = best_keys(one >= 0 ? key_of(sum) : 0, lane, a.top_groups, lane, a.top_groups, group_off(most));
   return g == -2 ? 0u : __reduce_or_sync(kAll, g >= 0 ? 1u << g : 0u);
 }
 
