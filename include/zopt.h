@@ -648,7 +648,9 @@ ZOPT_API zopt_status zopt_linear_ce_backward(const zopt_linear_ce_job* job, void
  * The order is that of the exact numbers (without a bias, or where two biases are equal: of the logits), the
  * lowest index (of experts, of runs) first among equal ones. Its limits: a score (of a logistic one above 1/2
  * what it lacks of 1) is known to 2^-50 of itself, a sum to 106 bits, and in a run's score nothing is below
- * e^-700 of the row's largest. An expert with a logit of -inf is never chosen; a slot
+ * e^-700 of the row's largest. To leave an expert out give it a logit of -inf: a bias far below the others
+ * takes it out as well, but sends rows to a ranking in fp64, the more the wider the biases spread, from some
+ * 1e4 or 1e5 on all of them, some 30 times as long. An expert with a logit of -inf is never chosen; a slot
  * that no expert is left for has index -1 and weight 0, and so has every slot of a row whose live
  * byte is 0, whatever its logits hold. A NaN ranks above every number and makes its weight NaN (its
  * row's, for softmax or where renormalised), and so does +inf for softmax, so that found_inf sees it.
@@ -716,10 +718,10 @@ ZOPT_API zopt_status zopt_route_backward(const zopt_route_job* job, zopt_stream 
  * every slot, row t top_k + j. Experts' matrices lie stride_* elements apart (any distance that keeps
  * them apart). What the TMA cannot read in place (weights whose ld is not a multiple of 8 elements or
  * whose stride is none of ld, the forward's up columns where F is not a multiple of 8, kept rows or ups
- * that do not start on 16 bytes) is copied into the workspace first, of weights those of experts with a slot. A forward of a few slots (at most
- * 64, fewer where the weights are large) runs on the CUDA cores instead, which read the weights in place
- * and keep h and the parts in fp32: a token's y may differ there from its y in a larger batch by their
- * roundings. Outputs must not overlap inputs or each other. Repeated on the same inputs a call gives the
+ * that do not start on 16 bytes) is copied into the workspace first, of weights those of experts with a
+ * slot (the workspace has room for all). A forward of a few slots (at most 64, fewer where the weights are
+ * large) runs on the CUDA cores instead, which read the weights in place and keep h and the parts in fp32:
+ * a token's y may differ there from its y in a larger batch by their roundings. Outputs must not overlap inputs or each other. Repeated on the same inputs a call gives the
  * same bits.
  * ====================================================================================== */
 typedef struct zopt_experts_job {
@@ -753,9 +755,9 @@ typedef struct zopt_experts_job {
 } zopt_experts_job; /* 256 bytes */
 
 /* Workspace bytes for a forward (backward = 0) or backward call, or either (backward = 1 covers
- * both), of a job: from its tokens, dim, hidden, experts, top_k and the ld_* and stride_* of the
- * weights and of kept (0: any; a known one may need less); no pointer is looked at. 0 for a shape that
- * the calls refuse. */
+ * both), of a job: from its tokens, dim, hidden, experts, top_k, the ld_* and stride_* of the weights, and
+ * ld_kept (0: any; a known one may need less); no pointer is looked at. 0 for a shape that the calls
+ * refuse. */
 ZOPT_API size_t zopt_experts_workspace(const zopt_experts_job* job, int32_t backward);
 /* Errors of both: EINVAL for NULL or misaligned pointers (matrices 16 bytes, vectors their element,
  * scale bytes any), tokens < 0, dim, hidden, experts or top_k < 1, experts above 1024, top_k above 32,

@@ -13,7 +13,8 @@
 // Measured (GB300, 8192 tokens' 6 slots among 64 experts, 2048 x 1408): forward with bf16 kept 725 us = 1.17
 // PFLOP/s: the products 350 and 180 by themselves (tensor pipe 87 and 79 % of elapsed at the clock that the power
 // cap leaves; what is lost beside it are the experts' last row tiles), the rows in and out 36 and 42, the plan
-// 13. Backward, 8 bits kept, 1450 us: dh and its epilogue 275, the three products behind it 860, rows in 75, out 45.
+// 14. Backward, 8 bits kept, 1385 to 1466 us: by themselves dh and its epilogue take 240, the three products behind
+// it 950, rows in 78, out 44.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -3,7 +3,8 @@
 //
 // A cluster of two CTAs computes a 256 x 256 tile with tcgen05.mma.cta_group::2: each CTA holds its
 // 128 rows of P and its 128 columns of Q, so a 64-deep k-block brings 32 KiB per SM and the ring
-// holds six stages (with five, units of eight k-blocks take 8 % longer, with four 25 %). A thread of
+// holds six stages (with five, units of eight k-blocks take 8 % longer, with four 25 %), the gated block's backward
+// five, whose epilogue needs the room more than its loads do. A thread of
 // each CTA for each operand streams it by TMA (all complete on the leader's stage barrier), one
 // thread of the leader issues the M=256, N=256, K=16 MMAs into one of two TMEM accumulators, and
 // eight epilogue warps (two per quarter of the TMEM lanes, each 128 of the 256 columns) turn the
@@ -17,7 +18,7 @@
 // Bound by the tensor cores where the inner length is long enough to hide a tile's epilogue (12 to 30
 // k-blocks' time): 521 cycles a k-block of 512, tensor pipe 92 % of elapsed in the cross entropy's
 // forward (4096 x 768 x 50304), 89 % in the block's first product and 90 % in its backward's second
-// launch (8192 x 2048 x 5632), all three at the clock that the power cap leaves; 61 % in the
+// launch (8192 x 2048 x 5632), all three at the clock that the power cap leaves; 61 % (137 us) in the
 // backward's first launch, whose epilogue (three results and two kept inputs an entry) outlasts its
 // 32 k-blocks; 76 % in y, 256 tiles over 76 pairs.
 #pragma once

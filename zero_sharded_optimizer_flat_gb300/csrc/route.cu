@@ -8,16 +8,21 @@
 // words up. Without a bias the 22 bits are the logit's own leading ones (a bf16 logit's are all of
 // it), with one, or with groups, the score's and the bias's sum in fixed point over the row's range.
 // Neighbours in the order that come closer than those bits and the score's error tell apart have the
-// warp rank their row again in fp64 (one row in some hundreds where there is a bias).
+// warp rank their row again in fp64, and where fp64 is too coarse by sums of two parts. How many rows that are
+// depends on the numbers (8192 rows of 256 experts): two in a thousand for logits of deviation 1 and biases of
+// 0.02, 20 us; nearly all where scores crowd at 0 and 1 and the biases are equal (deviation 8, zeros), 80 us;
+// biases that spread far (100: 23 us, 1e3: 35, 1e6 or the lowest value: 550) leave no word a meaning, every row is
+// ranked from all its experts. Without a bias 15 us whatever the logits.
 //
 // The choices of the rows lie side by side in the warp's lanes, so that weights, checks and stores are
 // done once for all of them, and two rows take turns, since a choice waits for the one before it.
 //
-// Bound by a row's instructions (310 for eight of 128 experts, 18 of them a choice; 530 with a bias for eight of
-// 256), which the chains of choices let a scheduler issue in half of its cycles: 32768 x 128 in bf16 20.5 us, 0.4
-// TB/s; 8192 x 256 in eight groups with a bias 22 us, 16384 x 256 with a bias 24 (and 10 for the backward, which
-// writes 17 MB in it). Tried: a row to eight or sixteen lanes, with 16 words each (a fifth fewer instructions,
-// half the warps: 25 and 50 us), scores in fp64 for whole rows (38 us: a close row took as long as the rest).
+// Bound by latency: a row's instructions (310 for eight of 128 experts, 18 of them a choice; 530 with a bias for
+// eight of 256) hang on chains of choices, two rows' at a time, and fill 40 to 49 % of the issue slots while an SM
+// has warps, 23 to 38 % of the whole time: 32768 x 128 in bf16 20.5 us, 0.4 TB/s; 8192 x 256 in eight groups with a
+// bias 22 us, 16384 x 256 with a bias 25 (and 10 for the backward, which writes 17 MB in it). Tried: a row to eight
+// or sixteen lanes, with 16 words each (a fifth fewer instructions, half the warps: 25 and 50 us), scores in fp64
+// for whole rows (38 us: a close row took as long as the rest).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
