@@ -647,8 +647,8 @@ ZOPT_API zopt_status zopt_linear_ce_backward(const zopt_linear_ce_job* job, void
  *   weight = s of those (without the bias), over their sum where renormalise, times scale.
  * The order is that of the exact numbers (without a bias, or where two biases are equal: of the logits), the
  * lowest index (of experts, of runs) first among equal ones. Its limits: a score (of a logistic one above 1/2
- * what it lacks of 1) is known to 2^-50 of itself, a sum to 106 bits, and in a run's score nothing is below
- * e^-700 of the row's largest. To leave an expert out give it a logit of -inf: a bias far below the others
+ * what it lacks of 1) is known to 2^-50 of itself, a sum to 106 bits, and in a run's score no score is below
+ * e^-700 (softmax: of the row's largest). To leave an expert out give it a logit of -inf: a bias far below the others
  * takes it out as well, but sends rows to a ranking in fp64, the more the wider the biases spread, from some
  * 1e4 or 1e5 on all of them, some 30 times as long. An expert with a logit of -inf is never chosen; a slot
  * that no expert is left for has index -1 and weight 0, and so has every slot of a row whose live
